@@ -281,6 +281,147 @@ fa_status fa_blocksparse_backward(const void* q, const void* k, const void* v, c
                                   const uint8_t* block_mask, int mask_heads, void* workspace,
                                   size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Per-head RMS norm of queries and keys with the position rotation, in one
+ * pass over each: what stands between the Q, K projections and attention.
+ * For every row x (d elements) of q with weights wq, and of k with wk:
+ *     y = x * w / sqrt(mean(x^2) + eps)
+ *     (a, b) -> (a c - b s, b c + a s) for the pairs of y's first `rot`
+ *     elements; c, s = row `position` of cos, sin
+ * pairs: (i, i + rot/2) with interleaved = 0, (2i, 2i + 1) otherwise, i the
+ * column of the tables.  Elements from `rot` on are only normed.  Sums and
+ * products are fp32 with one rounding to bf16 at the end.
+ *   q, k          bf16 [B, H, N, d] and [B, Hkv, N, d], any strides (below)
+ *   wq, wk        fp32 [d]
+ *   cos, sin      fp32 [table_rows, rot/2]
+ *   positions     int32 [B, N], or null for 0 .. N-1 in every sequence;
+ *                 clamped to [0, table_rows - 1]
+ *   q_out, k_out  bf16 [B, H, N, d], [B, Hkv, N, d], contiguous
+ *   strides       null (q and k contiguous), or a host array of 6 element
+ *                 strides: batch, head, row of q, then of k.  Multiples of 8
+ *                 (FA_ERR_MISALIGNED otherwise), not negative; strides of
+ *                 axes of length 1 are ignored.  So q and k may be views of
+ *                 one packed [B, N, H + 2 Hkv, d] projection.
+ * rot: a multiple of 16 in [16, d] (else FA_ERR_UNSUPPORTED); eps finite and
+ * > 0; wq, wk, cos, sin 16-byte aligned.  Outputs must not overlap inputs.
+ * Hkv need not divide H.
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, const float* wq, const float* wk,
+                          const float* cos, const float* sin, const int* positions, void* q_out,
+                          void* k_out, int B, int H, int Hkv, int N, int d, int rot,
+                          int table_rows, int interleaved, float eps, const long long* strides,
+                          cudaStream_t stream);
+
+/* Bytes of workspace fa_qk_norm_rope_backward needs (1024 partial sums of
+ * dwq and dwk: 8192 * d bytes, whatever the batch). */
+size_t fa_qk_norm_rope_workspace_size(int d);
+
+/*
+ * Backward of fa_qk_norm_rope: the norm is formed again from q and k.
+ *   in : dq_out, dk_out  bf16, gradients of q_out, k_out, contiguous (what
+ *        fa_backward writes); the forward's other inputs
+ *   out: dq, dk          bf16, strided by grad_strides (as `strides`; rows
+ *        must not overlap, else FA_ERR_INVALID_ARG)
+ *        dwq, dwk        fp32 [d], sums over every row, written whole; in a
+ *        fixed order (the same bits from call to call on one device)
+ *   workspace / workspace_bytes: as fa_backward.  Enqueues two kernels.
+ */
+fa_status fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,
+                                   const void* k, const float* wq, const float* wk,
+                                   const float* cos, const float* sin, const int* positions,
+                                   void* dq, void* dk, float* dwq, float* dwk, int B, int H,
+                                   int Hkv, int N, int d, int rot, int table_rows,
+                                   int interleaved, float eps, const long long* strides,
+                                   const long long* grad_strides, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Paged key/value cache.
+ *   k_cache, v_cache  [num_pages, Hkv, page_size, d] in the format's type
+ *   k_scale, v_scale  uint8 [num_pages, Hkv, page_size]; ignored (may be
+ *                     null) for FA_CACHE_BF16
+ *   page_table        int32 [B, max_pages]: position p of sequence b is row
+ *                     p mod page_size of page page_table[b][p / page_size]
+ * page_size 16, 32, 64 or 128; max_pages * page_size and num_pages * Hkv
+ * below 2^31; caches and scales 16-byte aligned.  Sequences may share pages
+ * that they only read.
+ *
+ * Formats: FA_CACHE_BF16 keeps rows as they are.  FA_CACHE_E4M3 and
+ * FA_CACHE_INT8 keep 8-bit numbers and one scale byte s per row (token,
+ * head, key or value), the value being number * 2^(s - 127): the smallest
+ * power of two that keeps the row within +-448 (+-127), at least 2^-117,
+ * then round to nearest, ties to even.  (The power is at most 2^119, 2^121,
+ * where the largest number is still finite in bf16; larger values saturate.)  What reads back is exact in bf16,
+ * and storing it again gives the same values, so tokens can be moved by
+ * reading and appending them.  A row that holds a NaN or an infinity is
+ * stored with s = 255 and reads back as NaN in all its elements.  The e4m3
+ * code of NaN (0x7f, 0xff) is never written and does not read as NaN.
+ */
+typedef enum fa_cache_format {
+  FA_CACHE_BF16 = 0,
+  FA_CACHE_E4M3 = 1,
+  FA_CACHE_INT8 = 2
+} fa_cache_format;
+
+/*
+ * Writes N new tokens of each sequence: token n of sequence b at position
+ * start[b] + n, for n < counts[b].
+ *   k, v     bf16 [B, Hkv, N, d], strides as in fa_qk_norm_rope (6: k, v)
+ *   start    int32 [B];  counts  int32 [B], or null for N in every sequence
+ * Positions below 0 or from max_pages * page_size on, and page ids outside
+ * [0, num_pages), are skipped.  Nothing else of the cache is touched.  Two
+ * tokens for the same row of a page: one of them is kept, element by
+ * element undefined which.
+ */
+fa_status fa_cache_append(const void* k, const void* v, const int* page_table, const int* start,
+                          const int* counts, void* k_cache, void* v_cache, uint8_t* k_scale,
+                          uint8_t* v_scale, int format, int B, int Hkv, int N, int d,
+                          int num_pages, int page_size, int max_pages, const long long* strides,
+                          cudaStream_t stream);
+
+/*
+ * Reads positions start[b] .. start[b] + counts[b] - 1 of each sequence back
+ * as bf16: k, v [B, Hkv, N, d], contiguous.  Rows from counts[b] on are left
+ * as they were; positions that fa_cache_append would skip read as zeros.
+ */
+fa_status fa_cache_read(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                        const uint8_t* v_scale, const int* page_table, const int* start,
+                        const int* counts, void* k, void* v, int format, int B, int Hkv, int N,
+                        int d, int num_pages, int page_size, int max_pages, cudaStream_t stream);
+
+/* Bytes of workspace fa_tree_attention needs, whatever the lengths of the
+ * histories. */
+size_t fa_tree_attention_workspace_size(int B, int H, int Hkv, int T, int d);
+
+/*
+ * Attention of drafted tokens over the cache (speculative decoding: a tree
+ * of drafts is verified at once; T = 1 is a plain decode step, no mask a
+ * chain of tokens).  Sequence b has hist_lens[b] accepted tokens at
+ * positions 0 .. hist_lens[b] - 1 and draft_lens[b] <= T drafts at the
+ * positions behind them, all appended to the cache before.  Draft i sees
+ * every accepted token and draft j when bit (j mod 32) of
+ * tree_mask[b][i][j / 32] is set (itself included or not, as the mask says;
+ * bits from draft_lens[b] on are ignored); without a mask, j <= i.
+ *   q          bf16 [B, H, T, d];  head h reads key/value head h / (H / Hkv)
+ *   hist_lens  int32 [B];  draft_lens  int32 [B], or null for T everywhere
+ *   tree_mask  32-bit words [B, T, ceil(T / 32)], or null
+ *   o          bf16 [B, H, T, d];  lse  fp32 [B, H, T], natural log
+ * A draft that sees nothing, and rows from draft_lens[b] on, get O = 0 and
+ * lse = -inf.  Keys and values that no draft of a row sees (other branches,
+ * rows of a page past the last draft, pages of other sequences) have no
+ * influence on it, whatever they hold.  Lengths are clamped to [0, T] and
+ * the table's capacity, page ids to the pool: bad ones give unspecified
+ * values but no access outside the cache.  T <= 1024; B*H*T*d < 2^31.
+ * The result for an 8-bit cache is that for a bf16 cache of the values that
+ * fa_cache_read returns.
+ */
+fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const uint8_t* k_scale, const uint8_t* v_scale, const int* page_table,
+                            const int* hist_lens, const int* draft_lens, const uint32_t* tree_mask,
+                            void* o, float* lse, int format, int B, int H, int Hkv, int T, int d,
+                            int num_pages, int page_size, int max_pages, float scale,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the status word of the
  * current device.  FA_OK, FA_ERR_TIMEOUT (a device wait gave up; outputs of
  * the calls since the last check are undefined) or FA_ERR_CUDA. */

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/fa.h"
+#include "fa_host.h"
 #include "fa_internal.h"
 
 namespace fa {
@@ -16,11 +17,25 @@ int* status_word_address();  // fa_aux.cu
 
 namespace {
 
+using fa::align256;
+using fa::check_ptr16;
+using fa::check_ptr4;
+using fa::check_ws;
 using fa::kTile;
+using fa::status_word;
+using fa::wait_limit_ns;
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{0};
 
+// status word address per device, looked up once per device
+constexpr int kMaxDevices = 64;
+std::atomic<int*> g_status[kMaxDevices];
+std::mutex g_status_mu;
+
+}  // namespace
+
+namespace fa {
 unsigned long long wait_limit_ns() {
   unsigned long long v = g_wait_ns.load();
   if (v == 0) {
@@ -33,11 +48,6 @@ unsigned long long wait_limit_ns() {
   }
   return v;
 }
-
-// status word address per device, looked up once per device
-constexpr int kMaxDevices = 64;
-std::atomic<int*> g_status[kMaxDevices];
-std::mutex g_status_mu;
 
 int* status_word(fa_status* st) {
   int dev = 0;
@@ -59,6 +69,9 @@ int* status_word(fa_status* st) {
   }
   return p;
 }
+}  // namespace fa
+
+namespace {
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -79,10 +92,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 fa_status check_shape(int B, int H, int N, int d, float scale) {
   if (B < 1 || H < 1 || N < 1) return FA_ERR_INVALID_ARG;
   if (!(isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
@@ -91,29 +100,6 @@ fa_status check_shape(int B, int H, int N, int d, float scale) {
   if (total >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
-
-fa_status check_ptr16(const void* p) {
-  if (!p) return FA_ERR_INVALID_ARG;
-  if (!aligned(p, 16)) return FA_ERR_MISALIGNED;
-  return FA_OK;
-}
-
-fa_status check_ptr4(const void* p) {
-  if (!p) return FA_ERR_INVALID_ARG;
-  if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
-  return FA_OK;
-}
-
-#define FA_TRY(x)                    \
-  do {                               \
-    const fa_status _s = (x);        \
-    if (_s != FA_OK) return _s;      \
-  } while (0)
-
-#define FA_CUDA(x)                                \
-  do {                                            \
-    if ((x) != cudaSuccess) return FA_ERR_CUDA;   \
-  } while (0)
 
 int num_tiles(int N) { return (N + kTile - 1) / kTile; }
 
@@ -360,13 +346,6 @@ bool sweep_config_ok(int d, int rows_per_cta, int key_tile, int kv_stages) {
     if (key_tile == 256) return kv_stages == 2 || kv_stages == 4;
   }
   return false;
-}
-
-fa_status check_ws(void* ws, size_t have, size_t need) {
-  if (!ws) return FA_ERR_INVALID_ARG;
-  if (!aligned(ws, 256)) return FA_ERR_MISALIGNED;
-  if (have < need) return FA_ERR_WORKSPACE;
-  return FA_OK;
 }
 
 // Encoded tensor maps are a pure function of (base, element type, BH, N,

@@ -344,6 +344,12 @@ FA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// elementwise difference of two packed bf16x2 words, rounded once to bf16
+FA_DEV uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // the two halves of a packed bf16x2 word as fp32 (exact)
 FA_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 FA_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
