@@ -6,11 +6,40 @@
 // ancestors and itself in a tree; all drafts up to itself without a mask):
 //   o_i = sum_j p_ij v_j,  p_i = softmax over the seen j of scale q_i k_j.
 //
-// One warp per (sequence, head, draft): the query row lives in registers
-// (D / 32 elements per lane), keys are taken one by one with a running max
-// and sum.
+// The G = H / Hkv query heads of a key/value head and the T drafts make
+// R = G T query rows that read the same keys, so the work is a matrix
+// product of R rows per (sequence, key/value head).  It is bound by reading
+// the cache: 4 d flops per row and key against 4 d bytes per key (bf16), so
+// up to about 290 rows the tensor cores can follow the memory.
+//
+// Work split.  A problem is (sequence, key/value head, group of rows), a unit
+// one 128-key tile of a problem.  The units of all problems form one line,
+// cut into equal runs, one per CTA (one CTA per SM): every SM reads the same
+// number of bytes whatever the lengths are.  A run may end inside a problem;
+// such a part leaves its unnormalised O and its (m, l) per row in the
+// workspace, and a second kernel joins the parts.  The lengths live on the
+// device, so the kernel finds its run itself (a sum over the sequences).
+//
+// CTA (warp 0 loads, warp 1 issues the MMAs, warps 2-5 and 6-9 do softmax):
+//   up to 128 rows ("split"): the tiles of the run alternate between the two
+//     softmax warpgroups, each with its own S and O in tensor memory, so that
+//     one tile's softmax overlaps the other's MMAs; the two are added at the
+//     end of each problem.
+//   more rows ("pair"): each warpgroup has 128 of 256 rows, every tile
+//     serves both.
+// bf16 caches: TMA brings each page's rows into the 128-byte-swizzled tile
+// the MMA reads.  8-bit caches: bulk copies bring the stored bytes, and 8 more
+// warps widen them to the same bf16 tile (exact, see fa_quant.cuh), so the
+// products are those of the values that fa_cache_read returns.
+//
+// Keys that nobody may see are never left to chance: scores are replaced by
+// -inf, values of rows past the last token are zeroed in shared memory, and
+// so are NaN and infinite values of drafts, which the rows that do see them
+// get back at the end (0 x NaN would reach every row otherwise).
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "../../include/fa.h"
 #include "fa_host.h"
@@ -20,108 +49,1028 @@
 namespace fa {
 namespace {
 
-struct TreeParams {
-  const void* q;                 // bf16 [B, H, T, d]
-  const void *kc, *vc;           // caches [num_pages, Hkv, page, d]
-  const uint8_t *ks, *vs;        // scale bytes [num_pages, Hkv, page]
-  const int *page_table, *hist, *drafts;
-  const uint32_t* mask;          // [B, T, words] or null
-  void* o;                       // bf16 [B, H, T, d]
-  float* lse;                    // [B, H, T]
-  int B, H, Hkv, T, num_pages, log_page, max_pages, words;
-  float scale;
-};
+static_assert(kCacheBf16 == static_cast<int>(FA_CACHE_BF16) &&
+                  kCacheE4m3 == static_cast<int>(FA_CACHE_E4M3) &&
+                  kCacheInt8 == static_cast<int>(FA_CACHE_INT8),
+              "the public formats are the kernels'");
 
+constexpr int kMaxGrid = 192;     // CTAs, at most (the workspace holds two parts of each)
+constexpr int kConvWarps = 8;     // warps that widen 8-bit tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the max grew by more than 2^8
 
-// D / 32 elements of a cache row as fp32
+struct TreeParams {
+  const void *kc, *vc;     // caches [num_pages, Hkv, page, d]
+  const uint8_t *ks, *vs;  // scale bytes [num_pages, Hkv, page]
+  const int *page_table, *hist, *drafts;
+  const uint32_t* mask;    // [B, T, words] or null
+  void* o;                 // bf16 [B, H, T, d]
+  float* lse;              // [B, H, T]
+  float2* part_ml;         // [2 * grid][slot_rows] (max in log2 units, sum)
+  float* part_o;           // [2 * grid][slot_rows][d]
+  int B, Hkv, T, rows;     // rows = H / Hkv * T
+  int groups, slot_rows;   // row groups per key/value head; rows of a part
+  int pair;                // 256-row groups
+  int num_pages, log_page, max_pages, words;
+  float scale;
+  int* err;
+  uint64_t wait_ns;
+};
+
+// Lengths of a sequence, clamped to what the page table can hold.
+struct SeqLen {
+  int hist, nd, tiles;
+  FA_DEV int len() const { return hist + nd; }
+};
+FA_DEV SeqLen seq_len(const TreeParams& p, int b) {
+  SeqLen s;
+  const int cap = p.max_pages << p.log_page;
+  s.hist = min(max(p.hist[b], 0), cap);
+  s.nd = min(p.drafts ? min(max(p.drafts[b], 0), p.T) : p.T, cap - s.hist);
+  // one unit even without a key: somebody has to write the rows
+  s.tiles = max(1, (s.len() + kTile - 1) / kTile);
+  return s;
+}
+
+FA_DEV long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// (all sequences' units, units in front of sequence `before`); whole warp.
+FA_DEV void unit_sums(const TreeParams& p, int before, int lane, long long& total,
+                      long long& front) {
+  long long t = 0, f = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const long long u = static_cast<long long>(seq_len(p, b).tiles) * p.Hkv * p.groups;
+    t += u;
+    if (b < before) f += u;
+  }
+  total = warp_sum(t);
+  front = warp_sum(f);
+}
+
+// A CTA's run of units.
+struct Run {
+  int b, hr, t;      // first unit: sequence, key/value head x group, tile
+  int pad;
+  long long left;    // units
+};
+
+// Run of CTA c of n: units [U c / n, U (c + 1) / n), n at most U so that no
+// run between two others is empty.  Whole warp.
+FA_DEV Run find_run(const TreeParams& p, int c, int n, int lane) {
+  long long total, dummy;
+  unit_sums(p, 0, lane, total, dummy);
+  if (n > total) n = static_cast<int>(total);
+  if (c >= n) return Run{0, 0, 0, 0, 0};
+  const long long u0 = total * c / n, u1 = total * (c + 1) / n;
+  Run r = {0, 0, 0, 0, u1 - u0};
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int tiles = b < p.B ? seq_len(p, b).tiles : 0;
+    const long long u = static_cast<long long>(tiles) * p.Hkv * p.groups;
+    long long incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > u0);
+    if (hit) {
+      const int w = __ffs(hit) - 1;
+      const long long rem = __shfl_sync(0xffffffffu, u0 - (base + incl - u), w);
+      const int tw = __shfl_sync(0xffffffffu, tiles, w);
+      r.b = b0 + w;
+      r.hr = static_cast<int>(rem / tw);
+      r.t = static_cast<int>(rem - static_cast<long long>(r.hr) * tw);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
+// The parts of problems in a run, in order; every role of the CTA walks it.
+struct PartIter {
+  SeqLen s;
+  int b, hr, t0, t1;  // tiles [t0, t1) of problem (b, hr)
+  int next_t;
+  long long left;
+  FA_DEV void init(const TreeParams& p, const Run& r) {
+    b = r.b;
+    hr = r.hr;
+    next_t = r.t;
+    left = r.left;
+    s = seq_len(p, b);
+  }
+  FA_DEV bool next(const TreeParams& p) {
+    if (left == 0) return false;
+    if (next_t == s.tiles) {
+      next_t = 0;
+      if (++hr == p.Hkv * p.groups) {
+        hr = 0;
+        ++b;
+        s = seq_len(p, b);
+      }
+    }
+    t0 = next_t;
+    const int n = left < s.tiles - t0 ? static_cast<int>(left) : s.tiles - t0;
+    t1 = next_t = t0 + n;
+    left -= n;
+    return true;
+  }
+};
+
+// The tiles of a run, in order.
+struct TileIter {
+  PartIter it;
+  int t = 0, part = -1;
+  bool first = false, last = false;
+  FA_DEV bool next(const TreeParams& p) {
+    first = part < 0 || t + 1 >= it.t1;
+    if (first) {
+      if (!it.next(p)) return false;
+      ++part;
+      t = it.t0;
+    } else {
+      ++t;
+    }
+    last = t + 1 == it.t1;
+    return true;
+  }
+};
+
+// One K or V tile to load: `first` of a part brings that part's Q.
+struct Load {
+  int b, hr, kb, part;
+  SeqLen s;
+  bool isv, first;
+};
+
+// The order in which the MMAs consume K and V tiles, which is the order of
+// the rings.  pair: K0 V0 K1 V1 ...; split, where a tile's scores are formed
+// before the previous tile's weights are used: K0 K1 V0 K2 V1 ... V(n-1).
+struct LoadIter {
+  TileIter ti;
+  Load cur, prev;
+  bool owe = false, any = false, done = false;
+  FA_DEV bool advance(const TreeParams& p) {
+    if (!ti.next(p)) return false;
+    cur.b = ti.it.b;
+    cur.hr = ti.it.hr;
+    cur.kb = ti.t * kTile;
+    cur.part = ti.part;
+    cur.s = ti.it.s;
+    cur.first = ti.first;
+    cur.isv = false;
+    return true;
+  }
+  FA_DEV bool next(const TreeParams& p, Load& x) {
+    if (owe) {
+      owe = false;
+      x = prev;
+      x.isv = true;
+      x.first = false;
+      prev = cur;
+      return true;
+    }
+    if (done) return false;
+    if (p.pair && any) {
+      x = cur;
+      x.isv = true;
+      x.first = false;
+      any = false;
+      return true;
+    }
+    if (advance(p)) {
+      x = cur;
+      if (p.pair) {
+        any = true;
+      } else if (any) {
+        owe = true;
+      } else {
+        prev = cur;
+        any = true;
+      }
+      return true;
+    }
+    done = true;
+    if (!p.pair && any) {
+      x = prev;
+      x.isv = true;
+      x.first = false;
+      return true;
+    }
+    return false;
+  }
+};
+
 template <int D, int FMT>
-FA_DEV void cache_elements(const void* cache, const uint8_t* scales, long long row, int lane,
-                           float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  if (FMT == kCacheBf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(cache) + row * D + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+struct TreeSmem {
+  static constexpr bool Q8 = FMT != kCacheBf16;
+  static constexpr int CH = D / 64;             // 128-byte column chunks per row
+  static constexpr int CHUNK = kTile * 128;     // [128 rows x 128 B] = 16 KB
+  static constexpr int TILE = CH * CHUNK;       // one 128 x D bf16 tile
+  static constexpr int RAW = kTile * D;         // one 128 x D tile of stored bytes
+  static constexpr int NS = Q8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);  // bf16 K/V tiles
+  static constexpr int NR = Q8 ? (D == 64 ? 8 : 4) : 0;                  // stored tiles
+  static constexpr int Q = 0;  // split: two parts' Q; pair: two row tiles
+  static constexpr int KV = 2 * TILE;
+  static constexpr int RW = KV + NS * TILE;
+  static constexpr int SC = RW + NR * RAW;      // scale bytes of the stored tiles
+  static constexpr int ML = SC + NR * kTile;    // (m, l) of the second warpgroup's rows
+  static constexpr int BAR = ML + kTile * 8;
+  static constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + NS, B_RF = B_KVE + NS,
+                       B_RE = B_RF + NR, B_SF = B_RE + NR, B_PF = B_SF + 2, B_OF = B_PF + 2,
+                       B_X1 = B_OF + 1, B_X2 = B_X1 + 1, B_DONE = B_X2 + 1, NBAR = B_DONE + 1;
+  static constexpr int RUN = BAR + NBAR * 8;    // Run
+  static constexpr int MISC = RUN + 24;
+  static constexpr int ALLOC = MISC + 40 + 1024;  // + slack for 1024-byte alignment
+  static constexpr int THREADS = 320 + (Q8 ? 32 * kConvWarps : 0);
+  // tensor memory columns: S0, S1 (128 each), O0, O1 (D each)
+  static constexpr int T_O = 2 * kTile;
+  // P (bf16) takes the upper half of its S: the scores of keys 64..127 are
+  // in registers when their weights are stored, those of keys 0..63 are
+  // read again
+  static constexpr int T_P = 64;
+  static_assert(ALLOC <= 232448, "shared memory budget");
+};
+
+// bits 0 .. n-1
+FA_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Which of the 32 keys from position `pos` on draft t of a sequence sees.
+FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const SeqLen& s, int t,
+                          int pos) {
+  const int d0 = pos - s.hist;  // draft index of bit 0
+  uint32_t w;
+  if (!mask_row) {
+    w = low_bits(t + 1 - d0);
+  } else if (d0 >= 0) {
+    const int i = d0 >> 5;
+    w = __funnelshift_r(i < p.words ? mask_row[i] : 0u, i + 1 < p.words ? mask_row[i + 1] : 0u,
+                        d0 & 31);
   } else {
-    const uint8_t* p = static_cast<const uint8_t*>(cache) + row * D + lane * E;
-    uint32_t w = 0, lo, hi;
-#pragma unroll
-    for (int i = 0; i < E; ++i) w |= static_cast<uint32_t>(p[i]) << (8 * i);
-    widen4<FMT>(w, widen_scale<FMT>(scales[row]), lo, hi);
-    x[0] = bf16_lo(lo);
-    x[1] = bf16_hi(lo);
-    if (E == 4) {
-      x[E - 2] = bf16_lo(hi);
-      x[E - 1] = bf16_hi(hi);
+    w = d0 > -32 ? mask_row[0] << -d0 : 0u;
+  }
+  return (w & low_bits(s.nd - d0)) | low_bits(-d0);
+}
+
+// untiled bulk copy (16-byte aligned, a multiple of 16 bytes)
+FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+FA_DEV uint32_t ld_shared_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+FA_DEV uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// a NaN or an infinity in a packed bf16 pair
+FA_DEV bool not_finite2(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+// the pair with NaN and infinities replaced by zero
+FA_DEV uint32_t finite2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Adds the NaN and infinite values among the drafts of positions [lo, hi)
+// that draft t sees to its written row of O (they were zeroed in the tiles):
+// `o` (bf16) or `part` (fp32).  Rare.
+template <int D, int FMT>
+__device__ __noinline__ void add_not_finite(const TreeParams& p, int b, int hkv, SeqLen s, int t,
+                                            int lo, int hi, uint16_t* o, float* part) {
+  const uint32_t* mr = p.mask ? p.mask + (static_cast<size_t>(b) * p.T + t) * p.words : nullptr;
+  for (int pos = lo; pos < hi; ++pos) {
+    if (!(seen_bits(p, mr, s, t, pos) & 1u)) continue;
+    int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (pos >> p.log_page)];
+    page = min(max(page, 0), p.num_pages - 1);
+    const long long row = ((static_cast<long long>(page) * p.Hkv + hkv) << p.log_page) +
+                          (pos & ((1 << p.log_page) - 1));
+    if (FMT != kCacheBf16 && p.vs[row] != kScaleNan) continue;
+    for (int j = 0; j < D; ++j) {
+      const float v = FMT != kCacheBf16
+                          ? __uint_as_float(0x7FFFFFFFu)
+                          : __uint_as_float(static_cast<uint32_t>(
+                                                static_cast<const uint16_t*>(p.vc)[row * D + j])
+                                            << 16);
+      if (isfinite(v)) continue;
+      if (part)
+        part[j] += v;
+      else
+        o[j] = static_cast<uint16_t>(
+            pack_bf16(__uint_as_float(static_cast<uint32_t>(o[j]) << 16) + v, 0.f) & 0xFFFFu);
     }
   }
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(128) fa_tree_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
+    fa_tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const TreeParams p) {
+  using L = TreeSmem<D, FMT>;
+  grid_dep_wait();  // the previous kernel's writes are visible from here on
+  grid_dep_launch();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) { return sb + L::BAR + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
+  // part p has NaN or infinite draft values if entry p % 8 says p (whoever
+  // finds them is less than 8 parts ahead of the end of a part)
+  volatile int* bad_parts = reinterpret_cast<volatile int*>(smem + L::MISC + 8);
+  Run* run_slot = reinterpret_cast<Run*>(smem + L::RUN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == 0) {
+    const Run r = find_run(p, blockIdx.x, gridDim.x, lane);
+    if (lane == 0) {
+      *run_slot = r;
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(L::B_QF + i), 1);
+        mbar_init(bar(L::B_QE + i), 1);
+        mbar_init(bar(L::B_SF + i), 1);
+        mbar_init(bar(L::B_PF + i), 4);
+      }
+      for (int i = 0; i < L::NS; ++i) {
+        mbar_init(bar(L::B_KVF + i), L::Q8 ? kConvWarps : 1);
+        mbar_init(bar(L::B_KVE + i), 1);
+      }
+      for (int i = 0; i < L::NR; ++i) {
+        mbar_init(bar(L::B_RF + i), 1);
+        mbar_init(bar(L::B_RE + i), kConvWarps);
+      }
+      mbar_init(bar(L::B_OF), 1);
+      mbar_init(bar(L::B_X1), 4);
+      mbar_init(bar(L::B_X2), 4);
+      mbar_init(bar(L::B_DONE), 1);
+      *abort_flag = 0;
+      for (int i = 0; i < 8; ++i) bad_parts[i] = -1;
+      fence_mbar_init();
+      prefetch_tmap(&tq);
+      if (!L::Q8) {
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+      }
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Run run = *run_slot;
+  const WaitCtl wc{abort_flag, p.err, p.wait_ns};
+  auto uwait = [&](uint32_t b, uint32_t ph) {
+    return __all_sync(0xffffffffu, wait_bar(b, ph, wc));
+  };
+  const bool pair = p.pair != 0;
+  TileIter tiles0;
+  if (run.left > 0) tiles0.it.init(p, run);
+  else tiles0.it.left = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ loads
+    LoadIter li;
+    li.ti = tiles0;
+    Load x;
+    uint32_t idx = 0;
+    int parts = 0;
+    bool ok = true;
+    const int page = 1 << p.log_page;
+    while (ok && li.next(p, x)) {
+      const int hkv = x.hr / p.groups;
+      if (x.first) {
+        const int qb = pair ? 0 : x.part & 1, use = pair ? x.part : x.part >> 1;
+        if (use > 0) ok = uwait(bar(L::B_QE + qb), (use - 1) & 1);
+        if (!ok) break;
+        ++parts;
+        if (lane == 0) {
+          const int r0 = (x.hr - hkv * p.groups) * 2 * kTile;
+          const bool two = pair && r0 + kTile < p.rows;
+          mbar_arrive_expect_tx(bar(L::B_QF + qb), (two ? 2 : 1) * L::TILE);
+          for (int i = 0; i < (two ? 2 : 1); ++i)
+#pragma unroll
+            for (int c = 0; c < L::CH; ++c)
+              tma_load_3d(sb + L::Q + (qb + i) * L::TILE + c * L::CHUNK, &tq, bar(L::B_QF + qb),
+                          64 * c, r0 + i * kTile, x.b * p.Hkv + hkv);
+        }
+      }
+      // pages of this tile that hold a token, one per lane
+      const int nval = min(max(x.s.len() - x.kb, 0), kTile);
+      const int np = (nval + page - 1) >> p.log_page;
+      int id = 0;
+      if (lane < np)
+        id = p.page_table[static_cast<size_t>(x.b) * p.max_pages + (x.kb >> p.log_page) + lane];
+      id = min(max(id, 0), p.num_pages - 1);
+      if (!L::Q8) {
+        const int slot = idx % L::NS;
+        const uint32_t round = idx / L::NS;
+        if (round > 0) ok = uwait(bar(L::B_KVE + slot), (round - 1) & 1);
+        if (!ok) break;
+        const uint32_t full = bar(L::B_KVF + slot);
+        if (lane == 0) mbar_arrive_expect_tx(full, np * page * D * 2);
+        __syncwarp();
+        if (lane < np)
+#pragma unroll
+          for (int c = 0; c < L::CH; ++c)
+            tma_load_3d(sb + L::KV + slot * L::TILE + c * L::CHUNK + lane * page * 128,
+                        x.isv ? &tv : &tk, full, 64 * c, 0, id * p.Hkv + hkv);
+      } else {
+        const int slot = idx % (L::Q8 ? L::NR : 1);
+        const uint32_t round = idx / (L::Q8 ? L::NR : 1);
+        if (round > 0) ok = uwait(bar(L::B_RE + slot), (round - 1) & 1);
+        if (!ok) break;
+        const uint32_t full = bar(L::B_RF + slot);
+        if (lane == 0) mbar_arrive_expect_tx(full, np * page * (D + 1));
+        __syncwarp();
+        if (lane < np) {
+          const size_t row = (static_cast<size_t>(id) * p.Hkv + hkv) << p.log_page;
+          bulk_load(sb + L::RW + slot * L::RAW + lane * page * D,
+                    static_cast<const uint8_t*>(x.isv ? p.vc : p.kc) + row * D, page * D, full);
+          bulk_load(sb + L::SC + slot * kTile + lane * page, (x.isv ? p.vs : p.ks) + row, page,
+                    full);
+        }
+      }
+      ++idx;
+    }
+    // let copies still in flight land before the CTA can exit
+    for (int i = max(0, parts - (pair ? 1 : 2)); i < parts; ++i)
+      drain_bar(bar(L::B_QF + (pair ? 0 : i & 1)), (pair ? i : i >> 1) & 1, p.wait_ns);
+    constexpr uint32_t n = L::Q8 ? L::NR : L::NS;
+    for (uint32_t j = idx > n ? idx - n : 0; j < idx; ++j)
+      drain_bar(bar((L::Q8 ? L::B_RF : L::B_KVF) + j % n), (j / n) & 1, p.wait_ns);
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer
+    auto ecommit = [&](uint32_t b) {
+      if (elect_one()) mma_commit(b);
+    };
+    constexpr uint32_t idS = idesc_bf16(128, kTile, false, false);
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint64_t dq0 = desc_sw128(sb + L::Q, 16, 1024);
+    const uint64_t dk0 = desc_sw128(sb + L::KV, 16, 1024);
+    const uint64_t dv0 = desc_sw128(sb + L::KV, L::CHUNK, 1024);
+    auto issue_s = [&](int s, int qtile, int slot) {
+      const uint64_t qa = desc_advance(dq0, qtile * L::TILE);
+      const uint64_t kb = desc_advance(dk0, slot * L::TILE);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = (kk >> 2) * L::CHUNK + (kk & 3) * 32;
+        const uint64_t da = desc_advance(qa, at), db = desc_advance(kb, at);
+        if (elect_one()) mma_bf16_ss(tmem + s * kTile, da, db, idS, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int s, int slot, bool acc) {
+      const uint64_t vb = desc_advance(dv0, slot * L::TILE);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk) {
+        const uint64_t db = desc_advance(vb, kk * 2048);
+        if (elect_one())
+          mma_bf16_ts(tmem + L::T_O + s * D, tmem + s * kTile + L::T_P + kk * 8, db, idO,
+                      (acc || kk > 0) ? 1u : 0u);
+      }
+    };
+    TileIter ti = tiles0;
+    uint32_t idx = 0;  // tiles taken from the ring
+    auto wait_kv = [&]() {
+      return uwait(bar(L::B_KVF + idx % L::NS), (idx / L::NS) & 1);
+    };
+    auto wait_q = [&](int part) {
+      return pair ? uwait(bar(L::B_QF), part & 1) : uwait(bar(L::B_QF + (part & 1)), (part >> 1) & 1);
+    };
+    // which warpgroups a pair tile serves
+    auto members = [&](const TileIter& x) {
+      return (x.it.hr % p.groups) * 2 * kTile + kTile < p.rows ? 3 : 1;
+    };
+    bool ok = true;
+    bool have = ti.next(p);
+    uint32_t g = 0, cnt0 = 0, cnt1 = 0;  // tiles; PVs of each warpgroup
+    bool acc0 = false, acc1 = false;
+    int mem = pair && have ? members(ti) : 1;
+    int part = ti.part;
+    bool last = ti.last;
+    if (have) {
+      ok = wait_q(part) && wait_kv();
+      if (ok) {
+        tc_fence_after();
+        const int slot = idx % L::NS;
+        issue_s(0, pair ? 0 : part & 1, slot);
+        ecommit(bar(L::B_SF));
+        if (pair && (mem & 2)) {
+          issue_s(1, 1, slot);
+          ecommit(bar(L::B_SF + 1));
+        }
+        ecommit(bar(L::B_KVE + slot));
+        if (last) ecommit(bar(L::B_QE + (pair ? 0 : part & 1)));
+        ++idx;
+      }
+    }
+    while (ok && have) {
+      const bool have_n = ti.next(p);
+      const int mem_n = have_n && pair ? members(ti) : 1;
+      if (!pair) {
+        const int s = g & 1;
+        if (have_n) {  // the next tile's scores go to the other warpgroup
+          if (ti.first) ok = wait_q(ti.part);
+          if (ok) ok = wait_kv();
+          if (!ok) break;
+          tc_fence_after();
+          const int slot = idx % L::NS;
+          issue_s(s ^ 1, ti.part & 1, slot);
+          ecommit(bar(L::B_SF + (s ^ 1)));
+          ecommit(bar(L::B_KVE + slot));
+          if (ti.last) ecommit(bar(L::B_QE + (ti.part & 1)));
+          ++idx;
+        }
+        ok = wait_kv() && uwait(bar(L::B_PF + s), (g >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int slot = idx % L::NS;
+        issue_pv(s, slot, s ? acc1 : acc0);
+        (s ? acc1 : acc0) = true;
+        ecommit(bar(L::B_KVE + slot));
+        ++idx;
+      } else {
+        ok = wait_kv();
+        if (!ok) break;
+        const int vslot = idx % L::NS;
+        ++idx;
+        bool ready = false;  // the next tile's K (and Q)
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (mem & (1 << s)) {
+            uint32_t& cnt = s ? cnt1 : cnt0;
+            ok = uwait(bar(L::B_PF + s), cnt & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(s, vslot, s ? acc1 : acc0);
+            (s ? acc1 : acc0) = true;
+            ++cnt;
+          }
+          if (have_n && (mem_n & (1 << s))) {
+            if (!ready) {
+              if (ti.first) ok = wait_q(ti.part);
+              if (ok) ok = wait_kv();
+              if (!ok) break;
+              tc_fence_after();
+              ready = true;
+            }
+            issue_s(s, s, idx % L::NS);
+            ecommit(bar(L::B_SF + s));
+          }
+        }
+        if (!ok) break;
+        ecommit(bar(L::B_KVE + vslot));
+        if (ready) {
+          ecommit(bar(L::B_KVE + idx % L::NS));
+          if (ti.last) ecommit(bar(L::B_QE));
+          ++idx;
+        }
+      }
+      if (last) {
+        ecommit(bar(L::B_OF));
+        acc0 = acc1 = false;
+      }
+      ++g;
+      have = have_n;
+      mem = mem_n;
+      part = ti.part;
+      last = ti.last;
+    }
+    // every MMA issued above completes before the CTA gives its memory back
+    ecommit(bar(L::B_DONE));
+    drain_bar(bar(L::B_DONE), 0, p.wait_ns);
+  } else if (warp < 10) {
+    // ------------------------------------------------------ softmax
+    const int s = (warp - 2) >> 2;
+    const int q4 = warp & 3;  // tensor memory lanes this warp may access
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t tS = tmem + lane_off + s * kTile;
+    const uint32_t tO = tmem + lane_off + L::T_O + s * D;
+    const uint32_t tP = tS + L::T_P;
+    const float sl2 = p.scale * kLog2e;
+    float2* ml = reinterpret_cast<float2*>(smem + L::ML);
+    PartIter it = tiles0.it;
+    uint32_t g = 0, cnt = 0;
+    const uint32_t total = static_cast<uint32_t>(run.left);
+    int part = -1;
+    bool ok = true, owe_x2 = false;
+    while (ok && it.next(p)) {
+      ++part;
+      const int hkv = it.hr / p.groups;
+      const int row0 = pair ? (it.hr - hkv * p.groups) * 2 * kTile + s * kTile : 0;
+      const bool mine_all = row0 < p.rows;             // pair: this warpgroup has rows
+      const bool busy = row0 + q4 * 32 < p.rows;       // this warp has rows
+      const int row = row0 + r, t = row % p.T;
+      const bool valid = row < p.rows && t < it.s.nd;
+      const uint32_t* mask_row =
+          p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words : nullptr;
+      float m = -INFINITY, l = 0.f;
+      int mine = 0;               // tiles of this part done by this warpgroup
+      for (int tile = it.t0; tile < it.t1 && ok; ++tile, ++g) {
+        if (pair ? !mine_all : static_cast<int>(g & 1) != s) continue;
+        const int kb = tile * kTile;
+        const bool tail = kb + kTile > it.s.hist;  // drafts or the end in this tile
+        ok = uwait(bar(L::B_SF + s), cnt & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (busy) {
+          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          if (tail) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              vis[w] = valid ? seen_bits(p, mask_row, it.s, t, kb + 32 * w) : 0u;
+          }
+          uint32_t sr[2][32];
+          auto load_scores = [&](int half) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + 32 * c, sr[c]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) reg_fence(sr[c]);
+            if (tail) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((vis[2 * half + c] >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
+            }
+          };
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            load_scores(half);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              mx0 = fmax3(mx0, __uint_as_float(sr[0][j]), __uint_as_float(sr[0][j + 1]));
+              mx1 = fmax3(mx1, __uint_as_float(sr[1][j]), __uint_as_float(sr[1][j + 1]));
+            }
+          }
+          const float m_new = fmaxf(m, fmaxf(mx0, mx1) * sl2);
+          const bool resc = m_new > m + kRescaleLog2;
+          const float alpha = resc ? ex2(m - m_new) : 1.f;
+          if (resc) {
+            l *= alpha;
+            m = m_new;
+          }
+          const bool rescale_o = mine > 0 && __any_sync(0xffffffffu, resc);
+          const float mu = (m == -INFINITY) ? 0.f : m;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), nmux2 = f2_pack(-mu, -mu);
+          uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int half = 1 - k;  // keys 64..127 are in registers
+            if (k == 1) load_scores(0);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1])),
+                                 sl2x2, nmux2),
+                          a, b);
+                a = ex2(a);
+                b = ex2(b);
+                // the sum takes the fp32 weights; P is rounded to bf16 for
+                // the MMA (half a step, 2^-8, of each weight)
+                uint64_t& lx = (j & 2) ? lb : la;
+                lx = f2_add(lx, f2_pack(a, b));
+                sr[c][j / 2] = pack_bf16(a, b);
+              }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              tmem_st16(tP + 32 * half + 16 * c,
+                        *reinterpret_cast<const uint32_t(*)[16]>(&sr[c][0]));
+          }
+          {
+            float a, b;
+            f2_unpack(f2_add(la, lb), a, b);
+            l += a + b;
+          }
+          if (rescale_o) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * c, o);
+              tmem_ld_wait();
+              reg_fence(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32(tO + 32 * c, o);
+            }
+          }
+          tmem_st_wait();
+        }
+        if (!L::Q8 && tail && !(pair && s == 1)) {
+          // One V row per thread: zero past the last token, zero NaN and
+          // infinities of drafts.  (Not before this tile's scores: only they
+          // show that the ring slot's last tile has come and gone.)
+          const uint32_t vi = pair ? 2 * g + 1 : g + 1 == total ? 2 * g + 1 : 2 * g + 2;
+          ok = uwait(bar(L::B_KVF + vi % L::NS), (vi / L::NS) & 1);
+          if (!ok) break;
+          const uint32_t v0 = sb + L::KV + (vi % L::NS) * L::TILE;
+          const int pos = kb + r;
+          if (pos >= it.s.hist) {
+            const bool past = pos >= it.s.len();
+#pragma unroll 1
+            for (int c = 0; c < L::CH * 8; ++c) {
+              const uint32_t a = v0 + (c >> 3) * L::CHUNK + sw128_offset(r, c & 7);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (!past) {
+                v = ld_shared_v4(a);
+                if (!(not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) ||
+                      not_finite2(v.w)))
+                  continue;
+                bad_parts[part & 7] = part;
+                v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+              }
+              st_shared_v4(a, v.x, v.y, v.z, v.w);
+            }
+          }
+          fence_async_smem();
+        }
+        if (owe_x2) {  // O of the last part has been read
+          ok = uwait(bar(L::B_X2), (part - 1) & 1);
+          if (!ok) break;
+          owe_x2 = false;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_PF + s));
+        ++cnt;
+        ++mine;
+      }
+      if (!ok) break;
+      // ---------------------------------------------------- end of a part
+      if (!pair && s == 1) {
+        if (owe_x2) ok = uwait(bar(L::B_X2), (part - 1) & 1);
+        if (!ok) break;
+        ml[r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_X1));
+        owe_x2 = true;
+        continue;
+      }
+      ok = uwait(bar(L::B_OF), part & 1);
+      if (ok && !pair) ok = uwait(bar(L::B_X1), part & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (busy) {
+        int other = 0;  // the other warpgroup's tiles of this part
+        float a0 = 1.f, a1 = 0.f;
+        if (!pair) {
+          other = it.t1 - it.t0 - mine;
+          const float2 x = ml[r];
+          const float mm = fmaxf(m, x.x), mu = mm == -INFINITY ? 0.f : mm;
+          a0 = ex2(m - mu);
+          a1 = ex2(x.x - mu);
+          l = l * a0 + x.y * a1;
+          m = mm;
+        }
+        const bool whole = it.t0 == 0 && it.t1 == it.s.tiles;
+        const bool has = valid && !(l == 0.f);  // a NaN sum stays one
+        const float inv = has ? 1.f / l : 0.f;
+        const size_t orow = (static_cast<size_t>(it.b) * p.Hkv + hkv) * p.rows + row;
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (it.t0 == 0 ? 1 : 0);
+        const size_t prow = slot * p.slot_rows + (pair ? s * kTile : 0) + r;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.f;
+          if (mine > 0) {
+            tmem_ld32(tO + 32 * c, x);
+            tmem_ld_wait();
+            reg_fence(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(x[j]) * a0;
+          }
+          if (other > 0) {
+            tmem_ld32(tO + D + 32 * c, x);
+            tmem_ld_wait();
+            reg_fence(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(x[j]), a1, o[j]);
+          }
+          if (row < p.rows) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * D + 32 * c);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const float* y = &o[8 * v];
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (has)
+                  w = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                                 pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
+                dst[v] = w;
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            }
+          }
+        }
+        if (row < p.rows) {
+          if (whole)
+            p.lse[orow] = has ? (m + lg2(l)) * kLn2 : -INFINITY;
+          else
+            p.part_ml[prow] = make_float2(valid ? m : -INFINITY, valid ? l : 0.f);
+        }
+        if (valid && bad_parts[part & 7] == part)
+          add_not_finite<D, FMT>(p, it.b, hkv, it.s, t, max(it.s.hist, it.t0 * kTile),
+                                 min(it.s.len(), it.t1 * kTile),
+                                 whole ? static_cast<uint16_t*>(p.o) + orow * D : nullptr,
+                                 whole ? nullptr : p.part_o + prow * D);
+      }
+      if (!pair) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_X2));
+      }
+    }
+  } else if (L::Q8) {
+    // ------------------------------------------------------ widening
+    // 16 stored bytes per lane and step: two 8-byte loads, two 16-byte
+    // stores.  Which half comes first alternates (`sel`) so that the lanes
+    // of an access fall on different banks.
+    constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per row, rows per step
+    constexpr int ROWS = kTile / kConvWarps;     // rows of a tile per warp
+    const int cw = warp - 10, u = lane % LPR, rl = lane / LPR;
+    LoadIter li;
+    li.ti = tiles0;
+    Load x;
+    uint32_t idx = 0;
+    bool ok = true;
+    constexpr uint32_t NR = L::Q8 ? L::NR : 1;
+    while (ok && li.next(p, x)) {
+      const uint32_t rs = idx % NR, ds = idx % L::NS, dr = idx / L::NS;
+      ok = uwait(bar(L::B_RF + rs), (idx / NR) & 1);
+      if (ok && dr > 0) ok = uwait(bar(L::B_KVE + ds), (dr - 1) & 1);
+      if (!ok) break;
+      const uint32_t raw = sb + L::RW + rs * L::RAW, sc = sb + L::SC + rs * kTile;
+      const uint32_t dst = sb + L::KV + ds * L::TILE;
+      const int nval = x.s.len() - x.kb, ndraft = x.s.hist - x.kb;
+#pragma unroll 2
+      for (int i = 0; i < ROWS / RPI; ++i) {
+        const int row = cw * ROWS + i * RPI + rl;
+        const int sel = D == 128 ? ((u >> 2) ^ row) & 1 : (row >> 1) & 1;
+        const uint32_t a = raw + row * D + 16 * u;
+        const uint2 w0 = ld_shared_v2(a + 8 * sel), w1 = ld_shared_v2(a + 8 * (sel ^ 1));
+        const uint32_t byte = ld_shared_u8(sc + row);
+        const RowScale scale = widen_scale<FMT>(byte);
+        uint4 y0, y1;
+        widen4<FMT>(w0.x, scale, y0.x, y0.y);
+        widen4<FMT>(w0.y, scale, y0.z, y0.w);
+        widen4<FMT>(w1.x, scale, y1.x, y1.y);
+        widen4<FMT>(w1.y, scale, y1.z, y1.w);
+        if (x.isv && row >= ndraft) {
+          const bool bad = row < nval && byte == kScaleNan;
+          if (bad) bad_parts[x.part & 7] = x.part;
+          if (bad || row >= nval) y0 = y1 = make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t out = dst + (D == 128 ? (u >> 2) * L::CHUNK : 0);
+        const int c0 = 2 * (u & 3);
+        const uint32_t o0 = out + sw128_offset(row, c0 + sel);
+        const uint32_t o1 = out + sw128_offset(row, c0 + (sel ^ 1));
+        st_shared_v4(o0, y0.x, y0.y, y0.z, y0.w);
+        st_shared_v4(o1, y1.x, y1.y, y1.z, y1.w);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::B_KVF + ds));
+        mbar_arrive(bar(L::B_RE + rs));
+      }
+      ++idx;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of problems that more than one CTA worked on: one warp per
+// row.  O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts i.
+template <int D>
+__global__ void __launch_bounds__(256) fa_tree_join_kernel(const TreeParams p, int n) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (r >= static_cast<long long>(p.B) * p.H * p.T) return;
-  const int t = static_cast<int>(r % p.T), h = static_cast<int>(r / p.T % p.H),
-            b = static_cast<int>(r / p.T / p.H), hkv = h / (p.H / p.Hkv);
-  const int cap = p.max_pages << p.log_page;
-  const int hist = min(max(p.hist[b], 0), cap);
-  const int nd = min(p.drafts ? min(max(p.drafts[b], 0), p.T) : p.T, cap - hist);
-  float q[E], o[E], x[E], m = -INFINITY, l = 0.f;
+  const long long gr = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (gr >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
+  const int bh = static_cast<int>(gr / p.rows), row = static_cast<int>(gr - static_cast<long long>(bh) * p.rows);
+  const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
+  const int grp = p.pair ? row / (2 * kTile) : 0, pr = row - grp * 2 * kTile * p.pair;
+  long long total, front;
+  unit_sums(p, b, lane, total, front);
+  if (n > total) n = static_cast<int>(total);
+  const int tiles = seq_len(p, b).tiles;
+  // CTA c has units [total c / n, total (c + 1) / n): unit u is in CTA
+  // ((u + 1) n - 1) / total
+  const long long u0 = front + static_cast<long long>(hkv * p.groups + grp) * tiles;
+  const int c0 = static_cast<int>(((u0 + 1) * n - 1) / total);
+  const int c1 = static_cast<int>(((u0 + tiles) * n - 1) / total);
+  if (c0 == c1) return;  // written by its CTA
+  // the first part starts the problem (slot 1 of its CTA), the others go on
+  auto at = [&](int c) {
+    return (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * p.slot_rows + pr;
+  };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[at(c)].x);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = __uint_as_float(
-        static_cast<uint32_t>(static_cast<const uint16_t*>(p.q)[r * D + lane * E + i]) << 16);
-    o[i] = 0.f;
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float mu = M == -INFINITY ? 0.f : M;
+  float l = 0.f, o[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = p.part_ml[at(c)];
+    const float a = ex2(x.x - mu);
+    l = fmaf(x.y, a, l);
+    const float* y = p.part_o + at(c) * D + lane * E;
+    float v[E];
+    if (E == 4)
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y);
+    else
+      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y);
+    // a part in which the row saw nothing counts nothing, whatever it holds
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = x.y == 0.f ? o[i] : fmaf(v[i], a, o[i]);
   }
-  for (int j = 0; t < nd && j < hist + nd; ++j) {
-    if (j >= hist) {
-      const int i = j - hist;
-      const bool seen =
-          p.mask ? (p.mask[(static_cast<size_t>(b) * p.T + t) * p.words + i / 32] >> (i % 32)) & 1u
-                 : i <= t;
-      if (!seen) continue;
-    }
-    int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (j >> p.log_page)];
-    page = min(max(page, 0), p.num_pages - 1);
-    const long long row = ((static_cast<long long>(page) * p.Hkv + hkv) << p.log_page) +
-                          (j & ((1 << p.log_page) - 1));
-    cache_elements<D, FMT>(p.kc, p.ks, row, lane, x);
-    float s = 0.f;
+  const bool has = !(l == 0.f);
+  const float inv = has ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + gr * D + lane * E);
 #pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], x[i], s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= p.scale * kLog2e;
-    const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
-    const float a = ex2(m - mu), e = ex2(s - mu);
-    cache_elements<D, FMT>(p.vc, p.vs, row, lane, x);
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = fmaf(e, x[i], o[i] * a);
-    m = mn;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is 0
-  uint16_t* out = static_cast<uint16_t*>(p.o) + r * D + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; i += 2)
-    *reinterpret_cast<uint32_t*>(out + i) = pack_bf16(o[i] * inv, o[i + 1] * inv);
-  if (lane == 0) p.lse[r] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+  for (int i = 0; i < E; i += 2) dst[i / 2] = has ? pack_bf16(o[i] * inv, o[i + 1] * inv) : 0u;
+  if (lane == 0) p.lse[gr] = has ? (M + lg2(l)) * kLn2 : -INFINITY;
+}
+
+// Rows of a part: one group of up to 128 (split) or 256 (pair) rows.
+int slot_rows(int rows) {
+  const int most = rows > kTile ? 2 * kTile : kTile;
+  return rows < most ? rows : most;
+}
+
+size_t tree_ml_bytes(int rows) {
+  return align256(2ull * kMaxGrid * slot_rows(rows) * sizeof(float2));
+}
+size_t tree_ws_bytes(int H, int Hkv, int T, int d) {
+  const int rows = H / Hkv * T;
+  return tree_ml_bytes(rows) + align256(2ull * kMaxGrid * slot_rows(rows) * d * sizeof(float));
 }
 
 template <int D, int FMT>
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.B) * p.H * p.T;
-  return launch_pdl(fa_tree_kernel<D, FMT>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128),
-                    0, stream, p);
+cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, cudaStream_t stream) {
+  using L = TreeSmem<D, FMT>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = smem_attr_once(
+      attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT>), L::ALLOC);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long most_tiles = ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
+  const long long most = static_cast<long long>(p.B) * p.Hkv * p.groups * most_tiles;
+  int grid = sms < kMaxGrid ? sms : kMaxGrid;
+  if (most < grid) grid = static_cast<int>(most);
+  e = launch_pdl(fa_tree_kernel<D, FMT>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream, tq, tk, tv,
+                 p);
+  // tables of one tile: every problem is one unit, nothing to join
+  if (e != cudaSuccess || most_tiles == 1) return e;
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.rows;
+  return launch_pdl(fa_tree_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256),
+                    0, stream, p, grid);
 }
-
-size_t tree_ws_bytes(int B, int H, int Hkv, int T, int d) { return 256; }
 
 }  // namespace
 }  // namespace fa
@@ -129,8 +1078,8 @@ size_t tree_ws_bytes(int B, int H, int Hkv, int T, int d) { return 256; }
 extern "C" {
 
 size_t fa_tree_attention_workspace_size(int B, int H, int Hkv, int T, int d) {
-  if (B < 1 || H < 1 || Hkv < 1 || T < 1 || d < 1) return 0;
-  return fa::tree_ws_bytes(B, H, Hkv, T, d);
+  if (B < 1 || H < 1 || Hkv < 1 || T < 1 || d < 1 || Hkv > H || H % Hkv != 0) return 0;
+  return fa::tree_ws_bytes(H, Hkv, T, d);
 }
 
 fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_cache,
@@ -152,9 +1101,11 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   FA_TRY(check_ptr4(hist_lens));
   if (draft_lens) FA_TRY(check_ptr4(draft_lens));
   if (tree_mask) FA_TRY(check_ptr4(tree_mask));
-  FA_TRY(check_ws(workspace, workspace_bytes, tree_ws_bytes(B, H, Hkv, T, d)));
+  FA_TRY(check_ws(workspace, workspace_bytes, tree_ws_bytes(H, Hkv, T, d)));
+  fa_status st = FA_OK;
+  int* err = status_word(&st);
+  if (!err) return st;
   TreeParams p = {};
-  p.q = q;
   p.kc = k_cache;
   p.vc = v_cache;
   p.ks = k_scale;
@@ -166,22 +1117,38 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.o = o;
   p.lse = lse;
   p.B = B;
-  p.H = H;
   p.Hkv = Hkv;
   p.T = T;
+  p.rows = H / Hkv * T;
+  p.pair = p.rows > kTile ? 1 : 0;
+  p.groups = p.pair ? (p.rows + 2 * kTile - 1) / (2 * kTile) : 1;
+  p.slot_rows = slot_rows(p.rows);
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + tree_ml_bytes(p.rows));
   p.num_pages = num_pages;
   p.log_page = log2_page(page_size);
   p.max_pages = max_pages;
   p.words = (T + 31) / 32;
   p.scale = scale;
+  p.err = err;
+  p.wait_ns = wait_limit_ns();
+  CUtensorMap tq, tk, tv;
+  if (!make_tile_map(&tq, q, B * Hkv, p.rows, d)) return FA_ERR_CUDA;
+  if (format == kCacheBf16) {
+    if (!make_tile_map(&tk, k_cache, num_pages * Hkv, page_size, d, page_size) ||
+        !make_tile_map(&tv, v_cache, num_pages * Hkv, page_size, d, page_size))
+      return FA_ERR_CUDA;
+  } else {
+    tk = tv = tq;  // not read: stored bytes come by untiled copies
+  }
   if (d == 64)
-    FA_CUDA(format == kCacheBf16   ? (launch_tree<64, kCacheBf16>(p, stream))
-            : format == kCacheE4m3 ? (launch_tree<64, kCacheE4m3>(p, stream))
-                                   : (launch_tree<64, kCacheInt8>(p, stream)));
+    FA_CUDA(format == kCacheBf16   ? (launch_tree<64, kCacheBf16>(p, tq, tk, tv, stream))
+            : format == kCacheE4m3 ? (launch_tree<64, kCacheE4m3>(p, tq, tk, tv, stream))
+                                   : (launch_tree<64, kCacheInt8>(p, tq, tk, tv, stream)));
   else
-    FA_CUDA(format == kCacheBf16   ? (launch_tree<128, kCacheBf16>(p, stream))
-            : format == kCacheE4m3 ? (launch_tree<128, kCacheE4m3>(p, stream))
-                                   : (launch_tree<128, kCacheInt8>(p, stream)));
+    FA_CUDA(format == kCacheBf16   ? (launch_tree<128, kCacheBf16>(p, tq, tk, tv, stream))
+            : format == kCacheE4m3 ? (launch_tree<128, kCacheE4m3>(p, tq, tk, tv, stream))
+                                   : (launch_tree<128, kCacheInt8>(p, tq, tk, tv, stream)));
   return FA_OK;
 }
 

@@ -126,6 +126,35 @@ def test_against_plain(case, fmt):
     p.check(o, lse)
 
 
+def many(B, lo, hi, seed):
+    return [int(x) for x in np.random.default_rng(seed).integers(lo, hi, B)]
+
+
+MANY = [
+    # as CASES, with several problems and several tiles for each SM: runs that
+    # begin and end inside problems, problems of one tile, all three of
+    # up to 128 rows, up to 256, and groups of 256 with a short last one
+    (40, 8, 8, 2, 64, 32, many(40, 0, 700, 1), many(40, 0, 3, 2), None),
+    (60, 4, 4, 3, 128, 16, many(60, 0, 260, 3), None, "tree"),
+    (30, 3, 1, 50, 64, 64, many(30, 0, 900, 4), many(30, 0, 51, 5), "any"),
+    (24, 3, 1, 100, 128, 128, many(24, 0, 800, 6), many(24, 1, 101, 7), "tree"),
+    (20, 5, 1, 120, 64, 16, many(20, 100, 600, 8), None, "any"),
+    # long runs
+    (4, 8, 2, 23, 128, 64, [9000, 8192, 5001, 12345], [23, 9, 22, 1], "tree"),
+    (3, 2, 1, 29, 64, 128, [30000, 16384, 777], None, "any"),
+    (2, 8, 2, 64, 128, 32, [8192, 6003], [64, 63], "tree"),
+]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("case", MANY, ids=name)
+def test_runs_over_many_problems(case, fmt):
+    p = Problem(fmt, *case, seed=sum(case[:6]) + fmt, dev=device())
+    o, lse = p.run()
+    status_ok()
+    p.check(o, lse)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_growing_scores(fmt):
     """Keys that grow along the sequence: the running max moves far, by more
