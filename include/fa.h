@@ -413,7 +413,7 @@ size_t fa_tree_attention_workspace_size(int B, int H, int Hkv, int T, int d);
  * the table's capacity, page ids to the pool: bad ones give unspecified
  * values but no access outside the cache.  T <= 1024; B*H*T*d < 2^31.
  * The result for an 8-bit cache is that for a bf16 cache of the values that
- * fa_cache_read returns.
+ * fa_cache_read returns, up to rounding.
  */
 fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_cache,
                             const uint8_t* k_scale, const uint8_t* v_scale, const int* page_table,

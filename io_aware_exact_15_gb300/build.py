@@ -17,9 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa_gb300.so")
 SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_aux.cu", "fa_api.cu", "fa_noalloc.cu",
-           "fa_norm_rope.cu", "fa_cache.cu", "fa_tree.cu"]
+           "fa_norm_rope.cu", "fa_cache.cu", "fa_tree.cu", "fa_tree_few.cu"]
 HEADERS = ["fa_ptx.cuh", "fa_sched.cuh", "fa_internal.h", "fa_philox.cuh", "fa_host.h",
-           "fa_quant.cuh"]
+           "fa_quant.cuh", "fa_tree.cuh"]
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -348,15 +348,18 @@ bool sweep_config_ok(int d, int rows_per_cta, int key_tile, int kv_stages) {
   return false;
 }
 
-// Encoded tensor maps are a pure function of (base, element type, BH, N,
-// d): a small per-thread cache returns the same 128 bytes without calling
+// Encoded tensor maps are a pure function of (base, element kind, BH, N, d,
+// box rows): a small per-thread cache returns the same 128 bytes without calling
 // the driver again when a caller repeats its buffers (every training step
 // does).  Direct-mapped, 16 entries per thread, no locking.
+// Element kinds of a map: bf16 rows, the fp32 dQ accumulator, stored bytes of
+// an 8-bit key/value cache.
+enum MapKind : int { kMapBf16 = 0, kMapF32 = 1, kMapU8 = 2 };
 struct MapKey {
   const void* base;
-  int BH, N, d, fp32, box_rows;
+  int BH, N, d, kind, box_rows;
   bool operator==(const MapKey& o) const {
-    return base == o.base && BH == o.BH && N == o.N && d == o.d && fp32 == o.fp32 &&
+    return base == o.base && BH == o.BH && N == o.N && d == o.d && kind == o.kind &&
            box_rows == o.box_rows;
   }
 };
@@ -372,7 +375,7 @@ int map_slot(const MapKey& k) {
   uint64_t h = reinterpret_cast<uintptr_t>(k.base) >> 8;
   h ^= static_cast<uint64_t>(k.BH) * 0x9E3779B97F4A7C15ull;
   h ^= static_cast<uint64_t>(k.N) * 0xC2B2AE3D27D4EB4Full;
-  h ^= static_cast<uint64_t>(k.d * 2 + k.fp32 + 1024 * k.box_rows) * 0x165667B19E3779F9ull;
+  h ^= static_cast<uint64_t>(k.d * 4 + k.kind + 2048 * k.box_rows) * 0x165667B19E3779F9ull;
   h ^= h >> 29;
   return static_cast<int>(h % kMapSlots);
 }
@@ -385,20 +388,27 @@ bool encode_map(CUtensorMap* map, const MapKey& key) {
   }
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t esz = key.fp32 ? 4 : 2;
+  const cuuint64_t esz = key.kind == kMapF32 ? 4 : key.kind == kMapU8 ? 1 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(key.d), static_cast<cuuint64_t>(key.N),
                               static_cast<cuuint64_t>(key.BH)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(key.d) * esz,
                                  static_cast<cuuint64_t>(key.N) * key.d * esz};
   // bf16: box_rows x 64-column boxes; fp32 accumulator: 32 x 32 boxes (both
-  // 128-byte rows, 128-byte swizzle)
-  const cuuint32_t box_bf16[3] = {64, static_cast<cuuint32_t>(key.box_rows), 1};
-  const cuuint32_t box_f32[3] = {32, 32, 1};
+  // 128-byte rows); bytes: box_rows x d boxes (128- or 64-byte rows).  The
+  // swizzle is the box's row size.
+  const cuuint32_t box[3] = {key.kind == kMapF32  ? 32u
+                             : key.kind == kMapU8 ? static_cast<cuuint32_t>(key.d)
+                                                  : 64u,
+                             key.kind == kMapF32 ? 32u : static_cast<cuuint32_t>(key.box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType type = key.kind == kMapF32  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : key.kind == kMapU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle swizzle = key.kind == kMapU8 && key.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                       : CU_TENSOR_MAP_SWIZZLE_128B;
   const bool ok =
-      fn(map, key.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-         const_cast<void*>(key.base), dims, strides, key.fp32 ? box_f32 : box_bf16, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      fn(map, type, 3, const_cast<void*>(key.base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   if (ok) {
     slot.key = key;
@@ -412,10 +422,13 @@ bool encode_map(CUtensorMap* map, const MapKey& key) {
 
 namespace fa {
 bool make_tile_map(CUtensorMap* map, const void* base, int BH, int N, int d, int box_rows) {
-  return encode_map(map, MapKey{base, BH, N, d, 0, box_rows});
+  return encode_map(map, MapKey{base, BH, N, d, kMapBf16, box_rows});
 }
 bool make_acc_map(CUtensorMap* map, const void* base, int BH, int N, int d) {
-  return encode_map(map, MapKey{base, BH, N, d, 1, 32});
+  return encode_map(map, MapKey{base, BH, N, d, kMapF32, 32});
+}
+bool make_cache_map(CUtensorMap* map, const void* base, int tiles, int page, int d, bool bytes) {
+  return encode_map(map, MapKey{base, tiles, page, d, bytes ? kMapU8 : kMapBf16, 16});
 }
 }  // namespace fa
 

@@ -28,7 +28,7 @@
 //   more rows ("pair"): each warpgroup has 128 of 256 rows, every tile
 //     serves both.
 // bf16 caches: TMA brings each page's rows into the 128-byte-swizzled tile
-// the MMA reads.  8-bit caches: bulk copies bring the stored bytes, and 8 more
+// the MMA reads.  8-bit caches: bulk copies bring the stored bytes, and 6 more
 // warps widen them to the same bf16 tile (exact, see fa_quant.cuh), so the
 // products are those of the values that fa_cache_read returns.
 //
@@ -45,6 +45,7 @@
 #include "fa_host.h"
 #include "fa_internal.h"
 #include "fa_quant.cuh"
+#include "fa_tree.cuh"
 
 namespace fa {
 namespace {
@@ -54,155 +55,10 @@ static_assert(kCacheBf16 == static_cast<int>(FA_CACHE_BF16) &&
                   kCacheInt8 == static_cast<int>(FA_CACHE_INT8),
               "the public formats are the kernels'");
 
-constexpr int kMaxGrid = 192;     // CTAs, at most (the workspace holds two parts of each)
-constexpr int kConvWarps = 8;     // warps that widen 8-bit tiles
+constexpr int kConvWarps = 6;  // warps that widen 8-bit tiles (16 in all: 128 registers)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the max grew by more than 2^8
-
-struct TreeParams {
-  const void *kc, *vc;     // caches [num_pages, Hkv, page, d]
-  const uint8_t *ks, *vs;  // scale bytes [num_pages, Hkv, page]
-  const int *page_table, *hist, *drafts;
-  const uint32_t* mask;    // [B, T, words] or null
-  void* o;                 // bf16 [B, H, T, d]
-  float* lse;              // [B, H, T]
-  float2* part_ml;         // [2 * grid][slot_rows] (max in log2 units, sum)
-  float* part_o;           // [2 * grid][slot_rows][d]
-  int B, Hkv, T, rows;     // rows = H / Hkv * T
-  int groups, slot_rows;   // row groups per key/value head; rows of a part
-  int pair;                // 256-row groups
-  int num_pages, log_page, max_pages, words;
-  float scale;
-  int* err;
-  uint64_t wait_ns;
-};
-
-// Lengths of a sequence, clamped to what the page table can hold.
-struct SeqLen {
-  int hist, nd, tiles;
-  FA_DEV int len() const { return hist + nd; }
-};
-FA_DEV SeqLen seq_len(const TreeParams& p, int b) {
-  SeqLen s;
-  const int cap = p.max_pages << p.log_page;
-  s.hist = min(max(p.hist[b], 0), cap);
-  s.nd = min(p.drafts ? min(max(p.drafts[b], 0), p.T) : p.T, cap - s.hist);
-  // one unit even without a key: somebody has to write the rows
-  s.tiles = max(1, (s.len() + kTile - 1) / kTile);
-  return s;
-}
-
-FA_DEV long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// (all sequences' units, units in front of sequence `before`); whole warp.
-FA_DEV void unit_sums(const TreeParams& p, int before, int lane, long long& total,
-                      long long& front) {
-  long long t = 0, f = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const long long u = static_cast<long long>(seq_len(p, b).tiles) * p.Hkv * p.groups;
-    t += u;
-    if (b < before) f += u;
-  }
-  total = warp_sum(t);
-  front = warp_sum(f);
-}
-
-// A CTA's run of units.
-struct Run {
-  int b, hr, t;      // first unit: sequence, key/value head x group, tile
-  int pad;
-  long long left;    // units
-};
-
-// Run of CTA c of n: units [U c / n, U (c + 1) / n), n at most U so that no
-// run between two others is empty.  Whole warp.
-FA_DEV Run find_run(const TreeParams& p, int c, int n, int lane) {
-  long long total, dummy;
-  unit_sums(p, 0, lane, total, dummy);
-  if (n > total) n = static_cast<int>(total);
-  if (c >= n) return Run{0, 0, 0, 0, 0};
-  const long long u0 = total * c / n, u1 = total * (c + 1) / n;
-  Run r = {0, 0, 0, 0, u1 - u0};
-  long long base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int tiles = b < p.B ? seq_len(p, b).tiles : 0;
-    const long long u = static_cast<long long>(tiles) * p.Hkv * p.groups;
-    long long incl = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > u0);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      const long long rem = __shfl_sync(0xffffffffu, u0 - (base + incl - u), w);
-      const int tw = __shfl_sync(0xffffffffu, tiles, w);
-      r.b = b0 + w;
-      r.hr = static_cast<int>(rem / tw);
-      r.t = static_cast<int>(rem - static_cast<long long>(r.hr) * tw);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return r;
-}
-
-// The parts of problems in a run, in order; every role of the CTA walks it.
-struct PartIter {
-  SeqLen s;
-  int b, hr, t0, t1;  // tiles [t0, t1) of problem (b, hr)
-  int next_t;
-  long long left;
-  FA_DEV void init(const TreeParams& p, const Run& r) {
-    b = r.b;
-    hr = r.hr;
-    next_t = r.t;
-    left = r.left;
-    s = seq_len(p, b);
-  }
-  FA_DEV bool next(const TreeParams& p) {
-    if (left == 0) return false;
-    if (next_t == s.tiles) {
-      next_t = 0;
-      if (++hr == p.Hkv * p.groups) {
-        hr = 0;
-        ++b;
-        s = seq_len(p, b);
-      }
-    }
-    t0 = next_t;
-    const int n = left < s.tiles - t0 ? static_cast<int>(left) : s.tiles - t0;
-    t1 = next_t = t0 + n;
-    left -= n;
-    return true;
-  }
-};
-
-// The tiles of a run, in order.
-struct TileIter {
-  PartIter it;
-  int t = 0, part = -1;
-  bool first = false, last = false;
-  FA_DEV bool next(const TreeParams& p) {
-    first = part < 0 || t + 1 >= it.t1;
-    if (first) {
-      if (!it.next(p)) return false;
-      ++part;
-      t = it.t0;
-    } else {
-      ++t;
-    }
-    last = t + 1 == it.t1;
-    return true;
-  }
-};
 
 // One K or V tile to load: `first` of a part brings that part's Q.
 struct Load {
@@ -214,6 +70,7 @@ struct Load {
 // The order in which the MMAs consume K and V tiles, which is the order of
 // the rings.  pair: K0 V0 K1 V1 ...; split, where a tile's scores are formed
 // before the previous tile's weights are used: K0 K1 V0 K2 V1 ... V(n-1).
+template <bool PAIR>
 struct LoadIter {
   TileIter ti;
   Load cur, prev;
@@ -239,7 +96,7 @@ struct LoadIter {
       return true;
     }
     if (done) return false;
-    if (p.pair && any) {
+    if (PAIR && any) {
       x = cur;
       x.isv = true;
       x.first = false;
@@ -248,7 +105,7 @@ struct LoadIter {
     }
     if (advance(p)) {
       x = cur;
-      if (p.pair) {
+      if (PAIR) {
         any = true;
       } else if (any) {
         owe = true;
@@ -259,7 +116,7 @@ struct LoadIter {
       return true;
     }
     done = true;
-    if (!p.pair && any) {
+    if (!PAIR && any) {
       x = prev;
       x.isv = true;
       x.first = false;
@@ -300,35 +157,6 @@ struct TreeSmem {
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
-// bits 0 .. n-1
-FA_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
-// Which of the 32 keys from position `pos` on draft t of a sequence sees.
-FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const SeqLen& s, int t,
-                          int pos) {
-  const int d0 = pos - s.hist;  // draft index of bit 0
-  uint32_t w;
-  if (!mask_row) {
-    w = low_bits(t + 1 - d0);
-  } else if (d0 >= 0) {
-    const int i = d0 >> 5;
-    w = __funnelshift_r(i < p.words ? mask_row[i] : 0u, i + 1 < p.words ? mask_row[i + 1] : 0u,
-                        d0 & 31);
-  } else {
-    w = d0 > -32 ? mask_row[0] << -d0 : 0u;
-  }
-  return (w & low_bits(s.nd - d0)) | low_bits(-d0);
-}
-
-// untiled bulk copy (16-byte aligned, a multiple of 16 bytes)
-FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 FA_DEV uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -340,48 +168,7 @@ FA_DEV uint2 ld_shared_v2(uint32_t addr) {
   return v;
 }
 
-// a NaN or an infinity in a packed bf16 pair
-FA_DEV bool not_finite2(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-// the pair with NaN and infinities replaced by zero
-FA_DEV uint32_t finite2(uint32_t w) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-  return w;
-}
-
-// Adds the NaN and infinite values among the drafts of positions [lo, hi)
-// that draft t sees to its written row of O (they were zeroed in the tiles):
-// `o` (bf16) or `part` (fp32).  Rare.
-template <int D, int FMT>
-__device__ __noinline__ void add_not_finite(const TreeParams& p, int b, int hkv, SeqLen s, int t,
-                                            int lo, int hi, uint16_t* o, float* part) {
-  const uint32_t* mr = p.mask ? p.mask + (static_cast<size_t>(b) * p.T + t) * p.words : nullptr;
-  for (int pos = lo; pos < hi; ++pos) {
-    if (!(seen_bits(p, mr, s, t, pos) & 1u)) continue;
-    int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (pos >> p.log_page)];
-    page = min(max(page, 0), p.num_pages - 1);
-    const long long row = ((static_cast<long long>(page) * p.Hkv + hkv) << p.log_page) +
-                          (pos & ((1 << p.log_page) - 1));
-    if (FMT != kCacheBf16 && p.vs[row] != kScaleNan) continue;
-    for (int j = 0; j < D; ++j) {
-      const float v = FMT != kCacheBf16
-                          ? __uint_as_float(0x7FFFFFFFu)
-                          : __uint_as_float(static_cast<uint32_t>(
-                                                static_cast<const uint16_t*>(p.vc)[row * D + j])
-                                            << 16);
-      if (isfinite(v)) continue;
-      if (part)
-        part[j] += v;
-      else
-        o[j] = static_cast<uint16_t>(
-            pack_bf16(__uint_as_float(static_cast<uint32_t>(o[j]) << 16) + v, 0.f) & 0xFFFFu);
-    }
-  }
-}
-
-template <int D, int FMT>
+template <int D, int FMT, bool PAIR>
 __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const TreeParams p) {
@@ -446,14 +233,13 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
   auto uwait = [&](uint32_t b, uint32_t ph) {
     return __all_sync(0xffffffffu, wait_bar(b, ph, wc));
   };
-  const bool pair = p.pair != 0;
   TileIter tiles0;
   if (run.left > 0) tiles0.it.init(p, run);
   else tiles0.it.left = 0;
 
   if (warp == 0) {
     // ------------------------------------------------------ loads
-    LoadIter li;
+    LoadIter<PAIR> li;
     li.ti = tiles0;
     Load x;
     uint32_t idx = 0;
@@ -463,13 +249,13 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     while (ok && li.next(p, x)) {
       const int hkv = x.hr / p.groups;
       if (x.first) {
-        const int qb = pair ? 0 : x.part & 1, use = pair ? x.part : x.part >> 1;
+        const int qb = PAIR ? 0 : x.part & 1, use = PAIR ? x.part : x.part >> 1;
         if (use > 0) ok = uwait(bar(L::B_QE + qb), (use - 1) & 1);
         if (!ok) break;
         ++parts;
         if (lane == 0) {
           const int r0 = (x.hr - hkv * p.groups) * 2 * kTile;
-          const bool two = pair && r0 + kTile < p.rows;
+          const bool two = PAIR && r0 + kTile < p.rows;
           mbar_arrive_expect_tx(bar(L::B_QF + qb), (two ? 2 : 1) * L::TILE);
           for (int i = 0; i < (two ? 2 : 1); ++i)
 #pragma unroll
@@ -517,8 +303,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       ++idx;
     }
     // let copies still in flight land before the CTA can exit
-    for (int i = max(0, parts - (pair ? 1 : 2)); i < parts; ++i)
-      drain_bar(bar(L::B_QF + (pair ? 0 : i & 1)), (pair ? i : i >> 1) & 1, p.wait_ns);
+    for (int i = max(0, parts - (PAIR ? 1 : 2)); i < parts; ++i)
+      drain_bar(bar(L::B_QF + (PAIR ? 0 : i & 1)), (PAIR ? i : i >> 1) & 1, p.wait_ns);
     constexpr uint32_t n = L::Q8 ? L::NR : L::NS;
     for (uint32_t j = idx > n ? idx - n : 0; j < idx; ++j)
       drain_bar(bar((L::Q8 ? L::B_RF : L::B_KVF) + j % n), (j / n) & 1, p.wait_ns);
@@ -558,7 +344,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       return uwait(bar(L::B_KVF + idx % L::NS), (idx / L::NS) & 1);
     };
     auto wait_q = [&](int part) {
-      return pair ? uwait(bar(L::B_QF), part & 1) : uwait(bar(L::B_QF + (part & 1)), (part >> 1) & 1);
+      return PAIR ? uwait(bar(L::B_QF), part & 1) : uwait(bar(L::B_QF + (part & 1)), (part >> 1) & 1);
     };
     // which warpgroups a pair tile serves
     auto members = [&](const TileIter& x) {
@@ -568,7 +354,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     bool have = ti.next(p);
     uint32_t g = 0, cnt0 = 0, cnt1 = 0;  // tiles; PVs of each warpgroup
     bool acc0 = false, acc1 = false;
-    int mem = pair && have ? members(ti) : 1;
+    int mem = PAIR && have ? members(ti) : 1;
     int part = ti.part;
     bool last = ti.last;
     if (have) {
@@ -576,21 +362,21 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       if (ok) {
         tc_fence_after();
         const int slot = idx % L::NS;
-        issue_s(0, pair ? 0 : part & 1, slot);
+        issue_s(0, PAIR ? 0 : part & 1, slot);
         ecommit(bar(L::B_SF));
-        if (pair && (mem & 2)) {
+        if (PAIR && (mem & 2)) {
           issue_s(1, 1, slot);
           ecommit(bar(L::B_SF + 1));
         }
         ecommit(bar(L::B_KVE + slot));
-        if (last) ecommit(bar(L::B_QE + (pair ? 0 : part & 1)));
+        if (last) ecommit(bar(L::B_QE + (PAIR ? 0 : part & 1)));
         ++idx;
       }
     }
     while (ok && have) {
       const bool have_n = ti.next(p);
-      const int mem_n = have_n && pair ? members(ti) : 1;
-      if (!pair) {
+      const int mem_n = have_n && PAIR ? members(ti) : 1;
+      if (!PAIR) {
         const int s = g & 1;
         if (have_n) {  // the next tile's scores go to the other warpgroup
           if (ti.first) ok = wait_q(ti.part);
@@ -680,7 +466,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     while (ok && it.next(p)) {
       ++part;
       const int hkv = it.hr / p.groups;
-      const int row0 = pair ? (it.hr - hkv * p.groups) * 2 * kTile + s * kTile : 0;
+      const int row0 = PAIR ? (it.hr - hkv * p.groups) * 2 * kTile + s * kTile : 0;
       const bool mine_all = row0 < p.rows;             // pair: this warpgroup has rows
       const bool busy = row0 + q4 * 32 < p.rows;       // this warp has rows
       const int row = row0 + r, t = row % p.T;
@@ -690,7 +476,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       float m = -INFINITY, l = 0.f;
       int mine = 0;               // tiles of this part done by this warpgroup
       for (int tile = it.t0; tile < it.t1 && ok; ++tile, ++g) {
-        if (pair ? !mine_all : static_cast<int>(g & 1) != s) continue;
+        if (PAIR ? !mine_all : static_cast<int>(g & 1) != s) continue;
         const int kb = tile * kTile;
         const bool tail = kb + kTile > it.s.hist;  // drafts or the end in this tile
         ok = uwait(bar(L::B_SF + s), cnt & 1);
@@ -703,32 +489,40 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
             for (int w = 0; w < 4; ++w)
               vis[w] = valid ? seen_bits(p, mask_row, it.s, t, kb + 32 * w) : 0u;
           }
-          uint32_t sr[2][32];
+          // the scores of a row: all 128 in registers (bf16), or in two
+          // halves, the first read again for its weights (8-bit: the widening
+          // warps leave fewer registers)
+          constexpr int NH = L::Q8 ? 2 : 1, C = 4 / NH;
+          uint32_t sr[C][32];
           auto load_scores = [&](int half) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + 32 * c, sr[c]);
+            for (int c = 0; c < C; ++c) tmem_ld32(tS + 32 * C * half + 32 * c, sr[c]);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) reg_fence(sr[c]);
+            for (int c = 0; c < C; ++c) reg_fence(sr[c]);
             if (tail) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+              for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (!((vis[2 * half + c] >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
+                  if (!((vis[C * half + c] >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
             }
           };
-          float mx0 = -INFINITY, mx1 = -INFINITY;
+          float mx[C];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int c = 0; c < C; ++c) mx[c] = -INFINITY;
+#pragma unroll
+          for (int half = 0; half < NH; ++half) {
             load_scores(half);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              mx0 = fmax3(mx0, __uint_as_float(sr[0][j]), __uint_as_float(sr[0][j + 1]));
-              mx1 = fmax3(mx1, __uint_as_float(sr[1][j]), __uint_as_float(sr[1][j + 1]));
-            }
+            for (int j = 0; j < 32; j += 2)
+#pragma unroll
+              for (int c = 0; c < C; ++c)
+                mx[c] = fmax3(mx[c], __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
           }
-          const float m_new = fmaxf(m, fmaxf(mx0, mx1) * sl2);
+          float mxa = fmaxf(mx[0], mx[1]);
+          if (C == 4) mxa = fmax3(mxa, mx[C - 2], mx[C - 1]);
+          const float m_new = fmaxf(m, mxa * sl2);
           const bool resc = m_new > m + kRescaleLog2;
           const float alpha = resc ? ex2(m - m_new) : 1.f;
           if (resc) {
@@ -740,11 +534,11 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
           const uint64_t sl2x2 = f2_pack(sl2, sl2), nmux2 = f2_pack(-mu, -mu);
           uint64_t la = f2_pack(0.f, 0.f), lb = la;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int half = 1 - k;  // keys 64..127 are in registers
-            if (k == 1) load_scores(0);
+          for (int k = 0; k < NH; ++k) {
+            const int half = NH - 1 - k;  // the last half is in registers
+            if (k > 0) load_scores(half);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < C; ++c) {
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
                 float a, b;
@@ -759,10 +553,9 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
                 lx = f2_add(lx, f2_pack(a, b));
                 sr[c][j / 2] = pack_bf16(a, b);
               }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              tmem_st16(tP + 32 * half + 16 * c,
+              tmem_st16(tP + 16 * (C * half + c),
                         *reinterpret_cast<const uint32_t(*)[16]>(&sr[c][0]));
+            }
           }
           {
             float a, b;
@@ -783,11 +576,11 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
           }
           tmem_st_wait();
         }
-        if (!L::Q8 && tail && !(pair && s == 1)) {
+        if (!L::Q8 && tail && !(PAIR && s == 1)) {
           // One V row per thread: zero past the last token, zero NaN and
           // infinities of drafts.  (Not before this tile's scores: only they
           // show that the ring slot's last tile has come and gone.)
-          const uint32_t vi = pair ? 2 * g + 1 : g + 1 == total ? 2 * g + 1 : 2 * g + 2;
+          const uint32_t vi = PAIR ? 2 * g + 1 : g + 1 == total ? 2 * g + 1 : 2 * g + 2;
           ok = uwait(bar(L::B_KVF + vi % L::NS), (vi / L::NS) & 1);
           if (!ok) break;
           const uint32_t v0 = sb + L::KV + (vi % L::NS) * L::TILE;
@@ -824,7 +617,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------- end of a part
-      if (!pair && s == 1) {
+      if (!PAIR && s == 1) {
         if (owe_x2) ok = uwait(bar(L::B_X2), (part - 1) & 1);
         if (!ok) break;
         ml[r] = make_float2(m, l);
@@ -834,13 +627,13 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         continue;
       }
       ok = uwait(bar(L::B_OF), part & 1);
-      if (ok && !pair) ok = uwait(bar(L::B_X1), part & 1);
+      if (ok && !PAIR) ok = uwait(bar(L::B_X1), part & 1);
       if (!ok) break;
       tc_fence_after();
       if (busy) {
         int other = 0;  // the other warpgroup's tiles of this part
         float a0 = 1.f, a1 = 0.f;
-        if (!pair) {
+        if (!PAIR) {
           other = it.t1 - it.t0 - mine;
           const float2 x = ml[r];
           const float mm = fmaxf(m, x.x), mu = mm == -INFINITY ? 0.f : mm;
@@ -854,7 +647,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         const float inv = has ? 1.f / l : 0.f;
         const size_t orow = (static_cast<size_t>(it.b) * p.Hkv + hkv) * p.rows + row;
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (it.t0 == 0 ? 1 : 0);
-        const size_t prow = slot * p.slot_rows + (pair ? s * kTile : 0) + r;
+        const size_t prow = slot * p.slot_rows + (PAIR ? s * kTile : 0) + r;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[32];
@@ -907,7 +700,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
                                  whole ? static_cast<uint16_t*>(p.o) + orow * D : nullptr,
                                  whole ? nullptr : p.part_o + prow * D);
       }
-      if (!pair) {
+      if (!PAIR) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::B_X2));
@@ -919,9 +712,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     // stores.  Which half comes first alternates (`sel`) so that the lanes
     // of an access fall on different banks.
     constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per row, rows per step
-    constexpr int ROWS = kTile / kConvWarps;     // rows of a tile per warp
     const int cw = warp - 10, u = lane % LPR, rl = lane / LPR;
-    LoadIter li;
+    LoadIter<PAIR> li;
     li.ti = tiles0;
     Load x;
     uint32_t idx = 0;
@@ -936,8 +728,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       const uint32_t dst = sb + L::KV + ds * L::TILE;
       const int nval = x.s.len() - x.kb, ndraft = x.s.hist - x.kb;
 #pragma unroll 2
-      for (int i = 0; i < ROWS / RPI; ++i) {
-        const int row = cw * ROWS + i * RPI + rl;
+      for (int r0 = cw * RPI; r0 < kTile; r0 += kConvWarps * RPI) {
+        const int row = r0 + rl;
         const int sel = D == 128 ? ((u >> 2) ^ row) & 1 : (row >> 1) & 1;
         const uint32_t a = raw + row * D + 16 * u;
         const uint2 w0 = ld_shared_v2(a + 8 * sel), w1 = ld_shared_v2(a + 8 * (sel ^ 1));
@@ -1049,27 +841,49 @@ size_t tree_ws_bytes(int H, int Hkv, int T, int d) {
   return tree_ml_bytes(rows) + align256(2ull * kMaxGrid * slot_rows(rows) * d * sizeof(float));
 }
 
-template <int D, int FMT>
-cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, cudaStream_t stream) {
+// Tiles of the longest sequence that the page table can hold.
+long long most_tiles(const TreeParams& p) {
+  return ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
+}
+
+// CTAs: one per SM, no more than there can be units (0 on error).
+int tree_grid(const TreeParams& p) {
+  const int sms = sm_count();
+  const long long most = static_cast<long long>(p.B) * p.Hkv * p.groups * most_tiles(p);
+  const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+  return most < grid ? static_cast<int>(most) : grid;
+}
+
+cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t stream) {
+  // tables of one tile: every problem is one unit, nothing to join
+  if (most_tiles(p) == 1) return cudaSuccess;
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.rows;
+  const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
+  return d == 64 ? launch_pdl(fa_tree_join_kernel<64>, blocks, dim3(256), 0, stream, p, grid)
+                 : launch_pdl(fa_tree_join_kernel<128>, blocks, dim3(256), 0, stream, p, grid);
+}
+
+template <int D, int FMT, bool PAIR>
+cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t stream) {
   using L = TreeSmem<D, FMT>;
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(
-      attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT>), L::ALLOC);
+      attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT, PAIR>), L::ALLOC);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const long long most_tiles = ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
-  const long long most = static_cast<long long>(p.B) * p.Hkv * p.groups * most_tiles;
-  int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  if (most < grid) grid = static_cast<int>(most);
-  e = launch_pdl(fa_tree_kernel<D, FMT>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream, tq, tk, tv,
-                 p);
-  // tables of one tile: every problem is one unit, nothing to join
-  if (e != cudaSuccess || most_tiles == 1) return e;
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.rows;
-  return launch_pdl(fa_tree_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256),
-                    0, stream, p, grid);
+  const int grid = tree_grid(p);
+  if (grid <= 0) return cudaErrorInvalidDevice;
+  e = launch_pdl(fa_tree_kernel<D, FMT, PAIR>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream, tq,
+                 tk, tv, p);
+  if (e != cudaSuccess) return e;
+  return launch_join(p, D, grid, stream);
+}
+
+template <int D, int FMT>
+cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, cudaStream_t stream) {
+  return p.pair ? launch_tree_mode<D, FMT, true>(p, tq, tk, tv, stream)
+                : launch_tree_mode<D, FMT, false>(p, tq, tk, tv, stream);
 }
 
 }  // namespace
@@ -1133,6 +947,16 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.err = err;
   p.wait_ns = wait_limit_ns();
   CUtensorMap tq, tk, tv;
+  if (p.rows <= kFewRows) {
+    if (!make_cache_map(&tk, k_cache, num_pages * Hkv, page_size, d, format != kCacheBf16) ||
+        !make_cache_map(&tv, v_cache, num_pages * Hkv, page_size, d, format != kCacheBf16))
+      return FA_ERR_CUDA;
+    const int grid = tree_grid(p);
+    if (grid <= 0) return FA_ERR_CUDA;
+    FA_CUDA(launch_tree_few(p, format, d, q, tk, tv, grid, stream));
+    FA_CUDA(launch_join(p, d, grid, stream));
+    return FA_OK;
+  }
   if (!make_tile_map(&tq, q, B * Hkv, p.rows, d)) return FA_ERR_CUDA;
   if (format == kCacheBf16) {
     if (!make_tile_map(&tk, k_cache, num_pages * Hkv, page_size, d, page_size) ||

@@ -1,0 +1,236 @@
+// What the tree attention kernels share: the arguments, the lengths of the
+// sequences, the split of the work into runs, and which keys a draft sees.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "fa_internal.h"
+#include "fa_quant.cuh"
+
+namespace fa {
+
+constexpr int kMaxGrid = 192;     // CTAs, at most (the workspace holds two parts of each)
+
+struct TreeParams {
+  const void *kc, *vc;     // caches [num_pages, Hkv, page, d]
+  const uint8_t *ks, *vs;  // scale bytes [num_pages, Hkv, page]
+  const int *page_table, *hist, *drafts;
+  const uint32_t* mask;    // [B, T, words] or null
+  void* o;                 // bf16 [B, H, T, d]
+  float* lse;              // [B, H, T]
+  float2* part_ml;         // [2 * grid][slot_rows] (max in log2 units, sum)
+  float* part_o;           // [2 * grid][slot_rows][d]
+  int B, Hkv, T, rows;     // rows = H / Hkv * T
+  int groups, slot_rows;   // row groups per key/value head; rows of a part
+  int pair;                // 256-row groups
+  int num_pages, log_page, max_pages, words;
+  float scale;
+  int* err;
+  uint64_t wait_ns;
+};
+
+// Lengths of a sequence, clamped to what the page table can hold.
+struct SeqLen {
+  int hist, nd, tiles;
+  FA_DEV int len() const { return hist + nd; }
+};
+FA_DEV SeqLen seq_len(const TreeParams& p, int b) {
+  SeqLen s;
+  const int cap = p.max_pages << p.log_page;
+  s.hist = min(max(p.hist[b], 0), cap);
+  s.nd = min(p.drafts ? min(max(p.drafts[b], 0), p.T) : p.T, cap - s.hist);
+  // one unit even without a key: somebody has to write the rows
+  s.tiles = max(1, (s.len() + kTile - 1) / kTile);
+  return s;
+}
+
+FA_DEV long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// (all sequences' units, units in front of sequence `before`); whole warp.
+FA_DEV void unit_sums(const TreeParams& p, int before, int lane, long long& total,
+                      long long& front) {
+  long long t = 0, f = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const long long u = static_cast<long long>(seq_len(p, b).tiles) * p.Hkv * p.groups;
+    t += u;
+    if (b < before) f += u;
+  }
+  total = warp_sum(t);
+  front = warp_sum(f);
+}
+
+// A CTA's run of units.
+struct Run {
+  int b, hr, t;      // first unit: sequence, key/value head x group, tile
+  int pad;
+  long long left;    // units
+};
+
+// Run of CTA c of n: units [U c / n, U (c + 1) / n), n at most U so that no
+// run between two others is empty.  Whole warp.
+FA_DEV Run find_run(const TreeParams& p, int c, int n, int lane) {
+  long long total, dummy;
+  unit_sums(p, 0, lane, total, dummy);
+  if (n > total) n = static_cast<int>(total);
+  if (c >= n) return Run{0, 0, 0, 0, 0};
+  const long long u0 = total * c / n, u1 = total * (c + 1) / n;
+  Run r = {0, 0, 0, 0, u1 - u0};
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int tiles = b < p.B ? seq_len(p, b).tiles : 0;
+    const long long u = static_cast<long long>(tiles) * p.Hkv * p.groups;
+    long long incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > u0);
+    if (hit) {
+      const int w = __ffs(hit) - 1;
+      const long long rem = __shfl_sync(0xffffffffu, u0 - (base + incl - u), w);
+      const int tw = __shfl_sync(0xffffffffu, tiles, w);
+      r.b = b0 + w;
+      r.hr = static_cast<int>(rem / tw);
+      r.t = static_cast<int>(rem - static_cast<long long>(r.hr) * tw);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
+// The parts of problems in a run, in order; every role of the CTA walks it.
+struct PartIter {
+  SeqLen s;
+  int b, hr, t0, t1;  // tiles [t0, t1) of problem (b, hr)
+  int next_t;
+  long long left;
+  FA_DEV void init(const TreeParams& p, const Run& r) {
+    b = r.b;
+    hr = r.hr;
+    next_t = r.t;
+    left = r.left;
+    s = seq_len(p, b);
+  }
+  FA_DEV bool next(const TreeParams& p) {
+    if (left == 0) return false;
+    if (next_t == s.tiles) {
+      next_t = 0;
+      if (++hr == p.Hkv * p.groups) {
+        hr = 0;
+        ++b;
+        s = seq_len(p, b);
+      }
+    }
+    t0 = next_t;
+    const int n = left < s.tiles - t0 ? static_cast<int>(left) : s.tiles - t0;
+    t1 = next_t = t0 + n;
+    left -= n;
+    return true;
+  }
+};
+
+// The tiles of a run, in order.
+struct TileIter {
+  PartIter it;
+  int t = 0, part = -1;
+  bool first = false, last = false;
+  FA_DEV bool next(const TreeParams& p) {
+    first = part < 0 || t + 1 >= it.t1;
+    if (first) {
+      if (!it.next(p)) return false;
+      ++part;
+      t = it.t0;
+    } else {
+      ++t;
+    }
+    last = t + 1 == it.t1;
+    return true;
+  }
+};
+
+// bits 0 .. n-1
+FA_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Which of the 32 keys from position `pos` on draft t of a sequence sees.
+FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const SeqLen& s, int t,
+                          int pos) {
+  const int d0 = pos - s.hist;  // draft index of bit 0
+  uint32_t w;
+  if (!mask_row) {
+    w = low_bits(t + 1 - d0);
+  } else if (d0 >= 0) {
+    const int i = d0 >> 5;
+    w = __funnelshift_r(i < p.words ? mask_row[i] : 0u, i + 1 < p.words ? mask_row[i + 1] : 0u,
+                        d0 & 31);
+  } else {
+    w = d0 > -32 ? mask_row[0] << -d0 : 0u;
+  }
+  return (w & low_bits(s.nd - d0)) | low_bits(-d0);
+}
+
+// untiled bulk copy (16-byte aligned, a multiple of 16 bytes)
+FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// a NaN or an infinity in a packed bf16 pair
+FA_DEV bool not_finite2(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+// the pair with NaN and infinities replaced by zero
+FA_DEV uint32_t finite2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Adds the NaN and infinite values among the drafts of positions [lo, hi)
+// that draft t sees to its written row of O (they were zeroed in the tiles):
+// `o` (bf16) or `part` (fp32).  Rare.
+template <int D, int FMT>
+static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, int hkv, SeqLen s, int t,
+                                            int lo, int hi, uint16_t* o, float* part) {
+  const uint32_t* mr = p.mask ? p.mask + (static_cast<size_t>(b) * p.T + t) * p.words : nullptr;
+  for (int pos = lo; pos < hi; ++pos) {
+    if (!(seen_bits(p, mr, s, t, pos) & 1u)) continue;
+    int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (pos >> p.log_page)];
+    page = min(max(page, 0), p.num_pages - 1);
+    const long long row = ((static_cast<long long>(page) * p.Hkv + hkv) << p.log_page) +
+                          (pos & ((1 << p.log_page) - 1));
+    if (FMT != kCacheBf16 && p.vs[row] != kScaleNan) continue;
+    for (int j = 0; j < D; ++j) {
+      const float v = FMT != kCacheBf16
+                          ? __uint_as_float(0x7FFFFFFFu)
+                          : __uint_as_float(static_cast<uint32_t>(
+                                                static_cast<const uint16_t*>(p.vc)[row * D + j])
+                                            << 16);
+      if (isfinite(v)) continue;
+      if (part)
+        part[j] += v;
+      else
+        o[j] = static_cast<uint16_t>(
+            pack_bf16(__uint_as_float(static_cast<uint32_t>(o[j]) << 16) + v, 0.f) & 0xFFFFu);
+    }
+  }
+}
+
+// Few query rows (p.rows <= kFewRows): fa_tree_few.cu.  tk, tv: maps of
+// 16-row boxes (make_cache_map).
+constexpr int kFewRows = 32;
+cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const void* q,
+                            const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                            cudaStream_t stream);
+
+}  // namespace fa
