@@ -3,26 +3,28 @@
 //
 // With so few rows the work is reading the cache: per 128 keys a
 // 128-row tensor-core tile would compute (and its softmax walk) mostly
-// padding.  So here the rows are the M = 16 side of warp-level MMAs and
-// every warp keeps its own running softmax over its own keys:
+// padding.  So here the keys are the M = 16 side of warp-level MMAs, the rows
+// the N = 8 side (these MMAs take 32 cycles each, so a 16-row side would
+// already cost more than the memory), and every warp keeps its own running
+// softmax over its own keys:
 //   A CTA has 8 warps and a run of units as in fa_tree.cu (a unit is 128 keys
 //   of a (sequence, key/value head)); warp w takes keys 16 w .. 16 w + 15 of
 //   each unit through its own ring of TMA slots (K and V of 16 keys each) and
 //   meets the other warps only at the end of a problem, where their O and
 //   (m, l) are added.  16 keys never cross a page.
-//   S = Q K^T and O += P V stay in registers: the accumulator layout of S is
-//   the operand layout of P.
+//   S^T = K Q^T (16 keys x 8 rows) and O^T += V^T P^T (16 columns x 8 rows)
+//   stay in registers; P^T becomes an operand by an 8 x 8 transpose.
 //
-// Contraction indices and key columns may be permuted freely as long as both
-// operands agree, which gives every lane whole 16-byte pieces of a row:
-//   * lane (g = lane / 4, c = lane % 4) reads for the key in column n = g of
-//     an 8-key tile the pieces c (and c + 4) of the row; Q's fragments are the
-//     same pieces of rows g and g + 8;
-//   * column n stands for key n / 2 (n even) or (n / 2) ^ 5 (n odd), which
-//     keeps the eight lanes of a shared-memory access on different banks;
+// Contraction indices, keys and columns may be permuted freely as long as
+// both operands agree, which gives every lane whole 16-byte pieces of a row:
+//   * lane (g = lane / 4, c = lane % 4) reads the pieces c (and c + 4) of its
+//     keys' rows; Q's fragments are the same pieces of row g;
+//   * index m of 8 keys stands for key m / 2 (m even) or (m / 2) ^ 5 (m odd),
+//     which keeps the eight lanes of a shared-memory access on different
+//     banks;
 //   * 8-bit V: lane (g, c) reads one piece (d / 8 elements) of the rows of
-//     keys c and c ^ 5 and pairs them byte by byte, so tile t of the output
-//     holds element t of the pieces.
+//     keys c and c ^ 5 and pairs them byte by byte, so column tile i of the
+//     output holds elements 2 i and 2 i + 1 of the pieces.
 //
 // 8-bit caches: the stored numbers go to the MMA as f16 (exact), the scales
 // stay outside: a key's scale multiplies its score, a value's is added to
@@ -52,15 +54,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // O is rescaled when the max grew by more than 2^8
 constexpr float kLift = 7.0f;  // f16 weights: 2^7 above the max, 2^15 at most
 
-template <int D, int FMT, int MT>
+// RT: 8-row tiles of the query rows
+template <int D, int FMT, int RT>
 struct FewSmem {
   static constexpr bool Q8 = FMT != kCacheBf16;
   static constexpr int EB = Q8 ? 1 : 2;
   static constexpr int KBYTES = kFewKeys * D * EB;  // 16 keys or values
   static constexpr int SLOT = 2 * KBYTES;
   static constexpr int R = Q8 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // slots per warp
-  static constexpr int ROWS = 16 * MT;
-  static constexpr int CW = 64 / MT;                // columns added up at a time
+  static constexpr int ROWS = 8 * RT;
+  // columns added up at a time: at most 32 KB of the 8 warps' rows
+  static constexpr int CW = RT == 1 ? D : RT == 2 ? 64 : 32;
   static constexpr int RING = 0;
   static constexpr int SUM = RING + kFewWarps * R * SLOT;  // [8][ROWS][CW] fp32; (m, l) first
   static constexpr int SC = SUM + kFewWarps * ROWS * CW * 4;  // scale bytes: 16 + 16 per slot
@@ -93,6 +97,14 @@ FA_DEV void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+
+// 8 x 8 transpose of 16-bit elements: lane (g, c) gives (g, 2c), (g, 2c + 1)
+// and gets (2c, g), (2c + 1, g)
+FA_DEV uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 FA_DEV uint32_t pack_f16(float lo, float hi) {
@@ -138,13 +150,16 @@ FA_DEV uint2 lds_v2(uint32_t addr) {
   return v;
 }
 
-FA_DEV float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// over the eight lanes of a row (the same lane % 4)
+FA_DEV float lanes_max(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
-FA_DEV float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+FA_DEV float lanes_sum(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // The 16-key pieces of one warp, in the order of its run.
@@ -168,13 +183,13 @@ struct PieceIter {
   FA_DEV int pos(int w) const { return t * kTile + w * kFewKeys; }
 };
 
-template <int D, int FMT, int MT>
+template <int D, int FMT, int RT>
 __global__ void __launch_bounds__(kFewWarps * 32, 1)
     fa_tree_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const void* q, const TreeParams p) {
-  using L = FewSmem<D, FMT, MT>;
+  using L = FewSmem<D, FMT, RT>;
   constexpr bool Q8 = L::Q8;
-  constexpr int NT = D / 8;   // 8-column tiles of O
+  constexpr int MT = D / 16;  // 16-column tiles of O
   constexpr int QR = D / 8;   // packed registers of a row's share of a lane (2 elements each)
   grid_dep_wait();  // the previous kernel's writes are visible from here on
   grid_dep_launch();
@@ -244,9 +259,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
   for (int i = 0; i < L::R; ++i) fetch();
 
   const float sl2 = p.scale * kLog2e;
-  // key of column n in an 8-key tile: lanes read column n = g
-  const int krow = (g & 1) ? (g >> 1) ^ 5 : g >> 1;
-  const int k0 = c, k1 = c ^ 5;  // keys of columns 2c, 2c + 1
+  const int k_own = (g & 1) ? (g >> 1) ^ 5 : g >> 1;  // key of index g
+  const int k0 = c, k1 = c ^ 5;                       // keys of indices 2c, 2c + 1
   PartIter it;
   it.init(p, run);
   uint32_t used = 0;
@@ -254,61 +268,61 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
   bool ok = true;  // false: a wait gave up; the warp still meets the others
   while (it.next(p)) {
     ++part;
-    // ---- Q of this part: rows g and g + 8 of each 16-row tile
-    uint32_t qf[MT][2][QR];
-    float frow[MT][2];          // score factor of a row (log2 units)
-    uint32_t vis[MT][2];
-    int trow[MT][2];            // draft of a row, -1 for none
+    // ---- Q of this part: row 8 rt + g of each tile
+    uint32_t qf[RT][QR];
+    float frow[RT][2];  // score factor of rows 8 rt + 2c, + 1 (log2 units)
+    int trow[RT][2];    // their drafts, -1 for none
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int rt = 0; rt < RT; ++rt) {
+      const int row = 8 * rt + g;
+      const uint16_t* qrow = static_cast<const uint16_t*>(q) +
+                             ((static_cast<size_t>(it.b) * p.Hkv + it.hr) * p.rows + row) * D;
+      // pieces of 16 bytes: bf16 keys pair with pieces c, c + 4 of each 64
+      // elements; 8-bit keys have 16 elements to a piece, two of these
+#pragma unroll
+      for (int i = 0; i < QR / 4; ++i) {
+        const int piece = Q8 ? 2 * (c + 4 * (i >> 1)) + (i & 1) : 8 * (i >> 1) + c + 4 * (i & 1);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < p.rows) v = *reinterpret_cast<const uint4*>(qrow + 8 * piece);
+        qf[rt][4 * i] = v.x;
+        qf[rt][4 * i + 1] = v.y;
+        qf[rt][4 * i + 2] = v.z;
+        qf[rt][4 * i + 3] = v.w;
+      }
+      float f = sl2;
+      if (Q8) {
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < QR; ++i) m2 = __vmaxu2(m2, qf[rt][i] & 0x7FFF7FFFu);
+        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // 2^E <= max < 2^(E+1); times 2^(14 - E).  E >= -100 keeps both
+        // factors normal.
+        const int E = max(static_cast<int>(m >> 7) - 127, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - E) << 23);
+        f = sl2 * __uint_as_float(static_cast<uint32_t>(127 + E - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < QR; ++i)
+          qf[rt][i] = pack_f16(bf16_lo(qf[rt][i]) * up, bf16_hi(qf[rt][i]) * up);
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = 16 * mt + 8 * r + g;
-        const bool in = row < p.rows;
-        const int t = row % p.T;
-        trow[mt][r] = in && t < it.s.nd ? t : -1;
-        const uint16_t* qrow = static_cast<const uint16_t*>(q) +
-                               ((static_cast<size_t>(it.b) * p.Hkv + it.hr) * p.rows + row) * D;
-        // pieces of 16 bytes: bf16 keys pair with pieces c, c + 4 of each 64
-        // elements; 8-bit keys have 16 elements to a piece, two of these
-#pragma unroll
-        for (int i = 0; i < QR / 4; ++i) {
-          const int piece = Q8 ? 2 * (c + 4 * (i >> 1)) + (i & 1) : 8 * (i >> 1) + c + 4 * (i & 1);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (in) v = *reinterpret_cast<const uint4*>(qrow + 8 * piece);
-          qf[mt][r][4 * i] = v.x;
-          qf[mt][r][4 * i + 1] = v.y;
-          qf[mt][r][4 * i + 2] = v.z;
-          qf[mt][r][4 * i + 3] = v.w;
-        }
-        frow[mt][r] = sl2;
-        if (Q8) {
-          uint32_t m2 = 0;
-#pragma unroll
-          for (int i = 0; i < QR; ++i) m2 = __vmaxu2(m2, qf[mt][r][i] & 0x7FFF7FFFu);
-          uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          // 2^E <= max < 2^(E+1); times 2^(14 - E).  E >= -100 keeps both
-          // factors normal.
-          const int E = max(static_cast<int>(m >> 7) - 127, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - max(E, -100)) << 23);
-          frow[mt][r] = sl2 * __uint_as_float(static_cast<uint32_t>(127 + E - 14) << 23);
-#pragma unroll
-          for (int i = 0; i < QR; ++i)
-            qf[mt][r][i] = pack_f16(bf16_lo(qf[mt][r][i]) * up, bf16_hi(qf[mt][r][i]) * up);
-        }
+        frow[rt][r] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + r));
+        const int row2 = 8 * rt + 2 * c + r, t = row2 % p.T;
+        trow[rt][r] = row2 < p.rows && t < it.s.nd ? t : -1;
       }
-    float o[MT][NT][4];
-    float M[MT][2], m[MT][2], l[MT][2];
+    }
+    float o[RT][MT][4];  // column tile: (element 0, rows 2c, 2c + 1), (element 1, ...)
+    float M[RT][2], m[RT][2], l[RT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[rt][i][e] = 0.f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) M[mt][r] = m[mt][r] = -INFINITY, l[mt][r] = 0.f;
+      for (int r = 0; r < 2; ++r) M[rt][r] = m[rt][r] = -INFINITY, l[rt][r] = 0.f;
     }
     bool bad = false;
 #pragma unroll 1
@@ -320,158 +334,143 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
       if (!ok) break;
       const uint32_t ka = ring + slot * L::SLOT, va = ka + L::KBYTES;
       const bool tail = pos + kFewKeys > it.s.hist;
-      // ---- S = Q K^T
-      float s[MT][2][4];
+      // ---- S^T = K Q^T: s[rt] = (key g, rows 2c, 2c + 1), (key 8 + g, ...)
+      float s[RT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int e = 0; e < 4; ++e) s[rt][e] = 0.f;
+      if (!Q8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
-        const int row = 8 * j + krow;
-        if (!Q8) {
+        for (int i = 0; i < D / 32; ++i) {  // pieces of 8 elements
+          const uint32_t at = (i >> 1) * kFewKeys * 128 + sw128_offset(k_own, c + 4 * (i & 1));
+          const uint4 a = ld_shared_v4(ka + at), b = ld_shared_v4(ka + at + 8 * 128);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {  // pieces of 8 elements
-            const int chunk = c + 4 * (i & 1);
-            const uint4 k = ld_shared_v4(ka + (i >> 1) * kFewKeys * 128 + sw128_offset(row, chunk));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16816<false>(s[mt][j], qf[mt][0][4 * i], qf[mt][1][4 * i], qf[mt][0][4 * i + 1],
-                              qf[mt][1][4 * i + 1], k.x, k.y);
-              mma16816<false>(s[mt][j], qf[mt][0][4 * i + 2], qf[mt][1][4 * i + 2],
-                              qf[mt][0][4 * i + 3], qf[mt][1][4 * i + 3], k.z, k.w);
-            }
+          for (int rt = 0; rt < RT; ++rt) {
+            mma16816<false>(s[rt], a.x, b.x, a.y, b.y, qf[rt][4 * i], qf[rt][4 * i + 1]);
+            mma16816<false>(s[rt], a.z, b.z, a.w, b.w, qf[rt][4 * i + 2], qf[rt][4 * i + 3]);
           }
-        } else {
+        }
+      } else {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {  // pieces of 16 elements
-            const uint32_t at = D == 128 ? sw128_offset(row, c + 4 * i)
-                                         : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-            const uint4 k = ld_shared_v4(ka + at);
-            const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
+        for (int i = 0; i < D / 64; ++i) {  // pieces of 16 elements
+          const uint32_t at = D == 128 ? sw128_offset(k_own, c + 4 * i)
+                                       : k_own * 64 + ((c ^ ((k_own >> 1) & 3)) << 4);
+          const uint4 a = ld_shared_v4(ka + at), b = ld_shared_v4(ka + at + 8 * D);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t b0, b1;
-              stored_f16<FMT>(kw[x], b0, b1);
+          for (int x = 0; x < 4; ++x) {
+            uint32_t a0, a2, a1, a3;
+            stored_f16<FMT>(aw[x], a0, a2);
+            stored_f16<FMT>(bw[x], a1, a3);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma16816<true>(s[mt][j], qf[mt][0][8 * i + 2 * x], qf[mt][1][8 * i + 2 * x],
-                               qf[mt][0][8 * i + 2 * x + 1], qf[mt][1][8 * i + 2 * x + 1], b0, b1);
-            }
+            for (int rt = 0; rt < RT; ++rt)
+              mma16816<true>(s[rt], a0, a1, a2, a3, qf[rt][8 * i + 2 * x],
+                             qf[rt][8 * i + 2 * x + 1]);
           }
         }
       }
-      // ---- softmax step; keys of s[.][j][e]: 8 j + (e & 1 ? k1 : k0)
-      float fk[4], ev[4];
+      // ---- softmax step over keys k_own and 8 + k_own
+      float fk[2], ev[2];
       if (Q8) {
         const uint32_t sc = scales + slot * 32;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = 8 * (x >> 1) + ((x & 1) ? k1 : k0);
-          fk[x] = scale_value(lds_u8(sc + key));
-          ev[x] = scale_exponent(lds_u8(sc + 16 + key));
+        for (int x = 0; x < 2; ++x) {
+          fk[x] = scale_value(lds_u8(sc + 8 * x + k_own));
+          ev[x] = scale_exponent(lds_u8(sc + 16 + 8 * x + k_own));
         }
       }
-      if (tail) {
+      uint32_t pf[RT][2];  // P^T operands: keys 0-7, 8-15
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int t = trow[mt][r];
-            vis[mt][r] =
-                t < 0 ? 0u
-                      : seen_bits(p,
-                                  p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words
-                                         : nullptr,
-                                  it.s, t, pos);
-          }
-      }
-      uint32_t pf[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int rt = 0; rt < RT; ++rt) {
+        float e[2][2];  // [row][key]
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float x[4], y[4];  // scores, and with the value's exponent (log2 units)
+          float x[2], y[2];  // scores, and with the value's exponent (log2 units)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = s[mt][i >> 1][2 * r + (i & 1)] * frow[mt][r];
+          for (int i = 0; i < 2; ++i) {
+            x[i] = s[rt][2 * i + r] * frow[rt][r];
             y[i] = x[i];
             if (Q8) {
               x[i] *= fk[i];
               y[i] = x[i] + ev[i];
             }
           }
-          if (tail)
+          if (tail) {
+            const int t = trow[rt][r];
+            const uint32_t vis =
+                t < 0 ? 0u
+                      : seen_bits(p,
+                                  p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words
+                                         : nullptr,
+                                  it.s, t, pos);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!((vis[mt][r] >> (8 * (i >> 1) + ((i & 1) ? k1 : k0))) & 1u))
-                x[i] = y[i] = -INFINITY;
-          const float ymax = quad_max(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
-          float alpha = 1.f;
-          if (ymax > M[mt][r] + kLazy) {
-            alpha = ex2(M[mt][r] - ymax);
-            M[mt][r] = ymax;
+            for (int i = 0; i < 2; ++i)
+              if (!((vis >> (8 * i + k_own)) & 1u)) x[i] = y[i] = -INFINITY;
           }
-          const float Mu = M[mt][r] == -INFINITY ? 0.f : M[mt][r] - (Q8 ? kLift : 0.f);
-          float e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2(y[i] - Mu);
+          const float ymax = lanes_max(fmaxf(y[0], y[1]));
+          float alpha = 1.f;
+          if (ymax > M[rt][r] + kLazy) {
+            alpha = ex2(M[rt][r] - ymax);
+            M[rt][r] = ymax;
+          }
+          const float Mu = M[rt][r] == -INFINITY ? 0.f : M[rt][r] - (Q8 ? kLift : 0.f);
+          e[r][0] = ex2(y[0] - Mu);
+          e[r][1] = ex2(y[1] - Mu);
           if (!Q8) {
-            l[mt][r] = l[mt][r] * alpha + ((e[0] + e[1]) + (e[2] + e[3]));
-            m[mt][r] = M[mt][r];
-            pf[mt][r] = pack_bf16(e[0], e[1]);
-            pf[mt][2 + r] = pack_bf16(e[2], e[3]);
+            l[rt][r] = l[rt][r] * alpha + (e[r][0] + e[r][1]);
+            m[rt][r] = M[rt][r];
           } else {
-            // the sum is the lane's own: its four keys of each piece
-            const float xmax = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            if (xmax > m[mt][r] + kLazy) {
-              l[mt][r] *= ex2(m[mt][r] - xmax);
-              m[mt][r] = xmax;
+            // the sum is the lane's own: its two keys of each piece
+            const float xmax = fmaxf(x[0], x[1]);
+            if (xmax > m[rt][r] + kLazy) {
+              l[rt][r] *= ex2(m[rt][r] - xmax);
+              m[rt][r] = xmax;
             }
-            const float mu = m[mt][r] == -INFINITY ? 0.f : m[mt][r];
-            l[mt][r] += (ex2(x[0] - mu) + ex2(x[1] - mu)) + (ex2(x[2] - mu) + ex2(x[3] - mu));
-            pf[mt][r] = pack_f16(e[0], e[1]);
-            pf[mt][2 + r] = pack_f16(e[2], e[3]);
+            const float mu = m[rt][r] == -INFINITY ? 0.f : m[rt][r];
+            l[rt][r] += ex2(x[0] - mu) + ex2(x[1] - mu);
           }
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              o[mt][t][2 * r] *= alpha;
-              o[mt][t][2 * r + 1] *= alpha;
+            for (int i = 0; i < MT; ++i) {
+              o[rt][i][r] *= alpha;
+              o[rt][i][2 + r] *= alpha;
             }
           }
         }
-      // ---- O += P V
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          pf[rt][i] =
+              transpose8(Q8 ? pack_f16(e[0][i], e[1][i]) : pack_bf16(e[0][i], e[1][i]));
+      }
+      // ---- O^T += V^T P^T
       const int nval = it.s.len() - pos, ndraft = it.s.hist - pos;
       if (!Q8) {
-        // rows of the four 8 x 8 pieces: keys 0-7 and 8-15 of two column tiles
-        const int j = lane & 7, vrow = 8 * ((lane >> 3) & 1) + ((j & 1) ? (j >> 1) ^ 5 : j >> 1);
+        // rows of the four 8 x 8 pieces: keys 0-7 and 8-15 of two column halves
+        const int j = lane & 7, vrow = 8 * (lane >> 4) + ((j & 1) ? (j >> 1) ^ 5 : j >> 1);
 #pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-          const int cc = t + (lane >> 4);
-          uint32_t b[4];
-          ldmatrix_x4_trans(va + (cc >> 3) * kFewKeys * 128 + sw128_offset(vrow, cc & 7), b);
+        for (int i = 0; i < MT; ++i) {
+          const int cc = 2 * i + ((lane >> 3) & 1);
+          uint32_t a[4];  // (keys 0-7, columns 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+          ldmatrix_x4_trans(va + (cc >> 3) * kFewKeys * 128 + sw128_offset(vrow, cc & 7), a);
           if (tail) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int ka0 = 8 * (x & 1) + k0, ka1 = 8 * (x & 1) + k1;
-              if (ka0 >= nval) b[x] &= 0xFFFF0000u;  // past the last token
-              if (ka1 >= nval) b[x] &= 0x0000FFFFu;
-              const uint32_t f = finite2(b[x]);  // drafts: back at the end of the part
-              if (f != b[x] && (ka0 >= ndraft || ka1 >= ndraft)) {
-                const uint32_t keep = (ka0 < ndraft ? 0x0000FFFFu : 0u) |
-                                      (ka1 < ndraft ? 0xFFFF0000u : 0u);
-                const uint32_t n = (f & ~keep) | (b[x] & keep);
-                bad |= n != b[x];
-                b[x] = n;
-              }
+              const int ka0 = 8 * (x >> 1) + k0, ka1 = 8 * (x >> 1) + k1;
+              if (ka0 >= nval) a[x] &= 0xFFFF0000u;  // past the last token
+              if (ka1 >= nval) a[x] &= 0x0000FFFFu;
+              // NaN and infinities of drafts: back at the end of the part
+              const uint32_t f = finite2(a[x]);
+              const uint32_t history =
+                  (ka0 < ndraft ? 0x0000FFFFu : 0u) | (ka1 < ndraft ? 0xFFFF0000u : 0u);
+              const uint32_t n = (f & ~history) | (a[x] & history);
+              bad |= n != a[x];
+              a[x] = n;
             }
           }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<false>(o[mt][t], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], b[0], b[1]);
-            mma16816<false>(o[mt][t + 1], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], b[2], b[3]);
-          }
+          for (int rt = 0; rt < RT; ++rt)
+            mma16816<false>(o[rt][i], a[0], a[1], a[2], a[3], pf[rt][0], pf[rt][1]);
         }
       } else {
         constexpr int WV = D / 32;  // words of a lane's piece: 16 or 8 elements
@@ -494,18 +493,18 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
 #pragma unroll
         for (int i = 0; i < WV; ++i) {
           // bytes (key a, key b) of two columns to a word
-          uint32_t b[2][4];
+          uint32_t a[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            stored_f16<FMT>(__byte_perm(v[2 * h][i], v[2 * h + 1][i], 0x5140), b[h][0], b[h][1]);
-            stored_f16<FMT>(__byte_perm(v[2 * h][i], v[2 * h + 1][i], 0x7362), b[h][2], b[h][3]);
+            stored_f16<FMT>(__byte_perm(v[2 * h][i], v[2 * h + 1][i], 0x5140), a[h][0], a[h][1]);
+            stored_f16<FMT>(__byte_perm(v[2 * h][i], v[2 * h + 1][i], 0x7362), a[h][2], a[h][3]);
           }
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma16816<true>(o[mt][4 * i + x], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], b[0][x],
-                             b[1][x]);
+            for (int rt = 0; rt < RT; ++rt)
+              mma16816<true>(o[rt][2 * i + x], a[0][2 * x], a[0][2 * x + 1], a[1][2 * x],
+                             a[1][2 * x + 1], pf[rt][0], pf[rt][1]);
         }
       }
       ++used;
@@ -517,13 +516,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     float2* ml = reinterpret_cast<float2*>(smem + L::SUM);
     float2* fin = reinterpret_cast<float2*>(smem + L::FIN);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float mq = Q8 ? quad_max(m[mt][r]) : m[mt][r];
+        const float mq = Q8 ? lanes_max(m[rt][r]) : m[rt][r];
         const float mu = mq == -INFINITY ? 0.f : mq;
-        const float lq = quad_sum(l[mt][r] * ex2(m[mt][r] - mu));
-        if (c == 0) ml[w * L::ROWS + 16 * mt + 8 * r + g] = make_float2(mq, lq);
+        const float lq = lanes_sum(l[rt][r] * ex2(m[rt][r] - mu));
+        if (g == 0) ml[w * L::ROWS + 8 * rt + 2 * c + r] = make_float2(mq, lq);
       }
     __syncthreads();
     if (threadIdx.x < L::ROWS) {
@@ -545,54 +544,50 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         (2 * static_cast<size_t>(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * p.slot_rows;
     float* sum = reinterpret_cast<float*>(smem + L::SUM);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         // O in units of 2^m; the factor in two steps (M - m reaches 128)
-        const float mm = fin[16 * mt + 8 * r + g].x;
-        const float a = mm == -INFINITY ? 0.f : ex2(0.5f * (M[mt][r] - (Q8 ? kLift : 0.f) - mm));
+        const float mm = fin[8 * rt + 2 * c + r].x;
+        const float a = mm == -INFINITY ? 0.f : ex2(0.5f * (M[rt][r] - (Q8 ? kLift : 0.f) - mm));
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) o[mt][t][2 * r + e] = o[mt][t][2 * r + e] * a * a;
+        for (int i = 0; i < MT; ++i) {
+          o[rt][i][r] = o[rt][i][r] * a * a;
+          o[rt][i][2 + r] = o[rt][i][2 + r] * a * a;
+        }
       }
 #pragma unroll
     for (int pass = 0; pass < D / L::CW; ++pass) {
       const int lo = pass * L::CW;
-      // column of o[.][t][e]; rows 8 apart share a bank pattern, turned by g
-      auto put = [&](int mt, int r, int col, float v) {
-        const int row = 16 * mt + 8 * r + g;
-        sum[(w * L::ROWS + row) * L::CW + ((col - lo) ^ (8 * (g & 3)))] = v;
-      };
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              int col;
-              if (!Q8) {
-                col = 8 * t + 2 * c + e;
-              } else if (D == 128) {
-                col = 64 * e + 16 * c + t;
-              } else {
-                col = 32 * (c & 1) + 16 * (c >> 1) + 8 * e + t;
-              }
-              if (col >= lo && col < lo + L::CW) put(mt, r, col, o[mt][t][2 * r + e]);
+          for (int e = 0; e < 4; ++e) {
+            const int hi = e >> 1, row = 8 * rt + 2 * c + (e & 1);
+            int col;
+            if (!Q8) {
+              col = 16 * i + 8 * hi + g;
+            } else if (D == 128) {
+              col = 16 * ((g >> 1) + 4 * (g & 1)) + 2 * i + hi;
+            } else {
+              col = 8 * ((g & 1) + 4 * ((g >> 1) & 1) + 2 * (g >> 2)) + 2 * i + hi;
             }
+            if (col >= lo && col < lo + L::CW)
+              sum[(w * L::ROWS + row) * L::CW + ((col - lo) ^ (8 * ((row >> 1) & 3)))] = o[rt][i][e];
+          }
       __syncthreads();
       constexpr int TPR = L::CW / 4;  // threads per row, four columns each
       const int row = threadIdx.x / TPR, col = 4 * (threadIdx.x % TPR);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < L::ROWS && row < p.rows) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kFewWarps; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(
-            &sum[(i * L::ROWS + row) * L::CW + (col ^ (8 * (row & 3)))]);
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-      }
-      if (row < p.rows) {
+        for (int i = 0; i < kFewWarps; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(
+              &sum[(i * L::ROWS + row) * L::CW + (col ^ (8 * ((row >> 1) & 3)))]);
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
         const bool valid = row % p.T < it.s.nd;
         const float2 f = fin[row];
         if (whole) {
@@ -625,23 +620,28 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
   for (uint32_t i = used; i < sent; ++i) drain_bar(bars + 8 * (i % L::R), (i / L::R) & 1, p.wait_ns);
 }
 
-template <int D, int FMT, int MT>
+template <int D, int FMT, int RT>
 cudaError_t launch_few_rows(const TreeParams& p, const void* q, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  using L = FewSmem<D, FMT, MT>;
+  using L = FewSmem<D, FMT, RT>;
   static std::atomic<unsigned long long> attr_done{0};
   const cudaError_t e = smem_attr_once(
-      attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, MT>), L::ALLOC);
+      attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, RT>), L::ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fa_tree_few_kernel<D, FMT, MT>, dim3(grid), dim3(kFewWarps * 32), L::ALLOC,
+  return launch_pdl(fa_tree_few_kernel<D, FMT, RT>, dim3(grid), dim3(kFewWarps * 32), L::ALLOC,
                     stream, tk, tv, q, p);
 }
 
 template <int D, int FMT>
 cudaError_t launch_few_fmt(const TreeParams& p, const void* q, const CUtensorMap& tk,
                            const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  return p.rows <= 16 ? launch_few_rows<D, FMT, 1>(p, q, tk, tv, grid, stream)
-                      : launch_few_rows<D, FMT, 2>(p, q, tk, tv, grid, stream);
+  switch ((p.rows + 7) / 8) {
+    case 1: return launch_few_rows<D, FMT, 1>(p, q, tk, tv, grid, stream);
+    case 2: return launch_few_rows<D, FMT, 2>(p, q, tk, tv, grid, stream);
+    case 3: return launch_few_rows<D, FMT, 3>(p, q, tk, tv, grid, stream);
+    case 4: return launch_few_rows<D, FMT, 4>(p, q, tk, tv, grid, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
