@@ -428,7 +428,7 @@ bool make_acc_map(CUtensorMap* map, const void* base, int BH, int N, int d) {
   return encode_map(map, MapKey{base, BH, N, d, kMapF32, 32});
 }
 bool make_cache_map(CUtensorMap* map, const void* base, int tiles, int page, int d, bool bytes) {
-  return encode_map(map, MapKey{base, tiles, page, d, bytes ? kMapU8 : kMapBf16, 16});
+  return encode_map(map, MapKey{base, tiles, page, d, bytes ? kMapU8 : kMapBf16, page});
 }
 }  // namespace fa
 

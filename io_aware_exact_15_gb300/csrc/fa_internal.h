@@ -151,9 +151,9 @@ bool make_tile_map(CUtensorMap* map, const void* base, int BH, int N, int d,
 // (128-byte rows, 128-byte swizzle): the dQ accumulator for TMA reduce-add.
 bool make_acc_map(CUtensorMap* map, const void* base, int BH, int N, int d);
 
-// 3-D view {d, page, pages x heads} of a paged key/value cache, 16-row boxes:
-// bf16 (64-column boxes, 128-byte swizzle) or stored bytes (whole rows,
-// swizzled over their 128 or 64 bytes).
+// 3-D view {d, page, pages x heads} of a paged key/value cache, boxes of a
+// page's rows: bf16 (64-column boxes, 128-byte swizzle) or stored bytes (whole
+// rows, swizzled over their 128 or 64 bytes).
 bool make_cache_map(CUtensorMap* map, const void* base, int tiles, int page, int d, bool bytes);
 
 cudaError_t launch_forward(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,

@@ -7,11 +7,12 @@
 // the N = 8 side (these MMAs take 32 cycles each, so a 16-row side would
 // already cost more than the memory), and every warp keeps its own running
 // softmax over its own keys:
-//   A CTA has 8 warps and a run of units as in fa_tree.cu (a unit is 128 keys
-//   of a (sequence, key/value head)); warp w takes keys 16 w .. 16 w + 15 of
-//   each unit through its own ring of TMA slots (K and V of 16 keys each) and
-//   meets the other warps only at the end of a problem, where their O and
-//   (m, l) are added.  16 keys never cross a page.
+//   A CTA has a run of units as in fa_tree.cu (a unit is 128 keys of a
+//   (sequence, key/value head)).  Two warps load (one K, one V) whole units
+//   into a ring of stages; the others take the units' 16-key chunks in turn
+//   and meet only at the end of a problem, where their O and (m, l) are
+//   added.  A chunk is a chain of dependent steps of some 1500 cycles, so
+//   many warps (14 where registers allow) are needed to follow the memory.
 //   S^T = K Q^T (16 keys x 8 rows) and O^T += V^T P^T (16 columns x 8 rows)
 //   stay in registers; P^T becomes an operand by an 8 x 8 transpose.
 //
@@ -47,8 +48,8 @@
 namespace fa {
 namespace {
 
-constexpr int kFewWarps = 8;
-constexpr int kFewKeys = 16;  // keys per warp and unit
+constexpr int kLoadWarps = 2;  // K, V
+constexpr int kFewKeys = 16;   // keys of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // O is rescaled when the max grew by more than 2^8
@@ -59,19 +60,25 @@ template <int D, int FMT, int RT>
 struct FewSmem {
   static constexpr bool Q8 = FMT != kCacheBf16;
   static constexpr int EB = Q8 ? 1 : 2;
-  static constexpr int KBYTES = kFewKeys * D * EB;  // 16 keys or values
-  static constexpr int SLOT = 2 * KBYTES;
-  static constexpr int R = Q8 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // slots per warp
+  static constexpr int CH = Q8 ? 1 : D / 64;            // column chunks of a tile
+  static constexpr int CHUNK = kTile * (Q8 ? D : 128);  // bytes of one: [128 rows x 128 or D B]
+  static constexpr int KBYTES = CH * CHUNK;             // 128 keys or values
+  static constexpr int STAGE = 2 * KBYTES;
+  static constexpr int R = Q8 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // stages
+  // warps that compute: 128, 168 or 255 registers each
+  static constexpr int NC = RT == 1 ? 14 : RT == 2 ? 10 : 6;
+  static constexpr int THREADS = 32 * (NC + kLoadWarps);
   static constexpr int ROWS = 8 * RT;
-  // columns added up at a time: at most 32 KB of the 8 warps' rows
-  static constexpr int CW = RT == 1 ? D : RT == 2 ? 64 : 32;
+  // columns added up at a time: at most 32 KB of the warps' rows
+  static constexpr int CW = RT == 1 ? 64 : 32;
   static constexpr int RING = 0;
-  static constexpr int SUM = RING + kFewWarps * R * SLOT;  // [8][ROWS][CW] fp32; (m, l) first
-  static constexpr int SC = SUM + kFewWarps * ROWS * CW * 4;  // scale bytes: 16 + 16 per slot
-  static constexpr int FIN = SC + (Q8 ? kFewWarps * R * 32 : 0);  // (m, l) of the rows
-  static constexpr int BAR = FIN + ROWS * 8;
-  static constexpr int MISC = BAR + kFewWarps * R * 8;  // abort flag, bad part
-  static constexpr int ALLOC = MISC + 16 + 1024;        // + slack for 1024-byte alignment
+  static constexpr int SUM = RING + R * STAGE;            // [NC][ROWS][CW] fp32; (m, l) first
+  static constexpr int SC = SUM + NC * ROWS * CW * 4;     // scale bytes: 128 + 128 per stage
+  static constexpr int FIN = SC + (Q8 ? R * 256 : 0);     // (m, l) of the rows
+  static constexpr int BAR = FIN + ROWS * 8;              // full, empty of each stage
+  static constexpr int RUN = BAR + R * 16;
+  static constexpr int MISC = RUN + 24;                   // abort flag, bad parts
+  static constexpr int ALLOC = MISC + 16 + 1024;          // + slack for 1024-byte alignment
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
@@ -162,29 +169,8 @@ FA_DEV float lanes_sum(float v) {
   return v;
 }
 
-// The 16-key pieces of one warp, in the order of its run.
-struct PieceIter {
-  PartIter it;
-  int t = 0;
-  bool in_part = false;
-  // next piece with a key; false at the end of the run
-  FA_DEV bool next(const TreeParams& p, int w) {
-    for (;;) {
-      if (in_part && t + 1 < it.t1) {
-        ++t;
-      } else {
-        if (!it.next(p)) return false;
-        in_part = true;
-        t = it.t0;
-      }
-      if (pos(w) < it.s.len()) return true;
-    }
-  }
-  FA_DEV int pos(int w) const { return t * kTile + w * kFewKeys; }
-};
-
 template <int D, int FMT, int RT>
-__global__ void __launch_bounds__(kFewWarps * 32, 1)
+__global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
     fa_tree_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const void* q, const TreeParams p) {
   using L = FewSmem<D, FMT, RT>;
@@ -197,73 +183,91 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC);
   // whether part p has NaN or infinite draft values: entry p % 2 says p
   volatile int* bad_parts = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
-  const uint32_t ring = sb + L::RING + w * L::R * L::SLOT;
-  const uint32_t scales = sb + L::SC + w * L::R * 32;
-  const uint32_t bars = sb + L::BAR + w * L::R * 8;
+  Run* run_slot = reinterpret_cast<Run*>(smem + L::RUN);
+  auto full = [&](int stage) { return sb + L::BAR + 16 * stage; };
+  auto empty = [&](int stage) { return sb + L::BAR + 16 * stage + 8; };
 
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
+    const Run r = find_run(p, blockIdx.x, gridDim.x, lane);
+    if (lane == 0) *run_slot = r;
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < L::R; ++i) {
+      mbar_init(full(i), 2);   // K and V
+      mbar_init(empty(i), 8);  // chunks
+    }
     *abort_flag = 0;
     bad_parts[0] = bad_parts[1] = -1;
+    fence_mbar_init();
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
-  if (lane == 0) {
-    for (int i = 0; i < L::R; ++i) mbar_init(bars + 8 * i, 1);
-    fence_mbar_init();
-  }
-  const Run run = find_run(p, blockIdx.x, gridDim.x, lane);
   __syncthreads();
+  const Run run = *run_slot;
   if (run.left == 0) return;
   const WaitCtl wc{abort_flag, p.err, p.wait_ns};
 
-  // ---- loads: this warp's next piece to fetch, its page already looked up
-  PieceIter ld;
-  ld.it.init(p, run);
-  bool more = ld.next(p, w);
-  int page = 0;
-  auto look_up = [&]() {
-    if (more)
-      page = p.page_table[static_cast<size_t>(ld.it.b) * p.max_pages + (ld.pos(w) >> p.log_page)];
-  };
-  look_up();
-  uint32_t sent = 0;
-  auto fetch = [&]() {
-    if (!more) return;
-    if (lane == 0) {
-      const int slot = sent % L::R;
-      const uint32_t bar = bars + 8 * slot, dst = ring + slot * L::SLOT;
-      const int id = min(max(page, 0), p.num_pages - 1);
-      const int hkv = ld.it.hr;
-      const int row = ld.pos(w) & ((1 << p.log_page) - 1), z = id * p.Hkv + hkv;
-      mbar_arrive_expect_tx(bar, L::SLOT + (Q8 ? 32 : 0));
-      constexpr int CH = Q8 ? 1 : D / 64;
+  if (warp < kLoadWarps) {
+    // ------------------------------------------------------ loads
+    const bool isv = warp == 1;
+    const CUtensorMap* map = isv ? &tv : &tk;
+    const uint8_t* sc = isv ? p.vs : p.ks;
+    const int psize = 1 << p.log_page;
+    TileIter ti;
+    ti.it.init(p, run);
+    uint32_t n = 0;
+    bool ok = true;
+    // pages of the next tile that hold a token, one per lane
+    bool have = ti.next(p);
+    int np = 0, id = 0;
+    auto look_up = [&]() {
+      const int kb = ti.t * kTile, nval = min(max(ti.it.s.len() - kb, 0), kTile);
+      np = (nval + psize - 1) >> p.log_page;
+      id = 0;
+      if (lane < np)
+        id = p.page_table[static_cast<size_t>(ti.it.b) * p.max_pages + (kb >> p.log_page) + lane];
+    };
+    if (have) look_up();
+    while (have) {
+      const int stage = n % L::R;
+      if (n >= L::R) ok = __all_sync(0xffffffffu, wait_bar(empty(stage), (n / L::R - 1) & 1, wc));
+      if (!ok) break;
+      if (lane == 0)
+        mbar_arrive_expect_tx(full(stage), np * psize * (D * L::EB + (Q8 ? 1 : 0)));
+      __syncwarp();
+      if (lane < np) {
+        const int z = min(max(id, 0), p.num_pages - 1) * p.Hkv + ti.it.hr;
+        const uint32_t dst = sb + L::RING + stage * L::STAGE + (isv ? L::KBYTES : 0) +
+                             lane * psize * (Q8 ? D : 128);
 #pragma unroll
-      for (int h = 0; h < CH; ++h) {
-        tma_load_3d(dst + h * kFewKeys * 128, &tk, bar, 64 * h, row, z);
-        tma_load_3d(dst + L::KBYTES + h * kFewKeys * 128, &tv, bar, 64 * h, row, z);
+        for (int h = 0; h < L::CH; ++h)
+          tma_load_3d(dst + h * L::CHUNK, map, full(stage), 64 * h, 0, z);
+        if (Q8)
+          bulk_load(sb + L::SC + stage * 256 + (isv ? 128 : 0) + lane * psize,
+                    sc + (static_cast<size_t>(z) << p.log_page), psize, full(stage));
       }
-      if (Q8) {
-        const size_t at = (static_cast<size_t>(z) << p.log_page) + row;
-        bulk_load(scales + slot * 32, p.ks + at, 16, bar);
-        bulk_load(scales + slot * 32 + 16, p.vs + at, 16, bar);
-      }
+      ++n;
+      have = ti.next(p);
+      if (have) look_up();
     }
-    ++sent;
-    more = ld.next(p, w);
-    look_up();
-  };
-  for (int i = 0; i < L::R; ++i) fetch();
+    // let copies still in flight land before the CTA can exit
+    for (uint32_t j = n > L::R ? n - L::R : 0; j < n; ++j)
+      drain_bar(full(j % L::R), (j / L::R) & 1, p.wait_ns);
+    return;
+  }
 
+  // -------------------------------------------------------- attention
+  const int w = warp - kLoadWarps, tid = threadIdx.x - 32 * kLoadWarps;
+  auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * L::NC) : "memory"); };
   const float sl2 = p.scale * kLog2e;
   const int k_own = (g & 1) ? (g >> 1) ^ 5 : g >> 1;  // key of index g
   const int k0 = c, k1 = c ^ 5;                       // keys of indices 2c, 2c + 1
   PartIter it;
   it.init(p, run);
-  uint32_t used = 0;
+  uint32_t n = 0;  // tiles of the run
   int part = -1;
   bool ok = true;  // false: a wait gave up; the warp still meets the others
   while (it.next(p)) {
@@ -325,14 +329,23 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
       for (int r = 0; r < 2; ++r) M[rt][r] = m[rt][r] = -INFINITY, l[rt][r] = 0.f;
     }
     bool bad = false;
+    int chunk = w;  // of the part; this warp's next one
 #pragma unroll 1
-    for (int tile = it.t0; ok && tile < it.t1; ++tile) {
-      const int pos = tile * kTile + w * kFewKeys;
-      if (pos >= it.s.len()) break;  // this warp's keys end in front of the tile's
-      const int slot = used % L::R;
-      ok = __all_sync(0xffffffffu, wait_bar(bars + 8 * slot, (used / L::R) & 1, wc));
-      if (!ok) break;
-      const uint32_t ka = ring + slot * L::SLOT, va = ka + L::KBYTES;
+    for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
+     const int stage = n % L::R;
+     // every tile is waited for in turn, also those without a chunk of this
+     // warp: a barrier's parity tells two loads of a stage apart, not three
+     ok = ok && __all_sync(0xffffffffu, wait_bar(full(stage), (n / L::R) & 1, wc));
+     if (!ok) continue;
+#pragma unroll 1
+     for (; chunk < 8 * (tile - it.t0 + 1); chunk += L::NC) {
+      const int sub = chunk & 7, pos = tile * kTile + sub * kFewKeys;
+      if (pos >= it.s.len()) {  // nothing there
+        if (lane == 0) mbar_arrive(empty(stage));
+        continue;
+      }
+      const uint32_t ka = sb + L::RING + stage * L::STAGE + sub * kFewKeys * (Q8 ? D : 128);
+      const uint32_t va = ka + L::KBYTES;
       const bool tail = pos + kFewKeys > it.s.hist;
       // ---- S^T = K Q^T: s[rt] = (key g, rows 2c, 2c + 1), (key 8 + g, ...)
       float s[RT][4];
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
       if (!Q8) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {  // pieces of 8 elements
-          const uint32_t at = (i >> 1) * kFewKeys * 128 + sw128_offset(k_own, c + 4 * (i & 1));
+          const uint32_t at = (i >> 1) * L::CHUNK + sw128_offset(k_own, c + 4 * (i & 1));
           const uint4 a = ld_shared_v4(ka + at), b = ld_shared_v4(ka + at + 8 * 128);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
@@ -373,11 +386,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
       // ---- softmax step over keys k_own and 8 + k_own
       float fk[2], ev[2];
       if (Q8) {
-        const uint32_t sc = scales + slot * 32;
+        const uint32_t sc = sb + L::SC + stage * 256 + sub * kFewKeys;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           fk[x] = scale_value(lds_u8(sc + 8 * x + k_own));
-          ev[x] = scale_exponent(lds_u8(sc + 16 + 8 * x + k_own));
+          ev[x] = scale_exponent(lds_u8(sc + 128 + 8 * x + k_own));
         }
       }
       uint32_t pf[RT][2];  // P^T operands: keys 0-7, 8-15
@@ -452,7 +465,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         for (int i = 0; i < MT; ++i) {
           const int cc = 2 * i + ((lane >> 3) & 1);
           uint32_t a[4];  // (keys 0-7, columns 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-          ldmatrix_x4_trans(va + (cc >> 3) * kFewKeys * 128 + sw128_offset(vrow, cc & 7), a);
+          ldmatrix_x4_trans(va + (cc >> 3) * L::CHUNK + sw128_offset(vrow, cc & 7), a);
           if (tail) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -507,9 +520,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
                              a[1][2 * x + 1], pf[rt][0], pf[rt][1]);
         }
       }
-      ++used;
-      __syncwarp();  // every lane has read the slot
-      fetch();
+      __syncwarp();  // every lane has read the chunk
+      if (lane == 0) mbar_arrive(empty(stage));
+     }
     }
     // ---- end of the part: the warps' rows are added in a fixed order
     if (bad) bad_parts[part & 1] = part;
@@ -524,20 +537,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         const float lq = lanes_sum(l[rt][r] * ex2(m[rt][r] - mu));
         if (g == 0) ml[w * L::ROWS + 8 * rt + 2 * c + r] = make_float2(mq, lq);
       }
-    __syncthreads();
-    if (threadIdx.x < L::ROWS) {
+    meet();
+    if (tid < L::ROWS) {
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int i = 0; i < kFewWarps; ++i) mm = fmaxf(mm, ml[i * L::ROWS + threadIdx.x].x);
+      for (int i = 0; i < L::NC; ++i) mm = fmaxf(mm, ml[i * L::ROWS + tid].x);
       const float mu = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-      for (int i = 0; i < kFewWarps; ++i) {
-        const float2 x = ml[i * L::ROWS + threadIdx.x];
+      for (int i = 0; i < L::NC; ++i) {
+        const float2 x = ml[i * L::ROWS + tid];
         ll = fmaf(x.y, ex2(x.x - mu), ll);
       }
-      fin[threadIdx.x] = make_float2(mm, ll);
+      fin[tid] = make_float2(mm, ll);
     }
-    __syncthreads();
+    meet();
     const bool whole = it.t0 == 0 && it.t1 == it.s.tiles;
     const size_t orow0 = (static_cast<size_t>(it.b) * p.Hkv + it.hr) * p.rows;
     const size_t prow0 =
@@ -577,16 +590,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
             if (col >= lo && col < lo + L::CW)
               sum[(w * L::ROWS + row) * L::CW + ((col - lo) ^ (8 * ((row >> 1) & 3)))] = o[rt][i][e];
           }
-      __syncthreads();
+      meet();
       constexpr int TPR = L::CW / 4;  // threads per row, four columns each
-      const int row = threadIdx.x / TPR, col = 4 * (threadIdx.x % TPR);
-      if (row < L::ROWS && row < p.rows) {
+      for (int x = tid; x < L::ROWS * TPR; x += 32 * L::NC) {
+        const int row = x / TPR, col = 4 * (x % TPR);
+        if (row >= p.rows) break;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kFewWarps; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(
+        for (int i = 0; i < L::NC; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(
               &sum[(i * L::ROWS + row) * L::CW + (col ^ (8 * ((row >> 1) & 3)))]);
-          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
         }
         const bool valid = row % p.T < it.s.nd;
         const float2 f = fin[row];
@@ -605,10 +619,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
             p.part_ml[prow0 + row] = make_float2(valid ? f.x : -INFINITY, valid ? f.y : 0.f);
         }
       }
-      __syncthreads();
+      meet();
     }
     if (!Q8 && bad_parts[part & 1] == part) {  // after the barrier: the rows are written
-      const int row = threadIdx.x, t = row % p.T;
+      const int row = tid, t = row % p.T;
       if (row < p.rows && t < it.s.nd)
         add_not_finite<D, FMT>(p, it.b, it.hr, it.s, t, max(it.s.hist, it.t0 * kTile),
                                min(it.s.len(), it.t1 * kTile),
@@ -616,8 +630,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
                                whole ? nullptr : p.part_o + (prow0 + row) * D);
     }
   }
-  // copies still in flight (only after a wait gave up) land before the CTA exits
-  for (uint32_t i = used; i < sent; ++i) drain_bar(bars + 8 * (i % L::R), (i / L::R) & 1, p.wait_ns);
 }
 
 template <int D, int FMT, int RT>
@@ -628,7 +640,7 @@ cudaError_t launch_few_rows(const TreeParams& p, const void* q, const CUtensorMa
   const cudaError_t e = smem_attr_once(
       attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, RT>), L::ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fa_tree_few_kernel<D, FMT, RT>, dim3(grid), dim3(kFewWarps * 32), L::ALLOC,
+  return launch_pdl(fa_tree_few_kernel<D, FMT, RT>, dim3(grid), dim3(L::THREADS), L::ALLOC,
                     stream, tk, tv, q, p);
 }
 
