@@ -8,11 +8,13 @@
 // already cost more than the memory), and every warp keeps its own running
 // softmax over its own keys:
 //   A CTA has a run of units as in fa_tree.cu (a unit is 128 keys of a
-//   (sequence, key/value head)).  Two warps load (one K, one V) whole units
-//   into a ring of stages; the others take the units' 16-key chunks in turn
-//   and meet only at the end of a problem, where their O and (m, l) are
-//   added.  A chunk is a chain of dependent steps of some 1500 cycles, so
-//   many warps (14 where registers allow) are needed to follow the memory.
+//   (sequence, key/value head)).  Some warps load whole units into a ring of
+//   stages (K and V apart, up to 8 rows also odd and even units apart: a unit
+//   costs such a warp 1700 cycles, the memory 1540 at 8 bits); the others
+//   take the units' 16-key chunks in turn and meet only at the end of a
+//   problem, where their O and (m, l) are added.  A chunk is a chain of
+//   dependent steps of some 1500 cycles, so many warps (12 where registers
+//   allow) are needed to follow the memory.
 //   S^T = K Q^T (16 keys x 8 rows) and O^T += V^T P^T (16 columns x 8 rows)
 //   stay in registers; P^T becomes an operand by an 8 x 8 transpose.
 //
@@ -48,7 +50,6 @@
 namespace fa {
 namespace {
 
-constexpr int kLoadWarps = 2;  // K, V
 constexpr int kFewKeys = 16;   // keys of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,10 +65,14 @@ struct FewSmem {
   static constexpr int CHUNK = kTile * (Q8 ? D : 128);  // bytes of one: [128 rows x 128 or D B]
   static constexpr int KBYTES = CH * CHUNK;             // 128 keys or values
   static constexpr int STAGE = 2 * KBYTES;
-  static constexpr int R = Q8 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // stages
-  // warps that compute: 128, 168 or 255 registers each
-  static constexpr int NC = RT == 1 ? 14 : RT == 2 ? 10 : 6;
-  static constexpr int THREADS = 32 * (NC + kLoadWarps);
+  static constexpr int R = Q8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);  // stages
+  // Warps that load.  With four each stage belongs to one pair of them (an
+  // even number of stages), so that no warp waits for a stage whose last
+  // load but one is another warp's.
+  static constexpr int NL = RT == 1 && R % 2 == 0 ? 4 : 2;
+  // warps that compute; 128, 168 or 255 registers for each of the CTA's
+  static constexpr int NC = RT == 1 ? 16 - NL : RT == 2 ? 10 : 6;
+  static constexpr int THREADS = 32 * (NC + NL);
   static constexpr int ROWS = 8 * RT;
   // columns added up at a time: at most 32 KB of the warps' rows
   static constexpr int CW = RT == 1 ? 64 : 32;
@@ -141,9 +146,10 @@ FA_DEV void stored_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
 FA_DEV float scale_value(uint32_t byte) {
   return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(byte << 23);
 }
-// byte - 127
+// byte - 127: the byte as the last bits of 2^23, less 2^23 + 127
 FA_DEV float scale_exponent(uint32_t byte) {
-  return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu) : static_cast<float>(static_cast<int>(byte) - 127);
+  return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu)
+                           : __uint_as_float(0x4B000000u | byte) - 8388735.f;
 }
 
 FA_DEV uint32_t lds_u8(uint32_t addr) {
@@ -210,18 +216,27 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
   if (run.left == 0) return;
   const WaitCtl wc{abort_flag, p.err, p.wait_ns};
 
-  if (warp < kLoadWarps) {
+  if (warp < L::NL) {
     // ------------------------------------------------------ loads
-    const bool isv = warp == 1;
+    // warp 0: K, warp 1: V; with four warps 2, 3 the same of the odd tiles
+    constexpr uint32_t STEP = L::NL / 2;
+    const bool isv = warp & 1;
     const CUtensorMap* map = isv ? &tv : &tk;
     const uint8_t* sc = isv ? p.vs : p.ks;
     const int psize = 1 << p.log_page;
     TileIter ti;
     ti.it.init(p, run);
-    uint32_t n = 0;
+    const uint32_t n0 = warp >> 1;
+    uint32_t n = n0;
     bool ok = true;
-    // pages of the next tile that hold a token, one per lane
+    auto next = [&]() {
+      bool have = ti.next(p);
+      for (uint32_t i = 1; i < STEP && have; ++i) have = ti.next(p);
+      return have;
+    };
     bool have = ti.next(p);
+    if (n0 > 0 && have) have = ti.next(p);
+    // pages of the next tile that hold a token, one per lane
     int np = 0, id = 0;
     auto look_up = [&]() {
       const int kb = ti.t * kTile, nval = min(max(ti.it.s.len() - kb, 0), kTile);
@@ -249,18 +264,18 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
           bulk_load(sb + L::SC + stage * 256 + (isv ? 128 : 0) + lane * psize,
                     sc + (static_cast<size_t>(z) << p.log_page), psize, full(stage));
       }
-      ++n;
-      have = ti.next(p);
+      n += STEP;
+      have = next();
       if (have) look_up();
     }
     // let copies still in flight land before the CTA can exit
-    for (uint32_t j = n > L::R ? n - L::R : 0; j < n; ++j)
-      drain_bar(full(j % L::R), (j / L::R) & 1, p.wait_ns);
+    for (uint32_t j = n0; j < n; j += STEP)
+      if (j + L::R >= n) drain_bar(full(j % L::R), (j / L::R) & 1, p.wait_ns);
     return;
   }
 
   // -------------------------------------------------------- attention
-  const int w = warp - kLoadWarps, tid = threadIdx.x - 32 * kLoadWarps;
+  const int w = warp - L::NL, tid = threadIdx.x - 32 * L::NL;
   auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * L::NC) : "memory"); };
   const float sl2 = p.scale * kLog2e;
   const int k_own = (g & 1) ? (g >> 1) ^ 5 : g >> 1;  // key of index g
@@ -396,18 +411,15 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
       uint32_t pf[RT][2];  // P^T operands: keys 0-7, 8-15
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float e[2][2];  // [row][key]
+        float x[2][2], y[2][2];  // [row][key]: scores, and with the value's exponent (log2 units)
+        bool over = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float x[2], y[2];  // scores, and with the value's exponent (log2 units)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            x[i] = s[rt][2 * i + r] * frow[rt][r];
-            y[i] = x[i];
-            if (Q8) {
-              x[i] *= fk[i];
-              y[i] = x[i] + ev[i];
-            }
+            x[r][i] = s[rt][2 * i + r] * frow[rt][r];
+            if (Q8) x[r][i] *= fk[i];
+            y[r][i] = Q8 ? x[r][i] + ev[i] : x[r][i];
           }
           if (tail) {
             const int t = trow[rt][r];
@@ -419,36 +431,47 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
                                   it.s, t, pos);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              if (!((vis >> (8 * i + k_own)) & 1u)) x[i] = y[i] = -INFINITY;
+              if (!((vis >> (8 * i + k_own)) & 1u)) x[r][i] = y[r][i] = -INFINITY;
           }
-          const float ymax = lanes_max(fmaxf(y[0], y[1]));
-          float alpha = 1.f;
-          if (ymax > M[rt][r] + kLazy) {
-            alpha = ex2(M[rt][r] - ymax);
-            M[rt][r] = ymax;
-          }
-          const float Mu = M[rt][r] == -INFINITY ? 0.f : M[rt][r] - (Q8 ? kLift : 0.f);
-          e[r][0] = ex2(y[0] - Mu);
-          e[r][1] = ex2(y[1] - Mu);
-          if (!Q8) {
-            l[rt][r] = l[rt][r] * alpha + (e[r][0] + e[r][1]);
-            m[rt][r] = M[rt][r];
-          } else {
-            // the sum is the lane's own: its two keys of each piece
-            const float xmax = fmaxf(x[0], x[1]);
-            if (xmax > m[rt][r] + kLazy) {
-              l[rt][r] *= ex2(m[rt][r] - xmax);
-              m[rt][r] = xmax;
-            }
-            const float mu = m[rt][r] == -INFINITY ? 0.f : m[rt][r];
-            l[rt][r] += ex2(x[0] - mu) + ex2(x[1] - mu);
-          }
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          over |= fmaxf(y[r][0], y[r][1]) > M[rt][r] + kLazy;
+          if (Q8) over |= fmaxf(x[r][0], x[r][1]) > m[rt][r] + kLazy;
+        }
+        // The maxima are looked for (over the row's lanes) only when a score
+        // passes one by more than 2^8: rarely after the first chunks.
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[rt][i][r] *= alpha;
-              o[rt][i][2 + r] *= alpha;
+          for (int r = 0; r < 2; ++r) {
+            const float ymax = lanes_max(fmaxf(y[r][0], y[r][1]));
+            if (ymax > M[rt][r] + kLazy) {
+              const float alpha = ex2(M[rt][r] - ymax);
+              M[rt][r] = ymax;
+              if (!Q8) l[rt][r] *= alpha;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[rt][i][r] *= alpha;
+                o[rt][i][2 + r] *= alpha;
+              }
             }
+            if (Q8) {
+              const float xmax = fmaxf(x[r][0], x[r][1]);  // the lane's own sum
+              if (xmax > m[rt][r] + kLazy) {
+                l[rt][r] *= ex2(m[rt][r] - xmax);
+                m[rt][r] = xmax;
+              }
+            }
+          }
+        }
+        float e[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float Mu = M[rt][r] == -INFINITY ? 0.f : M[rt][r] - (Q8 ? kLift : 0.f);
+          e[r][0] = ex2(y[r][0] - Mu);
+          e[r][1] = ex2(y[r][1] - Mu);
+          if (Q8) {
+            const float mu = m[rt][r] == -INFINITY ? 0.f : m[rt][r];
+            l[rt][r] += ex2(x[r][0] - mu) + ex2(x[r][1] - mu);
+          } else {
+            l[rt][r] += e[r][0] + e[r][1];
           }
         }
 #pragma unroll
@@ -532,9 +555,9 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float mq = Q8 ? lanes_max(m[rt][r]) : m[rt][r];
+        const float mq = Q8 ? lanes_max(m[rt][r]) : M[rt][r];
         const float mu = mq == -INFINITY ? 0.f : mq;
-        const float lq = lanes_sum(l[rt][r] * ex2(m[rt][r] - mu));
+        const float lq = lanes_sum(Q8 ? l[rt][r] * ex2(m[rt][r] - mu) : l[rt][r]);
         if (g == 0) ml[w * L::ROWS + 8 * rt + 2 * c + r] = make_float2(mq, lq);
       }
     meet();
@@ -569,53 +592,45 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
           o[rt][i][2 + r] = o[rt][i][2 + r] * a * a;
         }
       }
+    // Column tile i, element hi of lane g goes to place 8 (2 i + hi) + g of a
+    // row (with rows 2c turned by 8 c places: 32 banks); the place of a
+    // column is its own for bf16, element x of lane g's piece for 8 bits.
 #pragma unroll
     for (int pass = 0; pass < D / L::CW; ++pass) {
-      const int lo = pass * L::CW;
+      constexpr int IW = L::CW / 16;  // column tiles of a pass
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < IW; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int hi = e >> 1, row = 8 * rt + 2 * c + (e & 1);
-            int col;
-            if (!Q8) {
-              col = 16 * i + 8 * hi + g;
-            } else if (D == 128) {
-              col = 16 * ((g >> 1) + 4 * (g & 1)) + 2 * i + hi;
-            } else {
-              col = 8 * ((g & 1) + 4 * ((g >> 1) & 1) + 2 * (g >> 2)) + 2 * i + hi;
-            }
-            if (col >= lo && col < lo + L::CW)
-              sum[(w * L::ROWS + row) * L::CW + ((col - lo) ^ (8 * ((row >> 1) & 3)))] = o[rt][i][e];
+            const int row = 8 * rt + 2 * c + (e & 1), at = 8 * (2 * i + (e >> 1)) + g;
+            sum[(w * L::ROWS + row) * L::CW + (at ^ (8 * c))] = o[rt][pass * IW + i][e];
           }
       meet();
-      constexpr int TPR = L::CW / 4;  // threads per row, four columns each
-      for (int x = tid; x < L::ROWS * TPR; x += 32 * L::NC) {
-        const int row = x / TPR, col = 4 * (x % TPR);
+#pragma unroll 1
+      for (int x = tid; x < L::ROWS * L::CW; x += 32 * L::NC) {
+        const int row = x / L::CW, at = x % L::CW;
         if (row >= p.rows) break;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float v = 0.f;
 #pragma unroll
-        for (int i = 0; i < L::NC; ++i) {
-          const float4 y = *reinterpret_cast<const float4*>(
-              &sum[(i * L::ROWS + row) * L::CW + (col ^ (8 * ((row >> 1) & 3)))]);
-          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-        }
+        for (int i = 0; i < L::NC; ++i)
+          v += sum[(i * L::ROWS + row) * L::CW + (at ^ (8 * ((row >> 1) & 3)))];
+        const int el = 2 * pass * IW + (at >> 3), gl = at & 7;
+        const int col = !Q8        ? 8 * el + gl
+                        : D == 128 ? 16 * ((gl >> 1) + 4 * (gl & 1)) + el
+                                   : 8 * ((gl & 1) + 4 * ((gl >> 1) & 1) + 2 * (gl >> 2)) + el;
         const bool valid = row % p.T < it.s.nd;
         const float2 f = fin[row];
         if (whole) {
           const bool has = valid && !(f.y == 0.f);  // a NaN sum stays one
-          const float inv = has ? 1.f / f.y : 0.f;
-          uint2 out = make_uint2(0, 0);
-          if (has)
-            out = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (orow0 + row) * D + lo + col) = out;
-          if (pass == 0 && col == 0)
+          static_cast<uint16_t*>(p.o)[(orow0 + row) * D + col] =
+              has ? static_cast<uint16_t>(pack_bf16(v / f.y, 0.f)) : 0;
+          if (pass == 0 && at == 0)
             p.lse[orow0 + row] = has ? (f.x + lg2(f.y)) * kLn2 : -INFINITY;
         } else {
-          *reinterpret_cast<float4*>(p.part_o + (prow0 + row) * D + lo + col) = v;
-          if (pass == 0 && col == 0)
+          p.part_o[(prow0 + row) * D + col] = v;
+          if (pass == 0 && at == 0)
             p.part_ml[prow0 + row] = make_float2(valid ? f.x : -INFINITY, valid ? f.y : 0.f);
         }
       }
