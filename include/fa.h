@@ -304,7 +304,7 @@ fa_status fa_blocksparse_backward(const void* q, const void* k, const void* v, c
  *                 one packed [B, N, H + 2 Hkv, d] projection.
  * rot: a multiple of 16 in [16, d] (else FA_ERR_UNSUPPORTED); eps finite and
  * > 0; wq, wk, cos, sin 16-byte aligned.  Outputs must not overlap inputs.
- * Hkv need not divide H.
+ * Hkv need not divide H; B*N*(H + Hkv) < 2^31.
  */
 fa_status fa_qk_norm_rope(const void* q, const void* k, const float* wq, const float* wk,
                           const float* cos, const float* sin, const int* positions, void* q_out,

@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
     uint4 x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      x[u] = row[u] >= 0 ? *reinterpret_cast<const uint4*>(x0 + (n0 + u * RPW) * s.n)
-                         : make_uint4(0, 0, 0, 0);
+      x[u] = n0 + u * RPW < count ? *reinterpret_cast<const uint4*>(x0 + (n0 + u * RPW) * s.n)
+                                  : make_uint4(0, 0, 0, 0);  // does not wait for the page
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (FMT == kCacheBf16) {
@@ -140,13 +140,13 @@ template <int D, int FMT, bool WRITE>
 cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   constexpr int RPW = 32 / (D / 8);
   // Short rows of tokens (a decode step): one warp per (sequence, k or v,
-  // head).  Long ones: 8 warps of four rows in flight per lane.
+  // head).  Long ones: 8 warps of eight rows in flight per lane.
   const bool wide = p.N > 8 * RPW;
-  const int warps = wide ? 8 : (p.N + RPW - 1) / RPW, per = warps * RPW * (wide ? 4 : 1);
+  const int warps = wide ? 8 : (p.N + RPW - 1) / RPW, per = warps * RPW * (wide ? 8 : 1);
   const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N + per - 1) / per);
   if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(warps * 32);
-  return wide ? launch_pdl(fa_cache_kernel<D, FMT, WRITE, 4>, grid, block, 0, stream, p)
+  return wide ? launch_pdl(fa_cache_kernel<D, FMT, WRITE, 8>, grid, block, 0, stream, p)
               : launch_pdl(fa_cache_kernel<D, FMT, WRITE, 1>, grid, block, 0, stream, p);
 }
 

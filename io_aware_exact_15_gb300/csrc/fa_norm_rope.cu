@@ -139,20 +139,21 @@ FA_DEV void load_weights(const float* w, int e0, float (&x)[8]) {
   x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// One warp = one token x one group of U * RPW heads of q or of k; all loads
-// of the group are in flight together.
+// One block = eight consecutive tokens (a warp each) x one group of U * RPW
+// heads of q or of k: reads run along a token's heads, writes along a head's
+// tokens, both in pieces of 2 KB (d = 128).  All loads of a warp are in
+// flight together.
 template <int D, bool INTER, int U>
 __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopeParams p) {
   grid_dep_wait();  // the previous kernel's writes are visible from here on
   grid_dep_launch();
   constexpr int LPR = D / 8, RPW = 32 / LPR, GRP = U * RPW;
   const int lane = threadIdx.x & 31, e0 = 8 * (lane % LPR), sub = lane / LPR;
-  const int nq = (p.H + GRP - 1) / GRP, nk = (p.Hkv + GRP - 1) / GRP;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const long long token = unit / (nq + nk);
-  const int group = static_cast<int>(unit - token * (nq + nk));
-  if (token >= static_cast<long long>(p.B) * p.N) return;
-  const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(b) * p.N);
+  const uint32_t nq = (p.H + GRP - 1) / GRP, groups = nq + (p.Hkv + GRP - 1) / GRP;
+  const uint32_t block = blockIdx.x / groups, group = blockIdx.x - block * groups;
+  const uint32_t token = block * kWarps + (threadIdx.x >> 5);
+  if (token >= static_cast<uint32_t>(p.B) * p.N) return;
+  const int b = token / p.N, n = token - static_cast<uint32_t>(b) * p.N;
   const bool isq = group < nq;
   const int h0 = (isq ? group : group - nq) * GRP, H = isq ? p.H : p.Hkv;
   const Strides s = isq ? p.sq : p.sk;
@@ -185,83 +186,112 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopePar
   }
 }
 
-// The units (token x group of heads) of q or of k, dealt round-robin to the
-// grid's warps; dw of a warp's rows is summed in registers over its units.
+// Backward of U rows per lane group: acc += G xh, the rows' gradients are
+// written to d0 (+ h * sh).
 template <int D, bool INTER, int U>
-FA_DEV void norm_rope_back_rows(const RopeParams& p, bool isq, float (&acc)[8]) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, GRP = U * RPW;
-  const int lane = threadIdx.x & 31, e0 = 8 * (lane % LPR), sub = lane / LPR;
-  const int H = isq ? p.H : p.Hkv, groups = (H + GRP - 1) / GRP;
-  const long long units = static_cast<long long>(p.B) * p.N * groups;
-  const Strides s = isq ? p.sq : p.sk, sd = isq ? p.sdq : p.sdk;
-  const uint16_t* x0 = static_cast<const uint16_t*>(isq ? p.q : p.k) + e0;
-  const uint16_t* g0 = static_cast<const uint16_t*>(isq ? p.gq : p.gk) + e0;
-  uint16_t* d0 = static_cast<uint16_t*>(isq ? p.dq : p.dk) + e0;
+FA_DEV void norm_rope_back_rows(const uint4 (&rx)[U], const uint4 (&rg)[U], const float* weights,
+                                const Turn<D, INTER>& turn, float eps, uint16_t* d0, long long sh,
+                                int h0, int H, float (&acc)[8]) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
   float w[8];
-  load_weights(isq ? p.wq : p.wk, e0, w);
-#pragma unroll 1
-  for (long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-       unit < units; unit += static_cast<long long>(gridDim.x) * kWarps) {
-    const long long token = unit / groups;
-    const int h0 = static_cast<int>(unit - token * groups) * GRP;
-    const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(b) * p.N);
-    uint4 rx[U], rg[U];
+  load_weights(weights, 8 * (lane % LPR), w);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * RPW + sub;
+    float x[8], g[8];
+    widen(rx[u], x);
+    widen(rg[u], g);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + eps);
+    turn.template apply<true>(g);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= r;
+      acc[i] = fmaf(g[i], x[i], acc[i]);  // rows past H hold zeros
+      g[i] *= w[i];
+      dot = fmaf(g[i], x[i], dot);
+    }
+    const float mean = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = r * (g[i] - x[i] * mean);
+    if (h < H) *reinterpret_cast<uint4*>(d0 + h * sh) = narrow(g);
+  }
+}
+
+// A warp takes whole tokens (dealt round-robin to the grid's warps) and walks
+// their heads U * RPW at a time, the next rows already on their way; the
+// sums of dw stay in registers until the end.
+template <int D, bool INTER, int U>
+__global__ void __launch_bounds__(kWarps * 32, 3) fa_norm_rope_back_kernel(const RopeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int LPR = D / 8, RPW = 32 / LPR, GRP = U * RPW;
+  __shared__ float sums[kWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e0 = 8 * (lane % LPR), sub = lane / LPR;
+  const int nq = (p.H + GRP - 1) / GRP, steps = nq + (p.Hkv + GRP - 1) / GRP;
+  const uint32_t tokens = static_cast<uint32_t>(p.B) * p.N, stride = gridDim.x * kWarps;
+  float acc[2][8] = {};
+  uint4 rx[U], rg[U];
+  auto fetch = [&](uint32_t token, int step) {
+    const int b = token / p.N, n = token - static_cast<uint32_t>(b) * p.N;
+    const bool isq = step < nq;
+    const int h0 = (isq ? step : step - nq) * GRP, H = isq ? p.H : p.Hkv;
+    const Strides s = isq ? p.sq : p.sk;
+    const uint16_t* x0 = static_cast<const uint16_t*>(isq ? p.q : p.k) + b * s.b + n * s.n + e0;
+    const uint16_t* g0 = static_cast<const uint16_t*>(isq ? p.gq : p.gk) +
+                         (static_cast<size_t>(b) * H * p.N + n) * D + e0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * RPW + sub;
       rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
       if (h < H) {
-        rx[u] = ld16(x0 + b * s.b + n * s.n + h * s.h);
-        rg[u] = ld16(g0 + ((static_cast<size_t>(b) * H + h) * p.N + n) * D);
+        rx[u] = ld16(x0 + h * s.h);
+        rg[u] = ld16(g0 + static_cast<size_t>(h) * p.N * D);
       }
     }
+  };
+  uint32_t token = blockIdx.x * kWarps + warp;
+  if (token < tokens) fetch(token, 0);
+  for (; token < tokens; token += stride) {
+    const int b = token / p.N, n = token - static_cast<uint32_t>(b) * p.N;
     Turn<D, INTER> turn;
     turn.load(p.t, b, n, p.N, lane);
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step) {
+      uint4 cx[U], cg[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RPW + sub;
-      float x[8], g[8];
-      widen(rx[u], x);
-      widen(rg[u], g);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-      turn.template apply<true>(g);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= r;
-        acc[i] = fmaf(g[i], x[i], acc[i]);  // rows past H hold zeros
-        g[i] *= w[i];
-        dot = fmaf(g[i], x[i], dot);
-      }
-      const float mean = row_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = r * (g[i] - x[i] * mean);
-      if (h < H)
-        *reinterpret_cast<uint4*>(d0 + b * sd.b + n * sd.n + h * sd.h) = narrow(g);
+      for (int u = 0; u < U; ++u) cx[u] = rx[u], cg[u] = rg[u];
+      if (step + 1 < steps)
+        fetch(token, step + 1);
+      else if (tokens - token > stride)
+        fetch(token + stride, 0);
+      if (step < nq)
+        norm_rope_back_rows<D, INTER, U>(
+            cx, cg, p.wq, turn, p.eps,
+            static_cast<uint16_t*>(p.dq) + b * p.sdq.b + n * p.sdq.n + e0, p.sdq.h, step * GRP,
+            p.H, acc[0]);
+      else
+        norm_rope_back_rows<D, INTER, U>(
+            cx, cg, p.wk, turn, p.eps,
+            static_cast<uint16_t*>(p.dk) + b * p.sdk.b + n * p.sdk.n + e0, p.sdk.h,
+            (step - nq) * GRP, p.Hkv, acc[1]);
     }
   }
-}
-
-template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const RopeParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  constexpr int LPR = D / 8;
-  __shared__ float sums[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    norm_rope_back_rows<D, INTER, U>(p, kind == 0, acc);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      for (int o = LPR; o < 32; o <<= 1)
+        acc[kind][i] += __shfl_xor_sync(0xffffffffu, acc[kind][i], o);
     if (lane < LPR)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[warp][8 * lane + i] = acc[i];
+      for (int i = 0; i < 8; ++i) sums[warp][8 * lane + i] = acc[kind][i];
     __syncthreads();
     if (threadIdx.x < D) {
       float t = 0.f;
@@ -303,20 +333,19 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const long long tokens = static_cast<long long>(p.B) * p.N;
   const bool wide = tokens * (p.H + p.Hkv) >= 32LL * 1024;
   const int grp = wide ? 4 * RPW : RPW;
-  const long long units = tokens * ((p.H + grp - 1) / grp + (p.Hkv + grp - 1) / grp);
-  const dim3 grid(static_cast<unsigned>((units + kWarps - 1) / kWarps));
+  const long long groups = (p.H + grp - 1) / grp + (p.Hkv + grp - 1) / grp;
+  const dim3 grid(static_cast<unsigned>((tokens + kWarps - 1) / kWarps * groups));
   return wide ? launch_pdl(fa_norm_rope_kernel<D, INTER, 4>, grid, dim3(kWarps * 32), 0, stream, p)
               : launch_pdl(fa_norm_rope_kernel<D, INTER, 1>, grid, dim3(kWarps * 32), 0, stream, p);
 }
 
 template <int D, bool INTER>
 cudaError_t launch_rope_back(const RopeParams& p, float* dwq, float* dwk, cudaStream_t stream) {
-  constexpr int U = 2, RPW = 32 / (D / 8), GRP = U * RPW;
+  constexpr int U = 2;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const long long units = static_cast<long long>(p.B) * p.N * ((p.H + GRP - 1) / GRP);
-  long long blocks = (units + kWarps - 1) / kWarps;
-  if (blocks > 4LL * sms) blocks = 4LL * sms;
+  long long blocks = (static_cast<long long>(p.B) * p.N + kWarps - 1) / kWarps;
+  if (blocks > 3LL * sms) blocks = 3LL * sms;
   if (blocks > kMaxPartials) blocks = kMaxPartials;
   cudaError_t e = launch_pdl(fa_norm_rope_back_kernel<D, INTER, U>,
                              dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0, stream, p);
@@ -335,8 +364,8 @@ fa_status check_rope(const void* wq, const void* wk, const void* cos, const void
   if (table_rows < 1) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (rot < 16 || rot > d || rot % 16 != 0) return FA_ERR_UNSUPPORTED;
-  // one warp per token and group of at least two heads, eight warps per block
-  if (static_cast<long long>(B) * N > (1LL << 33) / (static_cast<long long>(H) + Hkv))
+  // tokens and blocks are counted in 31 bits
+  if (static_cast<long long>(B) * N >= (1LL << 31) / (static_cast<long long>(H) + Hkv))
     return FA_ERR_UNSUPPORTED;
   for (const void* p : {wq, wk, cos, sin}) FA_TRY(check_ptr16(p));
   if (positions) FA_TRY(check_ptr4(positions));

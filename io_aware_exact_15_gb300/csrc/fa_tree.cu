@@ -145,7 +145,7 @@ struct TreeSmem {
                        B_RE = B_RF + NR, B_SF = B_RE + NR, B_PF = B_SF + 2, B_OF = B_PF + 2,
                        B_X1 = B_OF + 1, B_X2 = B_X1 + 1, B_DONE = B_X2 + 1, NBAR = B_DONE + 1;
   static constexpr int RUN = BAR + NBAR * 8;    // Run
-  static constexpr int MISC = RUN + 24;
+  static constexpr int MISC = RUN + 32;
   static constexpr int ALLOC = MISC + 40 + 1024;  // + slack for 1024-byte alignment
   static constexpr int THREADS = 320 + (Q8 ? 32 * kConvWarps : 0);
   // tensor memory columns: S0, S1 (128 each), O0, O1 (D each)
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     float2* ml = reinterpret_cast<float2*>(smem + L::ML);
     PartIter it = tiles0.it;
     uint32_t g = 0, cnt = 0;
-    const uint32_t total = static_cast<uint32_t>(run.left);
+    const uint32_t total = run.left;
     int part = -1;
     bool ok = true, owe_x2 = false;
     while (ok && it.next(p)) {
@@ -706,6 +706,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(L::B_X2));
       }
     }
+    if (warp == 2 && lane == 0) note_join(p, run, it, blockIdx.x);
   } else if (L::Q8) {
     // ------------------------------------------------------ widening
     // 16 stored bytes per lane and step: two 8-byte loads, two 16-byte
@@ -770,57 +771,62 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
 }
 
 // Joins the parts of problems that more than one CTA worked on: one warp per
-// row.  O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts i.
+// row, one row of blocks per CTA of the main kernel, for the problem that
+// CTA began and did not end (its parts are its own last and the first ones
+// of the CTAs behind it).
+// O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts i.
 template <int D>
-__global__ void __launch_bounds__(256) fa_tree_join_kernel(const TreeParams p, int n) {
+__global__ void __launch_bounds__(256) fa_tree_join_kernel(const TreeParams p) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long gr = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (gr >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
-  const int bh = static_cast<int>(gr / p.rows), row = static_cast<int>(gr - static_cast<long long>(bh) * p.rows);
-  const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
-  const int grp = p.pair ? row / (2 * kTile) : 0, pr = row - grp * 2 * kTile * p.pair;
-  long long total, front;
-  unit_sums(p, b, lane, total, front);
-  if (n > total) n = static_cast<int>(total);
-  const int tiles = seq_len(p, b).tiles;
-  // CTA c has units [total c / n, total (c + 1) / n): unit u is in CTA
-  // ((u + 1) n - 1) / total
-  const long long u0 = front + static_cast<long long>(hkv * p.groups + grp) * tiles;
-  const int c0 = static_cast<int>(((u0 + 1) * n - 1) / total);
-  const int c1 = static_cast<int>(((u0 + tiles) * n - 1) / total);
-  if (c0 == c1) return;  // written by its CTA
-  // the first part starts the problem (slot 1 of its CTA), the others go on
-  auto at = [&](int c) {
-    return (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * p.slot_rows + pr;
+  const int lane = threadIdx.x & 31, c = blockIdx.y;
+  const int2 j = p.joins[c];
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int bh = j.x / p.groups, row = (j.x - bh * p.groups) * 2 * kTile + r;
+  if (j.y == 0 || r >= p.slot_rows || row >= p.rows) return;
+  auto at = [&](int i) {  // row of part i
+    return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.slot_rows + r;
   };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[at(c)].x);
+  float2 first = make_float2(-INFINITY, 0.f);  // part `lane`
+  if (lane < j.y) first = p.part_ml[at(lane)];
+  float M = first.x;
+  for (int i = 32 + lane; i < j.y; i += 32) M = fmaxf(M, p.part_ml[at(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float mu = M == -INFINITY ? 0.f : M;
   float l = 0.f, o[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 x = p.part_ml[at(c)];
-    const float a = ex2(x.x - mu);
-    l = fmaf(x.y, a, l);
-    const float* y = p.part_o + at(c) * D + lane * E;
-    float v[E];
-    if (E == 4)
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y);
-    else
-      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y);
+  for (int i0 = 0; i0 < j.y; i0 += 32) {
+    float2 x = first;
+    if (i0 > 0) {
+      x = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < j.y) x = p.part_ml[at(i0 + lane)];
+    }
     // a part in which the row saw nothing counts nothing, whatever it holds
+    const float a = x.y == 0.f ? 0.f : ex2(x.x - mu);
+    l = fmaf(x.y, a, l);  // summed over the lanes below
+    const uint32_t use = __ballot_sync(0xffffffffu, x.y != 0.f);
+    const int m = min(32, j.y - i0);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float ai = __shfl_sync(0xffffffffu, a, i);
+      const float* y = p.part_o + at(i0 + i) * D + lane * E;
+      float v[E];
+      if (E == 4)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y);
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = x.y == 0.f ? o[i] : fmaf(v[i], a, o[i]);
+      for (int k = 0; k < E; ++k) o[k] = (use >> i) & 1u ? fmaf(v[k], ai, o[k]) : o[k];
+    }
   }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
   const bool has = !(l == 0.f);
   const float inv = has ? 1.f / l : 0.f;
+  const size_t gr = static_cast<size_t>(bh) * p.rows + row;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + gr * D + lane * E);
 #pragma unroll
   for (int i = 0; i < E; i += 2) dst[i / 2] = has ? pack_bf16(o[i] * inv, o[i + 1] * inv) : 0u;
@@ -833,12 +839,13 @@ int slot_rows(int rows) {
   return rows < most ? rows : most;
 }
 
+constexpr size_t kJoinBytes = kMaxGrid * sizeof(int2);  // a multiple of 256
 size_t tree_ml_bytes(int rows) {
   return align256(2ull * kMaxGrid * slot_rows(rows) * sizeof(float2));
 }
 size_t tree_ws_bytes(int H, int Hkv, int T, int d) {
   const int rows = H / Hkv * T;
-  return tree_ml_bytes(rows) + align256(2ull * kMaxGrid * slot_rows(rows) * d * sizeof(float));
+  return kJoinBytes + tree_ml_bytes(rows) + align256(2ull * kMaxGrid * slot_rows(rows) * d * sizeof(float));
 }
 
 // Tiles of the longest sequence that the page table can hold.
@@ -857,10 +864,9 @@ int tree_grid(const TreeParams& p) {
 cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t stream) {
   // tables of one tile: every problem is one unit, nothing to join
   if (most_tiles(p) == 1) return cudaSuccess;
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.rows;
-  const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
-  return d == 64 ? launch_pdl(fa_tree_join_kernel<64>, blocks, dim3(256), 0, stream, p, grid)
-                 : launch_pdl(fa_tree_join_kernel<128>, blocks, dim3(256), 0, stream, p, grid);
+  const dim3 blocks((p.slot_rows + 7) / 8, grid);
+  return d == 64 ? launch_pdl(fa_tree_join_kernel<64>, blocks, dim3(256), 0, stream, p)
+                 : launch_pdl(fa_tree_join_kernel<128>, blocks, dim3(256), 0, stream, p);
 }
 
 template <int D, int FMT, bool PAIR>
@@ -937,8 +943,10 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.pair = p.rows > kTile ? 1 : 0;
   p.groups = p.pair ? (p.rows + 2 * kTile - 1) / (2 * kTile) : 1;
   p.slot_rows = slot_rows(p.rows);
-  p.part_ml = static_cast<float2*>(workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + tree_ml_bytes(p.rows));
+  char* ws = static_cast<char*>(workspace);
+  p.joins = reinterpret_cast<int2*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + kJoinBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kJoinBytes + tree_ml_bytes(p.rows));
   p.num_pages = num_pages;
   p.log_page = log2_page(page_size);
   p.max_pages = max_pages;
@@ -946,6 +954,8 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.scale = scale;
   p.err = err;
   p.wait_ns = wait_limit_ns();
+  if (static_cast<long long>(B) * Hkv * p.groups > (1LL << 31) / (most_tiles(p) + 1))
+    return FA_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
   if (p.rows <= kFewRows) {
     if (!make_cache_map(&tk, k_cache, num_pages * Hkv, page_size, d, format != kCacheBf16) ||

@@ -19,8 +19,13 @@ struct TreeParams {
   const uint32_t* mask;    // [B, T, words] or null
   void* o;                 // bf16 [B, H, T, d]
   float* lse;              // [B, H, T]
+  // Parts of problems that several CTAs work on.  CTA c has two places: 2 c
+  // for the part that begins its run inside a problem, 2 c + 1 for the one
+  // that ends it inside a problem begun there.
   float2* part_ml;         // [2 * grid][slot_rows] (max in log2 units, sum)
   float* part_o;           // [2 * grid][slot_rows][d]
+  int2* joins;             // [grid] the problem begun and not ended by CTA c
+                           // ((b * Hkv + head) * groups + group) and its parts, or 0 parts
   int B, Hkv, T, rows;     // rows = H / Hkv * T
   int groups, slot_rows;   // row groups per key/value head; rows of a part
   int pair;                // 256-row groups
@@ -45,60 +50,55 @@ FA_DEV SeqLen seq_len(const TreeParams& p, int b) {
   return s;
 }
 
-FA_DEV long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// (all sequences' units, units in front of sequence `before`); whole warp.
-FA_DEV void unit_sums(const TreeParams& p, int before, int lane, long long& total,
-                      long long& front) {
-  long long t = 0, f = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const long long u = static_cast<long long>(seq_len(p, b).tiles) * p.Hkv * p.groups;
-    t += u;
-    if (b < before) f += u;
-  }
-  total = warp_sum(t);
-  front = warp_sum(f);
+// Units of sequence b: its tiles for each key/value head and row group.  All
+// sequences together have less than 2^31 (checked on the host).
+FA_DEV uint32_t seq_units(const TreeParams& p, int b) {
+  return b < p.B ? static_cast<uint32_t>(seq_len(p, b).tiles) * (p.Hkv * p.groups) : 0u;
 }
 
 // A CTA's run of units.
 struct Run {
-  int b, hr, t;      // first unit: sequence, key/value head x group, tile
-  int pad;
-  long long left;    // units
+  int b, hr, t;         // first unit: sequence, key/value head x group, tile
+  uint32_t first, left; // its number, units
+  uint32_t total;       // units of all sequences
+  int n;                // CTAs that have some
 };
 
-// Run of CTA c of n: units [U c / n, U (c + 1) / n), n at most U so that no
-// run between two others is empty.  Whole warp.
-FA_DEV Run find_run(const TreeParams& p, int c, int n, int lane) {
-  long long total, dummy;
-  unit_sums(p, 0, lane, total, dummy);
-  if (n > total) n = static_cast<int>(total);
-  if (c >= n) return Run{0, 0, 0, 0, 0};
-  const long long u0 = total * c / n, u1 = total * (c + 1) / n;
-  Run r = {0, 0, 0, 0, u1 - u0};
-  long long base = 0;
+// First unit of CTA c of n: floor(total c / n).
+FA_DEV uint32_t run_begin(uint32_t total, uint32_t c, uint32_t n) {
+  const uint32_t q = total / n, r = total - q * n;
+  return q * c + r * c / n;
+}
+
+// Run of CTA c: with n = the grid's CTAs, or the units if there are fewer (no
+// run between two others is empty).  Whole warp.
+FA_DEV Run find_run(const TreeParams& p, int c, int grid, int lane) {
+  const uint32_t mine = seq_units(p, lane);  // the first 32 sequences
+  uint32_t total = __reduce_add_sync(0xffffffffu, mine);
+  for (int b0 = 32; b0 < p.B; b0 += 32)
+    total += __reduce_add_sync(0xffffffffu, seq_units(p, b0 + lane));
+  const int n = total < static_cast<uint32_t>(grid) ? static_cast<int>(total) : grid;
+  Run r = {0, 0, 0, 0, 0, total, n};
+  if (c >= n) return r;
+  r.first = run_begin(total, c, n);
+  r.left = run_begin(total, c + 1, n) - r.first;
+  uint32_t base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int tiles = b < p.B ? seq_len(p, b).tiles : 0;
-    const long long u = static_cast<long long>(tiles) * p.Hkv * p.groups;
-    long long incl = u;
+    const uint32_t u = b0 == 0 ? mine : seq_units(p, b0 + lane);
+    uint32_t incl = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > u0);
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > r.first);
     if (hit) {
       const int w = __ffs(hit) - 1;
-      const long long rem = __shfl_sync(0xffffffffu, u0 - (base + incl - u), w);
-      const int tw = __shfl_sync(0xffffffffu, tiles, w);
+      const uint32_t rem = __shfl_sync(0xffffffffu, r.first - (base + incl - u), w);
+      const uint32_t tiles = __shfl_sync(0xffffffffu, u, w) / (p.Hkv * p.groups);
       r.b = b0 + w;
-      r.hr = static_cast<int>(rem / tw);
-      r.t = static_cast<int>(rem - static_cast<long long>(r.hr) * tw);
+      r.hr = static_cast<int>(rem / tiles);
+      r.t = static_cast<int>(rem - r.hr * tiles);
       break;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -111,7 +111,7 @@ struct PartIter {
   SeqLen s;
   int b, hr, t0, t1;  // tiles [t0, t1) of problem (b, hr)
   int next_t;
-  long long left;
+  uint32_t left;
   FA_DEV void init(const TreeParams& p, const Run& r) {
     b = r.b;
     hr = r.hr;
@@ -130,12 +130,26 @@ struct PartIter {
       }
     }
     t0 = next_t;
-    const int n = left < s.tiles - t0 ? static_cast<int>(left) : s.tiles - t0;
+    const int n = min(left, static_cast<uint32_t>(s.tiles - t0));
     t1 = next_t = t0 + n;
     left -= n;
     return true;
   }
 };
+
+// The problem that this CTA begins and does not end, for the second kernel;
+// `it` after the last part of the run (one thread; idle CTAs too, with no
+// part).
+FA_DEV void note_join(const TreeParams& p, const Run& r, const PartIter& it, int c) {
+  int2 j = make_int2(0, 0);
+  if (r.left > 0 && it.t0 == 0 && it.t1 < it.s.tiles) {
+    // unit u belongs to CTA floor(((u + 1) n - 1) / total)
+    const uint64_t last = static_cast<uint64_t>(r.first) + r.left + (it.s.tiles - it.t1) - 1;
+    const int c1 = static_cast<int>(((last + 1) * r.n - 1) / r.total);
+    j = make_int2(it.b * p.Hkv * p.groups + it.hr, c1 - c + 1);
+  }
+  p.joins[c] = j;
+}
 
 // The tiles of a run, in order.
 struct TileIter {

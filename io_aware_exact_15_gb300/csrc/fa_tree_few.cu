@@ -82,7 +82,7 @@ struct FewSmem {
   static constexpr int FIN = SC + (Q8 ? R * 256 : 0);     // (m, l) of the rows
   static constexpr int BAR = FIN + ROWS * 8;              // full, empty of each stage
   static constexpr int RUN = BAR + R * 16;
-  static constexpr int MISC = RUN + 24;                   // abort flag, bad parts
+  static constexpr int MISC = RUN + 32;                   // abort flag, bad parts
   static constexpr int ALLOC = MISC + 16 + 1024;          // + slack for 1024-byte alignment
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
@@ -213,7 +213,10 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
   }
   __syncthreads();
   const Run run = *run_slot;
-  if (run.left == 0) return;
+  if (run.left == 0) {
+    if (threadIdx.x == 0) note_join(p, run, PartIter(), blockIdx.x);
+    return;
+  }
   const WaitCtl wc{abort_flag, p.err, p.wait_ns};
 
   if (warp < L::NL) {
@@ -645,6 +648,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
                                whole ? nullptr : p.part_o + (prow0 + row) * D);
     }
   }
+  if (tid == 0) note_join(p, run, it, blockIdx.x);
 }
 
 template <int D, int FMT, int RT>
