@@ -18,6 +18,14 @@
 // cosines and sines once for all its rows.  The input strides are free (a
 // packed [B, N, heads, d] projection is read in place) and the result is
 // [B, H, N, d], which the attention entry points take.
+//
+// A warp takes whole tokens, eight consecutive ones to a block (so that each
+// head's rows are written in longer pieces), and walks their heads a few rows
+// at a time.  Loads go through a queue in shared memory (asynchronous
+// copies, each lane its own 16 bytes, so nothing has to be synchronised):
+// loads that wait in registers kept at most 64 KB of an SM in flight and
+// lost the time between a block's loads (39.0 us for 4 x 4096 tokens of 20
+// heads of 128, where a plain copy of the bytes takes 29.0).
 #include <math.h>
 #include <stdint.h>
 
@@ -33,6 +41,7 @@ namespace {
 
 constexpr int kWarps = 8;          // warps per block
 constexpr int kMaxPartials = 1024; // blocks of the backward, at most
+constexpr int kQueue = 4;          // steps of a warp on their way or in use
 
 struct RopeTables {
   const float* cos;
@@ -56,19 +65,26 @@ struct RopeParams {
   float eps;
 };
 
-FA_DEV uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
-
-FA_DEV void widen(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-  }
+// 8 bf16 elements as four fp32 pairs (exact), and back (one rounding)
+FA_DEV void widen(const uint4& v, uint64_t (&x)[4]) {
+  x[0] = f2_pack(bf16_lo(v.x), bf16_hi(v.x));
+  x[1] = f2_pack(bf16_lo(v.y), bf16_hi(v.y));
+  x[2] = f2_pack(bf16_lo(v.z), bf16_hi(v.z));
+  x[3] = f2_pack(bf16_lo(v.w), bf16_hi(v.w));
 }
-FA_DEV uint4 narrow(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                    pack_bf16(x[6], x[7]));
+FA_DEV uint32_t narrow(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return pack_bf16(a, b);
+}
+FA_DEV uint4 narrow(const uint64_t (&x)[4]) {
+  return make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
+}
+// sum of the products of two rows' pieces
+FA_DEV float dot8(const uint64_t (&x)[4], const uint64_t (&y)[4]) {
+  float a, b;
+  f2_unpack(f2_fma(x[3], y[3], f2_fma(x[2], y[2], f2_fma(x[1], y[1], f2_mul(x[0], y[0])))), a, b);
+  return a + b;
 }
 
 // sum over the LPR lanes of a row
@@ -79,219 +95,329 @@ FA_DEV float row_sum(float v) {
   return v;
 }
 
-// The angles of one lane's 8 elements.  Adjacent pairs: c, s hold 4 values.
-// Half pairs (i, i + rot / 2): 8 values, and the partner element sits `hop`
-// lanes away (rot is a multiple of 16, so a half is a whole number of lanes).
+FA_DEV void load8(const float* w, uint64_t (&x)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  x[0] = f2_pack(a.x, a.y);
+  x[1] = f2_pack(a.z, a.w);
+  x[2] = f2_pack(b.x, b.y);
+  x[3] = f2_pack(b.z, b.w);
+}
+
+// The rotation of one lane's 8 elements: y_i = c_i x_i + s_i x'_i, where x'
+// is the other element of the pair and s carries the sign.  Adjacent pairs:
+// x' is the neighbour in the same packed word.  Half pairs (i, i + rot / 2):
+// x' sits `hop` lanes away (rot is a multiple of 16, so a half is a whole
+// number of lanes).  Elements from `rot` on have c = 1, s = 0.
 template <int D, bool INTER>
 struct Turn {
-  float c[8], s[8];
+  uint64_t c[4], s[4];
   bool in, upper;
-  int partner;  // lane that holds the other half's elements
+  int partner;  // lane of x'
+  int other;    // first of the elements x' (to find their weights)
 
-  FA_DEV void load(const RopeTables& t, int b, int n, int N, int lane) {
+  FA_DEV Turn(int rot, int lane) {
     constexpr int LPR = D / 8;
-    const int l = lane % LPR, e0 = 8 * l, hop = t.rot / 16;
-    in = e0 < t.rot;
-    upper = !INTER && e0 >= t.rot / 2;
-    partner = in ? (upper ? lane - hop : lane + hop) : lane;
-    int pos = t.positions ? t.positions[static_cast<size_t>(b) * N + n] : n;
-    pos = min(max(pos, 0), t.rows - 1);
-    const size_t row = static_cast<size_t>(pos) * (t.rot / 2);
-    constexpr int V = INTER ? 1 : 2;
-    const int i0 = INTER ? e0 / 2 : (upper ? e0 - t.rot / 2 : e0);
+    const int e0 = 8 * (lane % LPR), hop = rot / 16;
+    in = e0 < rot;
+    upper = !INTER && e0 >= rot / 2;
+    partner = !in || INTER ? lane : upper ? lane - hop : lane + hop;
+    other = e0 + 8 * (partner - lane);
+  }
+
+  // from this lane's numbers of the tables: 8 cosines and 8 sines (adjacent
+  // pairs: 4 and 4), 16 bytes at a time, `pitch` bytes apart
+  template <bool BACK>
+  FA_DEV void load(uint32_t at, uint32_t pitch) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float4 a = make_float4(1.f, 1.f, 1.f, 1.f), z = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in) {
-        a = __ldg(reinterpret_cast<const float4*>(t.cos + row + i0) + v);
-        z = __ldg(reinterpret_cast<const float4*>(t.sin + row + i0) + v);
+    for (int i = 0; i < 4; ++i) c[i] = f2_pack(1.f, 1.f), s[i] = f2_pack(0.f, 0.f);
+    if (!in) return;
+    auto four = [&](int i, uint64_t& a, uint64_t& b) {
+      const uint4 v = ld_shared_v4(at + i * pitch);
+      a = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+      b = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
+    };
+    if (INTER) {
+      four(0, c[0], c[2]);
+      four(1, s[0], s[2]);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        float a, b;
+        f2_unpack(c[i], a, b);
+        c[i] = f2_pack(a, a), c[i + 1] = f2_pack(b, b);
+        f2_unpack(s[i], a, b);
+        if (BACK) a = -a, b = -b;
+        s[i] = f2_pack(-a, a), s[i + 1] = f2_pack(-b, b);
       }
-      c[4 * v] = a.x, c[4 * v + 1] = a.y, c[4 * v + 2] = a.z, c[4 * v + 3] = a.w;
-      s[4 * v] = z.x, s[4 * v + 1] = z.y, s[4 * v + 2] = z.z, s[4 * v + 3] = z.w;
+    } else {
+      four(0, c[0], c[1]);
+      four(1, c[2], c[3]);
+      four(2, s[0], s[1]);
+      four(3, s[2], s[3]);
+      if (upper == BACK) {  // a' = a c - b s in the lower half, b' = b c + a s
+        const uint64_t m = f2_pack(-1.f, -1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = f2_mul(s[i], m);
+      }
     }
   }
 
-  // y turned by the angles (BACK: against them); all lanes of the warp
-  template <bool BACK>
-  FA_DEV void apply(float (&y)[8]) const {
-    if (INTER) {
+  // x' of a packed piece; all lanes of the warp
+  FA_DEV uint4 swap(const uint4& v) const {
+    if (INTER)
+      return make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032),
+                        __byte_perm(v.z, 0, 0x1032), __byte_perm(v.w, 0, 0x1032));
+    return make_uint4(__shfl_sync(0xffffffffu, v.x, partner), __shfl_sync(0xffffffffu, v.y, partner),
+                      __shfl_sync(0xffffffffu, v.z, partner),
+                      __shfl_sync(0xffffffffu, v.w, partner));
+  }
+
+  // c, s times the weights of the element that each multiplies
+  FA_DEV void weigh(const float* w, int e0) {
+    uint64_t own[4], others[4];
+    load8(w + e0, own);
+    load8(w + other, others);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = y[2 * i], b = y[2 * i + 1], z = BACK ? -s[i] : s[i];
-        y[2 * i] = in ? a * c[i] - b * z : a;
-        y[2 * i + 1] = in ? b * c[i] + a * z : b;
+    for (int i = 0; i < 4; ++i) {
+      c[i] = f2_mul(c[i], own[i]);
+      if (INTER) {
+        float a, b;
+        f2_unpack(own[i], a, b);
+        others[i] = f2_pack(b, a);
       }
-    } else {
-      const bool minus = upper == BACK;  // lower half forward, upper half backward
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xffffffffu, y[i], partner);
-        y[i] = in ? y[i] * c[i] + (minus ? -o : o) * s[i] : y[i];
-      }
+      s[i] = f2_mul(s[i], others[i]);
     }
   }
 };
 
-FA_DEV void load_weights(const float* w, int e0, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + e0));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(w + e0) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+FA_DEV void copy16(uint32_t dst, const void* src, bool real) {
+  // no bytes are read, and zeros written, where `real` is false
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+FA_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+FA_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One block = eight consecutive tokens (a warp each) x one group of U * RPW
-// heads of q or of k: reads run along a token's heads, writes along a head's
-// tokens, both in pieces of 2 KB (d = 128).  All loads of a warp are in
-// flight together.
+// Where a warp is in its tokens: token, its place (b, n), and the step (group
+// of U * RPW heads, of q first).
+struct Walk {
+  uint32_t token;
+  int b, n, step;
+  FA_DEV void place(const RopeParams& p) {
+    b = token / p.N;
+    n = token - static_cast<uint32_t>(b) * p.N;
+  }
+};
+
+// The queue of a warp: kQueue steps of x (and, backward, of the gradient), and
+// the numbers of the tables of the last two tokens.
+template <int D, bool INTER, bool BACK, int U>
+struct Queue {
+  static constexpr int LPR = D / 8, RPW = 32 / LPR, GRP = U * RPW;
+  static constexpr int PIECES = U * (BACK ? 2 : 1);
+  static constexpr int TAB = INTER ? 2 : 4;
+  static constexpr int BYTES = (kQueue * PIECES + 2 * TAB) * 512;  // of a warp
+  const RopeParams& p;
+  uint32_t at;     // shared memory of this lane
+  int nq, steps, lane, e0, sub;
+  uint32_t tokens, stride;
+  Walk next;       // step to send
+  uint32_t sent = 0, turn = 0;
+  int pos_next;    // position of the next token to send
+
+  FA_DEV int position(uint32_t token) const {
+    if (token >= tokens) return 0;
+    return p.t.positions ? __ldg(p.t.positions + token)
+                         : static_cast<int>(token % static_cast<uint32_t>(p.N));
+  }
+
+  FA_DEV Queue(const RopeParams& p_, uint32_t smem) : p(p_) {
+    lane = threadIdx.x & 31;
+    at = smem + (threadIdx.x >> 5) * BYTES + lane * 16;
+    e0 = 8 * (lane % LPR);
+    sub = lane / LPR;
+    nq = (p.H + GRP - 1) / GRP;
+    steps = nq + (p.Hkv + GRP - 1) / GRP;
+    tokens = static_cast<uint32_t>(p.B) * p.N;
+    stride = gridDim.x * kWarps;
+    next.token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    next.step = 0;
+    if (next.token < tokens) next.place(p);
+    pos_next = position(next.token);
+#pragma unroll 1
+    for (int i = 0; i < kQueue - 1; ++i) send();
+  }
+
+  FA_DEV uint32_t piece(uint32_t step, int i) const {
+    return at + ((step % kQueue) * PIECES + i) * 512;
+  }
+  FA_DEV uint32_t tables(uint32_t t) const { return at + (kQueue * PIECES + (t & 1) * TAB) * 512; }
+
+  // sends one step (or an empty one behind the last)
+  FA_DEV void send() {
+    if (next.token < tokens) {
+      if (next.step == 0) {
+        const int pos = min(max(pos_next, 0), p.t.rows - 1);
+        pos_next = position(tokens - next.token > stride ? next.token + stride : tokens);
+        if (e0 < p.t.rot) {
+          const size_t row = static_cast<size_t>(pos) * (p.t.rot / 2);
+          const int i0 = INTER ? e0 / 2 : e0 >= p.t.rot / 2 ? e0 - p.t.rot / 2 : e0;
+#pragma unroll
+          for (int i = 0; i < TAB / 2; ++i) {
+            copy16(tables(turn) + i * 512, p.t.cos + row + i0 + 4 * i, true);
+            copy16(tables(turn) + (TAB / 2 + i) * 512, p.t.sin + row + i0 + 4 * i, true);
+          }
+        }
+        ++turn;
+      }
+      const bool isq = next.step < nq;
+      const int h0 = (isq ? next.step : next.step - nq) * GRP, H = isq ? p.H : p.Hkv;
+      const Strides s = isq ? p.sq : p.sk;
+      const uint16_t* x0 =
+          static_cast<const uint16_t*>(isq ? p.q : p.k) + next.b * s.b + next.n * s.n + e0;
+      const uint16_t* g0 = static_cast<const uint16_t*>(isq ? p.gq : p.gk) +
+                           (static_cast<size_t>(next.b) * H * p.N + next.n) * D + e0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * RPW + sub;
+        const bool real = h < H;
+        copy16(piece(sent, u), x0 + (real ? h : 0) * s.h, real);
+        if (BACK)
+          copy16(piece(sent, U + u), g0 + static_cast<size_t>(real ? h : 0) * p.N * D, real);
+      }
+      if (++next.step == steps) {
+        next.step = 0;
+        // (the sum stays below 2^32: tokens and grid are far smaller)
+        next.token += stride;
+        if (next.token < tokens) next.place(p);
+      }
+    }
+    ++sent;
+    copy_commit();
+  }
+  FA_DEV uint4 take(uint32_t step, int i) const { return ld_shared_v4(piece(step, i)); }
+};
+
 template <int D, bool INTER, int U>
 __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopeParams p) {
   grid_dep_wait();  // the previous kernel's writes are visible from here on
   grid_dep_launch();
-  constexpr int LPR = D / 8, RPW = 32 / LPR, GRP = U * RPW;
-  const int lane = threadIdx.x & 31, e0 = 8 * (lane % LPR), sub = lane / LPR;
-  const uint32_t nq = (p.H + GRP - 1) / GRP, groups = nq + (p.Hkv + GRP - 1) / GRP;
-  const uint32_t block = blockIdx.x / groups, group = blockIdx.x - block * groups;
-  const uint32_t token = block * kWarps + (threadIdx.x >> 5);
-  if (token >= static_cast<uint32_t>(p.B) * p.N) return;
-  const int b = token / p.N, n = token - static_cast<uint32_t>(b) * p.N;
-  const bool isq = group < nq;
-  const int h0 = (isq ? group : group - nq) * GRP, H = isq ? p.H : p.Hkv;
-  const Strides s = isq ? p.sq : p.sk;
-  const uint16_t* x0 = static_cast<const uint16_t*>(isq ? p.q : p.k) + b * s.b + n * s.n + e0;
-  uint16_t* o0 = static_cast<uint16_t*>(isq ? p.oq : p.ok) +
-                 (static_cast<size_t>(b) * H * p.N + n) * D + e0;
-  uint4 raw[U];
+  using Q = Queue<D, INTER, false, U>;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  Q q(p, smem_u32(rope_smem));
+  Turn<D, INTER> turn(p.t.rot, q.lane);
+  Walk w;
+  w.token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  uint32_t step = 0, token_no = 0;
+  for (; w.token < q.tokens; w.token += q.stride, ++token_no) {
+    w.place(p);
+#pragma unroll 1
+    for (w.step = 0; w.step < q.steps; ++w.step, ++step) {
+      q.send();
+      copy_wait<kQueue - 1>();  // this step has come
+      const bool isq = w.step < q.nq;
+      // the weights go into the rotation's factors: out = r (c w x + s w' x')
+      if (w.step == 0 || w.step == q.nq) {
+        turn.template load<false>(q.tables(token_no), 512);
+        turn.weigh(isq ? p.wq : p.wk, q.e0);
+      }
+      const int h0 = (isq ? w.step : w.step - q.nq) * Q::GRP, H = isq ? p.H : p.Hkv;
+      uint16_t* o0 = static_cast<uint16_t*>(isq ? p.oq : p.ok) +
+                     (static_cast<size_t>(w.b) * H * p.N + w.n) * D + q.e0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RPW + sub;
-    raw[u] = h < H ? ld16(x0 + h * s.h) : make_uint4(0, 0, 0, 0);
-  }
-  Turn<D, INTER> turn;
-  turn.load(p.t, b, n, p.N, lane);
-  float w[8];
-  load_weights(isq ? p.wq : p.wk, e0, w);
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * Q::RPW + q.sub;
+        const uint4 raw = q.take(step, u);
+        uint64_t x[4], y[4];
+        widen(raw, x);
+        widen(turn.swap(raw), y);
+        const float r = rsqrtf(row_sum<Q::LPR>(dot8(x, x)) * (1.f / D) + p.eps);
+        const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RPW + sub;
-    float x[8];
-    widen(raw[u], x);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-    turn.template apply<false>(x);
-    if (h < H) *reinterpret_cast<uint4*>(o0 + static_cast<size_t>(h) * p.N * D) = narrow(x);
-  }
-}
-
-// Backward of U rows per lane group: acc += G xh, the rows' gradients are
-// written to d0 (+ h * sh).
-template <int D, bool INTER, int U>
-FA_DEV void norm_rope_back_rows(const uint4 (&rx)[U], const uint4 (&rg)[U], const float* weights,
-                                const Turn<D, INTER>& turn, float eps, uint16_t* d0, long long sh,
-                                int h0, int H, float (&acc)[8]) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, sub = lane / LPR;
-  float w[8];
-  load_weights(weights, 8 * (lane % LPR), w);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RPW + sub;
-    float x[8], g[8];
-    widen(rx[u], x);
-    widen(rg[u], g);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + eps);
-    turn.template apply<true>(g);
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] *= r;
-      acc[i] = fmaf(g[i], x[i], acc[i]);  // rows past H hold zeros
-      g[i] *= w[i];
-      dot = fmaf(g[i], x[i], dot);
-    }
-    const float mean = row_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = r * (g[i] - x[i] * mean);
-    if (h < H) *reinterpret_cast<uint4*>(d0 + h * sh) = narrow(g);
-  }
-}
-
-// A warp takes whole tokens (dealt round-robin to the grid's warps) and walks
-// their heads U * RPW at a time, the next rows already on their way; the
-// sums of dw stay in registers until the end.
-template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kWarps * 32, 3) fa_norm_rope_back_kernel(const RopeParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  constexpr int LPR = D / 8, RPW = 32 / LPR, GRP = U * RPW;
-  __shared__ float sums[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e0 = 8 * (lane % LPR), sub = lane / LPR;
-  const int nq = (p.H + GRP - 1) / GRP, steps = nq + (p.Hkv + GRP - 1) / GRP;
-  const uint32_t tokens = static_cast<uint32_t>(p.B) * p.N, stride = gridDim.x * kWarps;
-  float acc[2][8] = {};
-  uint4 rx[U], rg[U];
-  auto fetch = [&](uint32_t token, int step) {
-    const int b = token / p.N, n = token - static_cast<uint32_t>(b) * p.N;
-    const bool isq = step < nq;
-    const int h0 = (isq ? step : step - nq) * GRP, H = isq ? p.H : p.Hkv;
-    const Strides s = isq ? p.sq : p.sk;
-    const uint16_t* x0 = static_cast<const uint16_t*>(isq ? p.q : p.k) + b * s.b + n * s.n + e0;
-    const uint16_t* g0 = static_cast<const uint16_t*>(isq ? p.gq : p.gk) +
-                         (static_cast<size_t>(b) * H * p.N + n) * D + e0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RPW + sub;
-      rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
-      if (h < H) {
-        rx[u] = ld16(x0 + h * s.h);
-        rg[u] = ld16(g0 + static_cast<size_t>(h) * p.N * D);
+        for (int i = 0; i < 4; ++i)
+          x[i] = f2_mul(f2_fma(y[i], turn.s[i], f2_mul(x[i], turn.c[i])), r2);
+        if (h < H) *reinterpret_cast<uint4*>(o0 + static_cast<size_t>(h) * p.N * D) = narrow(x);
       }
     }
-  };
-  uint32_t token = blockIdx.x * kWarps + warp;
-  if (token < tokens) fetch(token, 0);
-  for (; token < tokens; token += stride) {
-    const int b = token / p.N, n = token - static_cast<uint32_t>(b) * p.N;
-    Turn<D, INTER> turn;
-    turn.load(p.t, b, n, p.N, lane);
-#pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
-      uint4 cx[U], cg[U];
+  }
+}
+
+template <int D, bool INTER, int U>
+__global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const RopeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  using Q = Queue<D, INTER, true, U>;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  __shared__ float sums[kWarps][D];
+  const int warp = threadIdx.x >> 5;
+  Q q(p, smem_u32(rope_smem));
+  Turn<D, INTER> turn(p.t.rot, q.lane);
+  Walk w;
+  w.token = blockIdx.x * kWarps + warp;
+  uint32_t step = 0, token_no = 0;
+  uint64_t acc[2][4] = {};  // dwq, dwk of this warp's rows: pairs of fp32 zeros
+  uint64_t weights[4];
+  auto rows = [&](uint64_t (&sum)[4], uint16_t* d0, long long sh, int h0, int H) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) cx[u] = rx[u], cg[u] = rg[u];
-      if (step + 1 < steps)
-        fetch(token, step + 1);
-      else if (tokens - token > stride)
-        fetch(token + stride, 0);
-      if (step < nq)
-        norm_rope_back_rows<D, INTER, U>(
-            cx, cg, p.wq, turn, p.eps,
-            static_cast<uint16_t*>(p.dq) + b * p.sdq.b + n * p.sdq.n + e0, p.sdq.h, step * GRP,
-            p.H, acc[0]);
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * Q::RPW + q.sub;
+      const uint4 rg = q.take(step, U + u);
+      uint64_t x[4], g[4], y[4];
+      widen(q.take(step, u), x);
+      widen(rg, g);
+      widen(turn.swap(rg), y);
+      const float r = rsqrtf(row_sum<Q::LPR>(dot8(x, x)) * (1.f / D) + p.eps);
+      const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g[i] = f2_fma(y[i], turn.s[i], f2_mul(g[i], turn.c[i]));  // G
+        x[i] = f2_mul(x[i], r2);                                  // xh
+        sum[i] = f2_fma(g[i], x[i], sum[i]);                      // rows past H hold zeros
+        g[i] = f2_mul(g[i], weights[i]);
+      }
+      const float mean = row_sum<Q::LPR>(dot8(g, x)) * (-1.f / D);
+      const uint64_t m2 = f2_pack(mean, mean);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = f2_mul(f2_fma(x[i], m2, g[i]), r2);
+      if (h < H) *reinterpret_cast<uint4*>(d0 + h * sh) = narrow(g);
+    }
+  };
+  for (; w.token < q.tokens; w.token += q.stride, ++token_no) {
+    w.place(p);
+#pragma unroll 1
+    for (w.step = 0; w.step < q.steps; ++w.step, ++step) {
+      q.send();
+      copy_wait<kQueue - 1>();  // this step has come
+      if (w.step == 0) {
+        turn.template load<true>(q.tables(token_no), 512);
+        load8(p.wq + q.e0, weights);
+      } else if (w.step == q.nq) {
+        load8(p.wk + q.e0, weights);
+      }
+      if (w.step < q.nq)
+        rows(acc[0], static_cast<uint16_t*>(p.dq) + w.b * p.sdq.b + w.n * p.sdq.n + q.e0, p.sdq.h,
+             w.step * Q::GRP, p.H);
       else
-        norm_rope_back_rows<D, INTER, U>(
-            cx, cg, p.wk, turn, p.eps,
-            static_cast<uint16_t*>(p.dk) + b * p.sdk.b + n * p.sdk.n + e0, p.sdk.h,
-            (step - nq) * GRP, p.Hkv, acc[1]);
+        rows(acc[1], static_cast<uint16_t*>(p.dk) + w.b * p.sdk.b + w.n * p.sdk.n + q.e0, p.sdk.h,
+             (w.step - q.nq) * Q::GRP, p.Hkv);
     }
   }
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(acc[kind][i], a[2 * i], a[2 * i + 1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1)
-        acc[kind][i] += __shfl_xor_sync(0xffffffffu, acc[kind][i], o);
-    if (lane < LPR)
+      for (int o = Q::LPR; o < 32; o <<= 1) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+    if (q.lane < Q::LPR)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[warp][8 * lane + i] = acc[kind][i];
+      for (int i = 0; i < 8; ++i) sums[warp][8 * q.lane + i] = a[i];
     __syncthreads();
     if (threadIdx.x < D) {
       float t = 0.f;
@@ -325,33 +451,44 @@ __global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* part
   }
 }
 
+// Blocks: a warp per token, at most as many as the SMs hold at once (0 on
+// error).
+int rope_grid(const RopeParams& p, int per_sm) {
+  const long long blocks = (static_cast<long long>(p.B) * p.N + kWarps - 1) / kWarps;
+  const long long most = static_cast<long long>(per_sm) * sm_count();
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
 template <int D, bool INTER>
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
-  constexpr int RPW = 32 / (D / 8);
-  // Few tokens: one row per lane group, so that the heads of a token spread
-  // over as many warps as there are.  Many: four rows in flight per lane.
-  const long long tokens = static_cast<long long>(p.B) * p.N;
-  const bool wide = tokens * (p.H + p.Hkv) >= 32LL * 1024;
-  const int grp = wide ? 4 * RPW : RPW;
-  const long long groups = (p.H + grp - 1) / grp + (p.Hkv + grp - 1) / grp;
-  const dim3 grid(static_cast<unsigned>((tokens + kWarps - 1) / kWarps * groups));
-  return wide ? launch_pdl(fa_norm_rope_kernel<D, INTER, 4>, grid, dim3(kWarps * 32), 0, stream, p)
-              : launch_pdl(fa_norm_rope_kernel<D, INTER, 1>, grid, dim3(kWarps * 32), 0, stream, p);
+  constexpr int U = 4;
+  constexpr int bytes = kWarps * Queue<D, INTER, false, U>::BYTES;
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = smem_attr_once(
+      attr_done, reinterpret_cast<const void*>(fa_norm_rope_kernel<D, INTER, U>), bytes);
+  if (e != cudaSuccess) return e;
+  const int grid = rope_grid(p, 2);
+  if (grid <= 0) return cudaErrorInvalidDevice;
+  return launch_pdl(fa_norm_rope_kernel<D, INTER, U>, dim3(grid), dim3(kWarps * 32), bytes, stream,
+                    p);
 }
 
 template <int D, bool INTER>
 cudaError_t launch_rope_back(const RopeParams& p, float* dwq, float* dwk, cudaStream_t stream) {
   constexpr int U = 2;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  long long blocks = (static_cast<long long>(p.B) * p.N + kWarps - 1) / kWarps;
-  if (blocks > 3LL * sms) blocks = 3LL * sms;
-  if (blocks > kMaxPartials) blocks = kMaxPartials;
-  cudaError_t e = launch_pdl(fa_norm_rope_back_kernel<D, INTER, U>,
-                             dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0, stream, p);
+  constexpr int bytes = kWarps * Queue<D, INTER, true, U>::BYTES;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = smem_attr_once(
+      attr_done, reinterpret_cast<const void*>(fa_norm_rope_back_kernel<D, INTER, U>), bytes);
+  if (e != cudaSuccess) return e;
+  int grid = rope_grid(p, 2);
+  if (grid <= 0) return cudaErrorInvalidDevice;
+  if (grid > kMaxPartials) grid = kMaxPartials;
+  e = launch_pdl(fa_norm_rope_back_kernel<D, INTER, U>, dim3(grid), dim3(kWarps * 32), bytes,
+                 stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(fa_norm_rope_dw_kernel, dim3(2 * D / 32), dim3(1024), 0, stream,
-                    static_cast<const float*>(p.part), static_cast<int>(blocks), D, dwq, dwk);
+                    static_cast<const float*>(p.part), grid, D, dwq, dwk);
 }
 
 size_t rope_ws_bytes(int d) { return static_cast<size_t>(kMaxPartials) * 2 * d * sizeof(float); }
