@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kWarps = 8;          // warps per block
 constexpr int kMaxPartials = 1024; // blocks of the backward, at most
-constexpr int kQueue = 4;          // steps of a warp on their way or in use
+constexpr int kQueue = 3;          // steps of a warp on their way or in use
 
 struct RopeTables {
   const float* cos;
@@ -87,21 +87,31 @@ FA_DEV float dot8(const uint64_t (&x)[4], const uint64_t (&y)[4]) {
   return a + b;
 }
 
-// sum over the LPR lanes of a row
-template <int LPR>
-FA_DEV float row_sum(float v) {
+// sums over the LPR lanes of each of U rows (step by step for all of them:
+// one row's five exchanges are a chain of latencies)
+template <int LPR, int U>
+FA_DEV void row_sums(float (&v)[U]) {
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
 }
 
-FA_DEV void load8(const float* w, uint64_t (&x)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(w) + 1);
-  x[0] = f2_pack(a.x, a.y);
-  x[1] = f2_pack(a.z, a.w);
-  x[2] = f2_pack(b.x, b.y);
-  x[3] = f2_pack(b.z, b.w);
+// 8 fp32 numbers of shared memory as pairs
+FA_DEV void load8(uint32_t at, uint64_t (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = ld_shared_v4(at + 16 * i);
+    x[2 * i] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[2 * i + 1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+}
+
+// wq, wk into shared memory (whole block)
+template <int D>
+FA_DEV void stage_weights(float (&w)[2][D], const float* wq, const float* wk) {
+  for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) w[i / D][i % D] = i < D ? wq[i] : wk[i - D];
+  __syncthreads();
 }
 
 // The rotation of one lane's 8 elements: y_i = c_i x_i + s_i x'_i, where x'
@@ -173,10 +183,10 @@ struct Turn {
   }
 
   // c, s times the weights of the element that each multiplies
-  FA_DEV void weigh(const float* w, int e0) {
+  FA_DEV void weigh(uint32_t w, int e0) {
     uint64_t own[4], others[4];
-    load8(w + e0, own);
-    load8(w + other, others);
+    load8(w + 4 * e0, own);
+    load8(w + 4 * other, others);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       c[i] = f2_mul(c[i], own[i]);
@@ -308,7 +318,9 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopePar
   grid_dep_launch();
   using Q = Queue<D, INTER, false, U>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
+  __shared__ __align__(16) float weights[2][D];
   Q q(p, smem_u32(rope_smem));
+  stage_weights(weights, p.wq, p.wk);
   Turn<D, INTER> turn(p.t.rot, q.lane);
   Walk w;
   w.token = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -323,24 +335,32 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopePar
       // the weights go into the rotation's factors: out = r (c w x + s w' x')
       if (w.step == 0 || w.step == q.nq) {
         turn.template load<false>(q.tables(token_no), 512);
-        turn.weigh(isq ? p.wq : p.wk, q.e0);
+        turn.weigh(smem_u32(weights[isq ? 0 : 1]), q.e0);
       }
       const int h0 = (isq ? w.step : w.step - q.nq) * Q::GRP, H = isq ? p.H : p.Hkv;
       uint16_t* o0 = static_cast<uint16_t*>(isq ? p.oq : p.ok) +
                      (static_cast<size_t>(w.b) * H * p.N + w.n) * D + q.e0;
+      uint4 raw[U];
+      uint64_t x[U][4], y[U][4];
+      float r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = q.take(step, u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        widen(raw[u], x[u]);
+        r[u] = dot8(x[u], x[u]);
+        widen(turn.swap(raw[u]), y[u]);
+      }
+      row_sums<Q::LPR>(r);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = h0 + u * Q::RPW + q.sub;
-        const uint4 raw = q.take(step, u);
-        uint64_t x[4], y[4];
-        widen(raw, x);
-        widen(turn.swap(raw), y);
-        const float r = rsqrtf(row_sum<Q::LPR>(dot8(x, x)) * (1.f / D) + p.eps);
-        const uint64_t r2 = f2_pack(r, r);
+        r[u] = rsqrtf(r[u] * (1.f / D) + p.eps);
+        const uint64_t r2 = f2_pack(r[u], r[u]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          x[i] = f2_mul(f2_fma(y[i], turn.s[i], f2_mul(x[i], turn.c[i])), r2);
-        if (h < H) *reinterpret_cast<uint4*>(o0 + static_cast<size_t>(h) * p.N * D) = narrow(x);
+          x[u][i] = f2_mul(f2_fma(y[u][i], turn.s[i], f2_mul(x[u][i], turn.c[i])), r2);
+        if (h < H) *reinterpret_cast<uint4*>(o0 + static_cast<size_t>(h) * p.N * D) = narrow(x[u]);
       }
     }
   }
@@ -353,8 +373,10 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const Ro
   using Q = Queue<D, INTER, true, U>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   __shared__ float sums[kWarps][D];
+  __shared__ __align__(16) float staged[2][D];
   const int warp = threadIdx.x >> 5;
   Q q(p, smem_u32(rope_smem));
+  stage_weights(staged, p.wq, p.wk);
   Turn<D, INTER> turn(p.t.rot, q.lane);
   Walk w;
   w.token = blockIdx.x * kWarps + warp;
@@ -362,28 +384,42 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const Ro
   uint64_t acc[2][4] = {};  // dwq, dwk of this warp's rows: pairs of fp32 zeros
   uint64_t weights[4];
   auto rows = [&](uint64_t (&sum)[4], uint16_t* d0, long long sh, int h0, int H) {
+    uint4 rx[U], rg[U];
+    uint64_t x[U][4], g[U][4], y[4];
+    float r[U], mean[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) rx[u] = q.take(step, u), rg[u] = q.take(step, U + u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      widen(rx[u], x[u]);
+      r[u] = dot8(x[u], x[u]);
+      widen(rg[u], g[u]);
+      widen(turn.swap(rg[u]), y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        g[u][i] = f2_fma(y[i], turn.s[i], f2_mul(g[u][i], turn.c[i]));  // G
+    }
+    row_sums<Q::LPR>(r);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      r[u] = rsqrtf(r[u] * (1.f / D) + p.eps);
+      const uint64_t r2 = f2_pack(r[u], r[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[u][i] = f2_mul(x[u][i], r2);                // xh
+        sum[i] = f2_fma(g[u][i], x[u][i], sum[i]);    // rows past H hold zeros
+        g[u][i] = f2_mul(g[u][i], weights[i]);
+      }
+      mean[u] = dot8(g[u], x[u]) * (-1.f / D);
+    }
+    row_sums<Q::LPR>(mean);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * Q::RPW + q.sub;
-      const uint4 rg = q.take(step, U + u);
-      uint64_t x[4], g[4], y[4];
-      widen(q.take(step, u), x);
-      widen(rg, g);
-      widen(turn.swap(rg), y);
-      const float r = rsqrtf(row_sum<Q::LPR>(dot8(x, x)) * (1.f / D) + p.eps);
-      const uint64_t r2 = f2_pack(r, r);
+      const uint64_t r2 = f2_pack(r[u], r[u]), m2 = f2_pack(mean[u], mean[u]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        g[i] = f2_fma(y[i], turn.s[i], f2_mul(g[i], turn.c[i]));  // G
-        x[i] = f2_mul(x[i], r2);                                  // xh
-        sum[i] = f2_fma(g[i], x[i], sum[i]);                      // rows past H hold zeros
-        g[i] = f2_mul(g[i], weights[i]);
-      }
-      const float mean = row_sum<Q::LPR>(dot8(g, x)) * (-1.f / D);
-      const uint64_t m2 = f2_pack(mean, mean);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = f2_mul(f2_fma(x[i], m2, g[i]), r2);
-      if (h < H) *reinterpret_cast<uint4*>(d0 + h * sh) = narrow(g);
+      for (int i = 0; i < 4; ++i) g[u][i] = f2_mul(f2_fma(x[u][i], m2, g[u][i]), r2);
+      if (h < H) *reinterpret_cast<uint4*>(d0 + h * sh) = narrow(g[u]);
     }
   };
   for (; w.token < q.tokens; w.token += q.stride, ++token_no) {
@@ -394,9 +430,9 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const Ro
       copy_wait<kQueue - 1>();  // this step has come
       if (w.step == 0) {
         turn.template load<true>(q.tables(token_no), 512);
-        load8(p.wq + q.e0, weights);
+        load8(smem_u32(staged[0]) + 4 * q.e0, weights);
       } else if (w.step == q.nq) {
-        load8(p.wk + q.e0, weights);
+        load8(smem_u32(staged[1]) + 4 * q.e0, weights);
       }
       if (w.step < q.nq)
         rows(acc[0], static_cast<uint16_t*>(p.dq) + w.b * p.sdq.b + w.n * p.sdq.n + q.e0, p.sdq.h,
