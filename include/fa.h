@@ -349,13 +349,14 @@ fa_status fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const
  * Formats: FA_CACHE_BF16 keeps rows as they are.  FA_CACHE_E4M3 and
  * FA_CACHE_INT8 keep 8-bit numbers and one scale byte s per row (token,
  * head, key or value), the value being number * 2^(s - 127): the smallest
- * power of two that keeps the row within +-448 (+-127), at least 2^-117,
+ * power of two that keeps the row within +-448 (+-127), at least 2^-100,
  * then round to nearest, ties to even.  (The power is at most 2^119, 2^121,
  * where the largest number is still finite in bf16; larger values saturate.)  What reads back is exact in bf16,
  * and storing it again gives the same values, so tokens can be moved by
  * reading and appending them.  A row that holds a NaN or an infinity is
  * stored with s = 255 and reads back as NaN in all its elements.  The e4m3
- * code of NaN (0x7f, 0xff) is never written and does not read as NaN.
+ * code of NaN (0x7f, 0xff) is never written; what it stands for in a cache
+ * filled by other means is not specified.
  */
 typedef enum fa_cache_format {
   FA_CACHE_BF16 = 0,

@@ -338,6 +338,12 @@ FA_DEV uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// the same in fp16
+FA_DEV uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // elementwise product of two packed bf16x2 words, rounded once to bf16
 FA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;

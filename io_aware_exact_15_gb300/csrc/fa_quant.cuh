@@ -3,13 +3,13 @@
 //
 // A row x of d bf16 numbers is stored as rne(x 2^-e) with the smallest e
 // that keeps max|x| 2^-e within the type's largest number (448 or 127), at
-// least -117, and at most 119 (e4m3) or 121 (int8), where the largest number
+// least -100, and at most 119 (e4m3) or 121 (int8), where the largest number
 // is still finite in bf16: beyond (|x| > 2.97e38) it saturates.  The scale
 // byte is e + 127.  A power of two scales
 // without rounding, so there is one rounding per element, the same in any
 // precision, and what reads back is exact in bf16 (e4m3 has 4 significant
-// bits, int8 at most 7; e >= -117 keeps the smallest e4m3 number, 2^-9, at
-// 2^-126 or above).  Storing what was read back gives the same numbers
+// bits, int8 at most 7; e >= -100 keeps numbers and scales
+// far from the ends of fp32's range).  Storing what was read back gives the same numbers
 // again.  A row with a NaN or an infinity gets the scale byte 255 and reads
 // back as NaN whole.
 #pragma once
@@ -32,10 +32,10 @@ FA_DEV uint32_t row_scale(uint32_t amax) {
   if (amax >= 0x7F80u) return kScaleNan;
   const int ex = static_cast<int>(amax >> 7) - 127, frac = static_cast<int>(amax & 0x7Fu);
   const int e = FMT == kCacheE4m3 ? ex - 8 + (frac > 0x60) : ex - 6 + (frac > 0x7E);
-  return static_cast<uint32_t>(min(max(e, -117), FMT == kCacheE4m3 ? 119 : 121) + 127);
+  return static_cast<uint32_t>(min(max(e, -100), FMT == kCacheE4m3 ? 119 : 121) + 127);
 }
 
-// 2^-e for the scale byte e + 127 of row_scale (10 .. 248)
+// 2^-e for the scale byte e + 127 of row_scale (27 .. 248)
 FA_DEV float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
 // four fp32 numbers, already scaled, as four stored bytes (x0 lowest)
@@ -104,6 +104,33 @@ FA_DEV void widen4(uint32_t w, const RowScale& s, uint32_t& lo, uint32_t& hi) {
     hi = mul_bf16x2(sub_bf16x2((b & 0x007F007Fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u),
                     s.f1);
   }
+}
+
+// four stored bytes as f16 pairs (bytes 0, 1) and (2, 3), exact
+template <int FMT>
+FA_DEV void stored_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == kCacheE4m3) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // x + 128 under the exponent of 1024, less 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+  }
+}
+
+// 2^(byte - 127); NaN for the scale of a bad row
+FA_DEV float scale_value(uint32_t byte) {
+  return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(byte << 23);
+}
+// byte - 127: the byte as the last bits of 2^23, less 2^23 + 127
+FA_DEV float scale_exponent(uint32_t byte) {
+  return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu)
+                           : __uint_as_float(0x4B000000u | byte) - 8388735.f;
 }
 
 }  // namespace fa

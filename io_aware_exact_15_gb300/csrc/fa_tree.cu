@@ -934,6 +934,7 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.hist = hist_lens;
   p.drafts = draft_lens;
   p.mask = tree_mask;
+  p.q = q;
   p.o = o;
   p.lse = lse;
   p.B = B;
@@ -963,7 +964,7 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
       return FA_ERR_CUDA;
     const int grid = tree_grid(p);
     if (grid <= 0) return FA_ERR_CUDA;
-    FA_CUDA(launch_tree_few(p, format, d, q, tk, tv, grid, stream));
+    FA_CUDA(launch_tree_few(p, format, d, tk, tv, grid, stream));
     FA_CUDA(launch_join(p, d, grid, stream));
     return FA_OK;
   }

@@ -13,6 +13,7 @@ namespace fa {
 constexpr int kMaxGrid = 192;     // CTAs, at most (the workspace holds two parts of each)
 
 struct TreeParams {
+  const void* q;           // bf16 [B, H, T, d]
   const void *kc, *vc;     // caches [num_pages, Hkv, page, d]
   const uint8_t *ks, *vs;  // scale bytes [num_pages, Hkv, page]
   const int *page_table, *hist, *drafts;
@@ -243,8 +244,7 @@ static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, i
 // Few query rows (p.rows <= kFewRows): fa_tree_few.cu.  tk, tv: maps of
 // 16-row boxes (make_cache_map).
 constexpr int kFewRows = 32;
-cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const void* q,
-                            const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                            cudaStream_t stream);
+cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const CUtensorMap& tk,
+                            const CUtensorMap& tv, int grid, cudaStream_t stream);
 
 }  // namespace fa

@@ -119,39 +119,6 @@ FA_DEV uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-FA_DEV uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// four stored bytes as f16 pairs (bytes 0, 1) and (2, 3), exact
-template <int FMT>
-FA_DEV void stored_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (FMT == kCacheE4m3) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  } else {
-    // x + 128 under the exponent of 1024, less 1152
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-  }
-}
-
-// 2^(byte - 127); NaN for the scale of a bad row
-FA_DEV float scale_value(uint32_t byte) {
-  return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(byte << 23);
-}
-// byte - 127: the byte as the last bits of 2^23, less 2^23 + 127
-FA_DEV float scale_exponent(uint32_t byte) {
-  return byte == kScaleNan ? __uint_as_float(0x7FFFFFFFu)
-                           : __uint_as_float(0x4B000000u | byte) - 8388735.f;
-}
-
 FA_DEV uint32_t lds_u8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -178,7 +145,7 @@ FA_DEV float lanes_sum(float v) {
 template <int D, int FMT, int RT>
 __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
     fa_tree_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                       const void* q, const TreeParams p) {
+                       const TreeParams p) {
   using L = FewSmem<D, FMT, RT>;
   constexpr bool Q8 = L::Q8;
   constexpr int MT = D / 16;  // 16-column tiles of O
@@ -297,7 +264,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int row = 8 * rt + g;
-      const uint16_t* qrow = static_cast<const uint16_t*>(q) +
+      const uint16_t* qrow = static_cast<const uint16_t*>(p.q) +
                              ((static_cast<size_t>(it.b) * p.Hkv + it.hr) * p.rows + row) * D;
       // pieces of 16 bytes: bf16 keys pair with pieces c, c + 4 of each 64
       // elements; 8-bit keys have 16 elements to a piece, two of these
@@ -652,7 +619,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
 }
 
 template <int D, int FMT, int RT>
-cudaError_t launch_few_rows(const TreeParams& p, const void* q, const CUtensorMap& tk,
+cudaError_t launch_few_rows(const TreeParams& p, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream) {
   using L = FewSmem<D, FMT, RT>;
   static std::atomic<unsigned long long> attr_done{0};
@@ -660,33 +627,32 @@ cudaError_t launch_few_rows(const TreeParams& p, const void* q, const CUtensorMa
       attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, RT>), L::ALLOC);
   if (e != cudaSuccess) return e;
   return launch_pdl(fa_tree_few_kernel<D, FMT, RT>, dim3(grid), dim3(L::THREADS), L::ALLOC,
-                    stream, tk, tv, q, p);
+                    stream, tk, tv, p);
 }
 
 template <int D, int FMT>
-cudaError_t launch_few_fmt(const TreeParams& p, const void* q, const CUtensorMap& tk,
+cudaError_t launch_few_fmt(const TreeParams& p, const CUtensorMap& tk,
                            const CUtensorMap& tv, int grid, cudaStream_t stream) {
   switch ((p.rows + 7) / 8) {
-    case 1: return launch_few_rows<D, FMT, 1>(p, q, tk, tv, grid, stream);
-    case 2: return launch_few_rows<D, FMT, 2>(p, q, tk, tv, grid, stream);
-    case 3: return launch_few_rows<D, FMT, 3>(p, q, tk, tv, grid, stream);
-    case 4: return launch_few_rows<D, FMT, 4>(p, q, tk, tv, grid, stream);
+    case 1: return launch_few_rows<D, FMT, 1>(p, tk, tv, grid, stream);
+    case 2: return launch_few_rows<D, FMT, 2>(p, tk, tv, grid, stream);
+    case 3: return launch_few_rows<D, FMT, 3>(p, tk, tv, grid, stream);
+    case 4: return launch_few_rows<D, FMT, 4>(p, tk, tv, grid, stream);
   }
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const void* q,
-                            const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                            cudaStream_t stream) {
+cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const CUtensorMap& tk,
+                            const CUtensorMap& tv, int grid, cudaStream_t stream) {
   if (d == 64)
-    return format == kCacheBf16   ? launch_few_fmt<64, kCacheBf16>(p, q, tk, tv, grid, stream)
-           : format == kCacheE4m3 ? launch_few_fmt<64, kCacheE4m3>(p, q, tk, tv, grid, stream)
-                                  : launch_few_fmt<64, kCacheInt8>(p, q, tk, tv, grid, stream);
-  return format == kCacheBf16   ? launch_few_fmt<128, kCacheBf16>(p, q, tk, tv, grid, stream)
-         : format == kCacheE4m3 ? launch_few_fmt<128, kCacheE4m3>(p, q, tk, tv, grid, stream)
-                                : launch_few_fmt<128, kCacheInt8>(p, q, tk, tv, grid, stream);
+    return format == kCacheBf16   ? launch_few_fmt<64, kCacheBf16>(p, tk, tv, grid, stream)
+           : format == kCacheE4m3 ? launch_few_fmt<64, kCacheE4m3>(p, tk, tv, grid, stream)
+                                  : launch_few_fmt<64, kCacheInt8>(p, tk, tv, grid, stream);
+  return format == kCacheBf16   ? launch_few_fmt<128, kCacheBf16>(p, tk, tv, grid, stream)
+         : format == kCacheE4m3 ? launch_few_fmt<128, kCacheE4m3>(p, tk, tv, grid, stream)
+                                : launch_few_fmt<128, kCacheInt8>(p, tk, tv, grid, stream);
 }
 
 }  // namespace fa

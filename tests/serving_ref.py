@@ -64,10 +64,10 @@ def quantise(x, fmt):
     out = np.full_like(x, np.nan)
     ok = np.isfinite(x).all(-1)
     amax = np.abs(np.where(np.isfinite(x), x, 0)).max(-1)
-    e = np.full(amax.shape, -117)
+    e = np.full(amax.shape, -100)
     # the smallest exponent that holds the row, as far as the format's largest
     # number times it is finite in bf16
-    for k in range(-117, 120 if fmt == E4M3 else 122):
+    for k in range(-100, 120 if fmt == E4M3 else 122):
         e = np.where(amax > most * 2.0 ** (k - 1), k, e)
     e = e[..., None]
     z = np.clip(x * 2.0 ** -e.astype(np.float64), -most, most)

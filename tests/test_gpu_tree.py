@@ -84,11 +84,11 @@ class Problem:
             # (its own weight and the sum's)
             off = 2.0 ** -20 * (1 + score)
             tol = (R.HALF_BF16 + 2 * off[..., None]) * size + R.HALF_BF16 * np.abs(ref) + 1e-30
-            # 8-bit caches, few rows: weights times the values' scales are f16
+            # 8-bit caches: weights times the values' scales are f16
             # numbers of up to 2^15, the largest at least 2^7: below 2^-14 they
             # are off by up to 2^-25, which is 2^-32 of the largest.  A value's
             # number is at most 448 times its scale (127) and a row's largest
-            # at least half of that (or the scale is 2^-117), so a key adds at
+            # at least half of that (or the scale is 2^-100), so a key adds at
             # most 2^-32 x 2 x the largest weighted value
             if self.fmt != R.BF16 and vv.size:
                 tol = tol + vv.shape[1] * 2.0 ** -31 * np.abs(vv[np.isfinite(vv)]).max(initial=0)
