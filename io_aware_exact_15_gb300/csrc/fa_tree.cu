@@ -28,7 +28,7 @@
 //   more rows ("pair"): each warpgroup has 128 of 256 rows, every tile
 //     serves both.
 // bf16 caches: TMA brings each page's rows into the 128-byte-swizzled tile
-// the MMA reads.  8-bit caches: bulk copies bring the stored bytes, and 6 more
+// the MMA reads.  8-bit caches: bulk copies bring the stored bytes, and 8 more
 // warps widen them to the same bf16 tile (exact, see fa_quant.cuh), so the
 // products are those of the values that fa_cache_read returns.
 //
@@ -55,7 +55,9 @@ static_assert(kCacheBf16 == static_cast<int>(FA_CACHE_BF16) &&
                   kCacheInt8 == static_cast<int>(FA_CACHE_INT8),
               "the public formats are the kernels'");
 
-constexpr int kConvWarps = 6;  // warps that widen 8-bit tiles (16 in all: 128 registers)
+// Warps that widen 8-bit tiles, half of them K and half V (18 in all: 96
+// registers).  One tile is a chain of some 2000 cycles for its warps.
+constexpr int kConvWarps = 8, kConvTeam = kConvWarps / 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the max grew by more than 2^8
@@ -139,7 +141,8 @@ struct TreeSmem {
   static constexpr int KV = 2 * TILE;
   static constexpr int RW = KV + NS * TILE;
   static constexpr int SC = RW + NR * RAW;      // scale bytes of the stored tiles
-  static constexpr int ML = SC + NR * kTile;    // (m, l) of the second warpgroup's rows
+  static constexpr int NOTE = SC + NR * kTile;  // what a stored tile holds: int4 each
+  static constexpr int ML = NOTE + NR * 16;     // (m, l) of the second warpgroup's rows
   static constexpr int BAR = ML + kTile * 8;
   static constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + NS, B_RF = B_KVE + NS,
                        B_RE = B_RF + NR, B_SF = B_RE + NR, B_PF = B_SF + 2, B_OF = B_PF + 2,
@@ -150,9 +153,8 @@ struct TreeSmem {
   static constexpr int THREADS = 320 + (Q8 ? 32 * kConvWarps : 0);
   // tensor memory columns: S0, S1 (128 each), O0, O1 (D each)
   static constexpr int T_O = 2 * kTile;
-  // P (bf16) takes the upper half of its S: the scores of keys 64..127 are
-  // in registers when their weights are stored, those of keys 0..63 are
-  // read again
+  // P (bf16) takes the upper half of its S: from the last keys to the first,
+  // the scores are in registers when weights are stored over them
   static constexpr int T_P = 64;
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
@@ -199,12 +201,12 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         mbar_init(bar(L::B_PF + i), 4);
       }
       for (int i = 0; i < L::NS; ++i) {
-        mbar_init(bar(L::B_KVF + i), L::Q8 ? kConvWarps : 1);
+        mbar_init(bar(L::B_KVF + i), L::Q8 ? kConvTeam : 1);
         mbar_init(bar(L::B_KVE + i), 1);
       }
       for (int i = 0; i < L::NR; ++i) {
         mbar_init(bar(L::B_RF + i), 1);
-        mbar_init(bar(L::B_RE + i), kConvWarps);
+        mbar_init(bar(L::B_RE + i), kConvTeam);
       }
       mbar_init(bar(L::B_OF), 1);
       mbar_init(bar(L::B_X1), 4);
@@ -290,7 +292,11 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         if (round > 0) ok = uwait(bar(L::B_RE + slot), (round - 1) & 1);
         if (!ok) break;
         const uint32_t full = bar(L::B_RF + slot);
-        if (lane == 0) mbar_arrive_expect_tx(full, np * page * (D + 1));
+        if (lane == 0) {
+          *reinterpret_cast<int4*>(smem + L::NOTE + slot * 16) =
+              make_int4(x.s.len() - x.kb, x.s.hist - x.kb, x.part, 0);
+          mbar_arrive_expect_tx(full, np * page * (D + 1));
+        }
         __syncwarp();
         if (lane < np) {
           const size_t row = (static_cast<size_t>(id) * p.Hkv + hkv) << p.log_page;
@@ -489,10 +495,10 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
             for (int w = 0; w < 4; ++w)
               vis[w] = valid ? seen_bits(p, mask_row, it.s, t, kb + 32 * w) : 0u;
           }
-          // the scores of a row: all 128 in registers (bf16), or in two
-          // halves, the first read again for its weights (8-bit: the widening
-          // warps leave fewer registers)
-          constexpr int NH = L::Q8 ? 2 : 1, C = 4 / NH;
+          // the scores of a row: all 128 in registers (bf16), or a quarter at
+          // a time, read again for the weights (8-bit: the widening warps
+          // leave fewer registers)
+          constexpr int NH = L::Q8 ? 4 : 1, C = 4 / NH;
           uint32_t sr[C][32];
           auto load_scores = [&](int half) {
 #pragma unroll
@@ -508,20 +514,21 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
                   if (!((vis[C * half + c] >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
             }
           };
-          float mx[C];
+          float mx[4];
 #pragma unroll
-          for (int c = 0; c < C; ++c) mx[c] = -INFINITY;
+          for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
 #pragma unroll
           for (int half = 0; half < NH; ++half) {
             load_scores(half);
 #pragma unroll
             for (int j = 0; j < 32; j += 2)
 #pragma unroll
-              for (int c = 0; c < C; ++c)
-                mx[c] = fmax3(mx[c], __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
+              for (int c = 0; c < C; ++c) {
+                float& x = mx[C == 1 ? (j >> 1) & 3 : c];
+                x = fmax3(x, __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
+              }
           }
-          float mxa = fmaxf(mx[0], mx[1]);
-          if (C == 4) mxa = fmax3(mxa, mx[C - 2], mx[C - 1]);
+          const float mxa = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
           const float m_new = fmaxf(m, mxa * sl2);
           const bool resc = m_new > m + kRescaleLog2;
           const float alpha = resc ? ex2(m - m_new) : 1.f;
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
           uint64_t la = f2_pack(0.f, 0.f), lb = la;
 #pragma unroll
           for (int k = 0; k < NH; ++k) {
-            const int half = NH - 1 - k;  // the last half is in registers
+            const int half = NH - 1 - k;  // the last ones are in registers
             if (k > 0) load_scores(half);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
@@ -713,45 +720,61 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     // stores.  Which half comes first alternates (`sel`) so that the lanes
     // of an access fall on different banks.
     constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per row, rows per step
-    const int cw = warp - 10, u = lane % LPR, rl = lane / LPR;
-    LoadIter<PAIR> li;
-    li.ti = tiles0;
-    Load x;
-    uint32_t idx = 0;
+    constexpr int BATCH = 4;                     // rows of a lane on their way together
+    const int cw = (warp - 10) % kConvTeam, u = lane % LPR, rl = lane / LPR;
+    const bool isv = warp - 10 >= kConvTeam;
     bool ok = true;
     constexpr uint32_t NR = L::Q8 ? L::NR : 1;
-    while (ok && li.next(p, x)) {
+    const uint32_t total = run.left;
+    for (uint32_t g = 0; ok && g < total; ++g) {
+      // place in the rings (see LoadIter).  The tile before this one in either
+      // slot has been consumed: a team's own last tile waited for it or for a
+      // later one, so the parities tell the right loads apart.
+      const uint32_t idx = PAIR  ? 2 * g + (isv ? 1 : 0)
+                           : isv ? (g + 1 == total ? 2 * g + 1 : 2 * g + 2)
+                           : g   ? 2 * g - 1
+                                 : 0;
       const uint32_t rs = idx % NR, ds = idx % L::NS, dr = idx / L::NS;
       ok = uwait(bar(L::B_RF + rs), (idx / NR) & 1);
       if (ok && dr > 0) ok = uwait(bar(L::B_KVE + ds), (dr - 1) & 1);
       if (!ok) break;
       const uint32_t raw = sb + L::RW + rs * L::RAW, sc = sb + L::SC + rs * kTile;
-      const uint32_t dst = sb + L::KV + ds * L::TILE;
-      const int nval = x.s.len() - x.kb, ndraft = x.s.hist - x.kb;
-#pragma unroll 2
-      for (int r0 = cw * RPI; r0 < kTile; r0 += kConvWarps * RPI) {
-        const int row = r0 + rl;
-        const int sel = D == 128 ? ((u >> 2) ^ row) & 1 : (row >> 1) & 1;
-        const uint32_t a = raw + row * D + 16 * u;
-        const uint2 w0 = ld_shared_v2(a + 8 * sel), w1 = ld_shared_v2(a + 8 * (sel ^ 1));
-        const uint32_t byte = ld_shared_u8(sc + row);
-        const RowScale scale = widen_scale<FMT>(byte);
-        uint4 y0, y1;
-        widen4<FMT>(w0.x, scale, y0.x, y0.y);
-        widen4<FMT>(w0.y, scale, y0.z, y0.w);
-        widen4<FMT>(w1.x, scale, y1.x, y1.y);
-        widen4<FMT>(w1.y, scale, y1.z, y1.w);
-        if (x.isv && row >= ndraft) {
-          const bool bad = row < nval && byte == kScaleNan;
-          if (bad) bad_parts[x.part & 7] = x.part;
-          if (bad || row >= nval) y0 = y1 = make_uint4(0, 0, 0, 0);
+      const uint32_t dst = sb + L::KV + ds * L::TILE + (D == 128 ? (u >> 2) * L::CHUNK : 0);
+      const uint4 note = ld_shared_v4(sb + L::NOTE + rs * 16);
+      const int nval = static_cast<int>(note.x), ndraft = static_cast<int>(note.y);
+      const int part = static_cast<int>(note.z), c0 = 2 * (u & 3);
+      const bool check = isv && ndraft < kTile;  // drafts or the end in this tile
+#pragma unroll 1
+      for (int r0 = cw * RPI; r0 < kTile; r0 += BATCH * kConvTeam * RPI) {
+        uint2 w[BATCH][2];
+        uint32_t byte[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int row = r0 + i * kConvTeam * RPI + rl;
+          const int sel = D == 128 ? ((u >> 2) ^ row) & 1 : (row >> 1) & 1;
+          const uint32_t a = raw + row * D + 16 * u;
+          w[i][0] = ld_shared_v2(a + 8 * sel);
+          w[i][1] = ld_shared_v2(a + 8 * (sel ^ 1));
+          byte[i] = ld_shared_u8(sc + row);
         }
-        const uint32_t out = dst + (D == 128 ? (u >> 2) * L::CHUNK : 0);
-        const int c0 = 2 * (u & 3);
-        const uint32_t o0 = out + sw128_offset(row, c0 + sel);
-        const uint32_t o1 = out + sw128_offset(row, c0 + (sel ^ 1));
-        st_shared_v4(o0, y0.x, y0.y, y0.z, y0.w);
-        st_shared_v4(o1, y1.x, y1.y, y1.z, y1.w);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int row = r0 + i * kConvTeam * RPI + rl;
+          const int sel = D == 128 ? ((u >> 2) ^ row) & 1 : (row >> 1) & 1;
+          const RowScale scale = widen_scale<FMT>(byte[i]);
+          uint4 y0, y1;
+          widen4<FMT>(w[i][0].x, scale, y0.x, y0.y);
+          widen4<FMT>(w[i][0].y, scale, y0.z, y0.w);
+          widen4<FMT>(w[i][1].x, scale, y1.x, y1.y);
+          widen4<FMT>(w[i][1].y, scale, y1.z, y1.w);
+          if (check && row >= ndraft) {
+            const bool bad = row < nval && byte[i] == kScaleNan;
+            if (bad) bad_parts[part & 7] = part;
+            if (bad || row >= nval) y0 = y1 = make_uint4(0, 0, 0, 0);
+          }
+          st_shared_v4(dst + sw128_offset(row, c0 + sel), y0.x, y0.y, y0.z, y0.w);
+          st_shared_v4(dst + sw128_offset(row, c0 + (sel ^ 1)), y1.x, y1.y, y1.z, y1.w);
+        }
       }
       fence_async_smem();
       __syncwarp();
@@ -759,7 +782,6 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         mbar_arrive(bar(L::B_KVF + ds));
         mbar_arrive(bar(L::B_RE + rs));
       }
-      ++idx;
     }
   }
   tc_fence_before();
