@@ -20,7 +20,8 @@
 // workspace, and a second kernel joins the parts.  The lengths live on the
 // device, so the kernel finds its run itself (a sum over the sequences).
 //
-// CTA (warp 0 loads, warp 1 issues the MMAs, warps 2-5 and 6-9 do softmax):
+// CTA (warp 0 loads K and Q, warp 10 V, warp 1 issues the MMAs, warps 2-5 and
+// 6-9 do softmax):
 //   up to 128 rows ("split"): the tiles of the run alternate between the two
 //     softmax warpgroups, each with its own S and O in tensor memory, so that
 //     one tile's softmax overlaps the other's MMAs; the two are added at the
@@ -55,102 +56,57 @@ static_assert(kCacheBf16 == static_cast<int>(FA_CACHE_BF16) &&
                   kCacheInt8 == static_cast<int>(FA_CACHE_INT8),
               "the public formats are the kernels'");
 
-// Warps that widen 8-bit tiles, half of them K and half V (18 in all: 96
+// Warps that widen 8-bit tiles, half of them K and half V (19 in all: 96
 // registers).  One tile is a chain of some 2000 cycles for its warps.
 constexpr int kConvWarps = 8, kConvTeam = kConvWarps / 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the max grew by more than 2^8
 
-// One K or V tile to load: `first` of a part brings that part's Q.
-struct Load {
-  int b, hr, kb, part;
-  SeqLen s;
-  bool isv, first;
-};
-
-// The order in which the MMAs consume K and V tiles, which is the order of
-// the rings.  pair: K0 V0 K1 V1 ...; split, where a tile's scores are formed
-// before the previous tile's weights are used: K0 K1 V0 K2 V1 ... V(n-1).
+// Place of K or V of the run's tile g of `total` in the rings, which is the
+// order in which the MMAs consume them.  pair: K0 V0 K1 V1 ...; split, where a
+// tile's scores are formed before the previous tile's weights are used:
+// K0 K1 V0 K2 V1 ... V(n-1).
+// K and V of the same kind of step are handled by warps of their own.  Such a
+// warp never meets a slot two loads late, which a barrier's parity could not
+// tell: its own last tile needed the consumption of one at most two places
+// before the load in question, and tiles are consumed in order.
 template <bool PAIR>
-struct LoadIter {
-  TileIter ti;
-  Load cur, prev;
-  bool owe = false, any = false, done = false;
-  FA_DEV bool advance(const TreeParams& p) {
-    if (!ti.next(p)) return false;
-    cur.b = ti.it.b;
-    cur.hr = ti.it.hr;
-    cur.kb = ti.t * kTile;
-    cur.part = ti.part;
-    cur.s = ti.it.s;
-    cur.first = ti.first;
-    cur.isv = false;
-    return true;
-  }
-  FA_DEV bool next(const TreeParams& p, Load& x) {
-    if (owe) {
-      owe = false;
-      x = prev;
-      x.isv = true;
-      x.first = false;
-      prev = cur;
-      return true;
-    }
-    if (done) return false;
-    if (PAIR && any) {
-      x = cur;
-      x.isv = true;
-      x.first = false;
-      any = false;
-      return true;
-    }
-    if (advance(p)) {
-      x = cur;
-      if (PAIR) {
-        any = true;
-      } else if (any) {
-        owe = true;
-      } else {
-        prev = cur;
-        any = true;
-      }
-      return true;
-    }
-    done = true;
-    if (!PAIR && any) {
-      x = prev;
-      x.isv = true;
-      x.first = false;
-      return true;
-    }
-    return false;
-  }
-};
+FA_DEV uint32_t ring_place(uint32_t g, uint32_t total, bool isv) {
+  if (PAIR) return 2 * g + (isv ? 1 : 0);
+  if (isv) return g + 1 == total ? 2 * g + 1 : 2 * g + 2;
+  return g ? 2 * g - 1 : 0;
+}
 
-template <int D, int FMT>
+template <int D, int FMT, bool PAIR>
 struct TreeSmem {
   static constexpr bool Q8 = FMT != kCacheBf16;
   static constexpr int CH = D / 64;             // 128-byte column chunks per row
   static constexpr int CHUNK = kTile * 128;     // [128 rows x 128 B] = 16 KB
   static constexpr int TILE = CH * CHUNK;       // one 128 x D bf16 tile
   static constexpr int RAW = kTile * D;         // one 128 x D tile of stored bytes
-  static constexpr int NS = Q8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);  // bf16 K/V tiles
-  static constexpr int NR = Q8 ? (D == 64 ? 8 : 4) : 0;                  // stored tiles
-  static constexpr int Q = 0;  // split: two parts' Q; pair: two row tiles
-  static constexpr int KV = 2 * TILE;
+  static constexpr int NS = D == 64 ? (Q8 ? 6 : 8) : Q8 && PAIR ? 3 : 4;  // bf16 K/V tiles
+  static constexpr int NR = !Q8 ? 0 : D == 64 ? 8 : 4;                    // stored tiles
+  // Q: pair: two row tiles; split: the tiles of two parts, or of one where
+  // the stored tiles need the room
+  static constexpr int QB = PAIR || Q8 ? 1 : 2;  // parts whose Q has a place
+  static constexpr int Q = 0;
+  static constexpr int KV = (PAIR ? 2 : QB) * TILE;
   static constexpr int RW = KV + NS * TILE;
-  static constexpr int SC = RW + NR * RAW;      // scale bytes of the stored tiles
+  // bf16: each softmax warp's 32 rows x 32 columns of O on their way out (8-bit
+  // tiles leave no room)
+  static constexpr int OUT = RW + NR * RAW;
+  static constexpr int SC = OUT + (Q8 ? 0 : 8 * 4096);  // scale bytes of the stored tiles
   static constexpr int NOTE = SC + NR * kTile;  // what a stored tile holds: int4 each
   static constexpr int ML = NOTE + NR * 16;     // (m, l) of the second warpgroup's rows
-  static constexpr int BAR = ML + kTile * 8;
+  static constexpr int BAR = ML + (PAIR ? 0 : kTile * 8);
   static constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + NS, B_RF = B_KVE + NS,
                        B_RE = B_RF + NR, B_SF = B_RE + NR, B_PF = B_SF + 2, B_OF = B_PF + 2,
                        B_X1 = B_OF + 1, B_X2 = B_X1 + 1, B_DONE = B_X2 + 1, NBAR = B_DONE + 1;
   static constexpr int RUN = BAR + NBAR * 8;    // Run
   static constexpr int MISC = RUN + 32;
   static constexpr int ALLOC = MISC + 40 + 1024;  // + slack for 1024-byte alignment
-  static constexpr int THREADS = 320 + (Q8 ? 32 * kConvWarps : 0);
+  static constexpr int THREADS = 352 + (Q8 ? 32 * kConvWarps : 0);
   // tensor memory columns: S0, S1 (128 each), O0, O1 (D each)
   static constexpr int T_O = 2 * kTile;
   // P (bf16) takes the upper half of its S: from the last keys to the first,
@@ -171,10 +127,10 @@ FA_DEV uint2 ld_shared_v2(uint32_t addr) {
 }
 
 template <int D, int FMT, bool PAIR>
-__global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
+__global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const TreeParams p) {
-  using L = TreeSmem<D, FMT>;
+  using L = TreeSmem<D, FMT, PAIR>;
   grid_dep_wait();  // the previous kernel's writes are visible from here on
   grid_dep_launch();
   extern __shared__ uint8_t smem_raw[];
@@ -239,81 +195,83 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
   if (run.left > 0) tiles0.it.init(p, run);
   else tiles0.it.left = 0;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 10) {
     // ------------------------------------------------------ loads
-    LoadIter<PAIR> li;
-    li.ti = tiles0;
-    Load x;
-    uint32_t idx = 0;
+    const bool isv = warp == 10;
+    TileIter ti = tiles0;
+    uint32_t g = 0;
     int parts = 0;
     bool ok = true;
     const int page = 1 << p.log_page;
-    while (ok && li.next(p, x)) {
-      const int hkv = x.hr / p.groups;
-      if (x.first) {
-        const int qb = PAIR ? 0 : x.part & 1, use = PAIR ? x.part : x.part >> 1;
+    // pages of the next tile that hold a token, one per lane: looked up one
+    // tile ahead
+    bool have = ti.next(p);
+    int np = 0, id = 0;
+    auto look_up = [&]() {
+      const int kb = ti.t * kTile, nval = min(max(ti.it.s.len() - kb, 0), kTile);
+      np = (nval + page - 1) >> p.log_page;
+      id = 0;
+      if (lane < np)
+        id = p.page_table[static_cast<size_t>(ti.it.b) * p.max_pages + (kb >> p.log_page) + lane];
+    };
+    if (have) look_up();
+    constexpr uint32_t N = L::Q8 ? L::NR : L::NS;
+    constexpr int B_FULL = L::Q8 ? L::B_RF : L::B_KVF, B_FREE = L::Q8 ? L::B_RE : L::B_KVE;
+    while (have) {
+      const int hkv = ti.it.hr / p.groups;
+      if (!isv && ti.first) {
+        const int qb = L::QB == 1 ? 0 : ti.part & 1, use = L::QB == 1 ? ti.part : ti.part >> 1;
         if (use > 0) ok = uwait(bar(L::B_QE + qb), (use - 1) & 1);
         if (!ok) break;
         ++parts;
         if (lane == 0) {
-          const int r0 = (x.hr - hkv * p.groups) * 2 * kTile;
+          const int r0 = (ti.it.hr - hkv * p.groups) * 2 * kTile;
           const bool two = PAIR && r0 + kTile < p.rows;
           mbar_arrive_expect_tx(bar(L::B_QF + qb), (two ? 2 : 1) * L::TILE);
           for (int i = 0; i < (two ? 2 : 1); ++i)
 #pragma unroll
             for (int c = 0; c < L::CH; ++c)
               tma_load_3d(sb + L::Q + (qb + i) * L::TILE + c * L::CHUNK, &tq, bar(L::B_QF + qb),
-                          64 * c, r0 + i * kTile, x.b * p.Hkv + hkv);
+                          64 * c, r0 + i * kTile, ti.it.b * p.Hkv + hkv);
         }
       }
-      // pages of this tile that hold a token, one per lane
-      const int nval = min(max(x.s.len() - x.kb, 0), kTile);
-      const int np = (nval + page - 1) >> p.log_page;
-      int id = 0;
-      if (lane < np)
-        id = p.page_table[static_cast<size_t>(x.b) * p.max_pages + (x.kb >> p.log_page) + lane];
-      id = min(max(id, 0), p.num_pages - 1);
-      if (!L::Q8) {
-        const int slot = idx % L::NS;
-        const uint32_t round = idx / L::NS;
-        if (round > 0) ok = uwait(bar(L::B_KVE + slot), (round - 1) & 1);
-        if (!ok) break;
-        const uint32_t full = bar(L::B_KVF + slot);
-        if (lane == 0) mbar_arrive_expect_tx(full, np * page * D * 2);
-        __syncwarp();
-        if (lane < np)
+      const uint32_t idx = ring_place<PAIR>(g, run.left, isv), slot = idx % N;
+      if (idx >= N) ok = uwait(bar(B_FREE + slot), (idx / N - 1) & 1);
+      if (!ok) break;
+      const uint32_t full = bar(B_FULL + slot);
+      if (lane == 0) {
+        if (L::Q8)
+          *reinterpret_cast<int4*>(smem + L::NOTE + slot * 16) =
+              make_int4(ti.it.s.len() - ti.t * kTile, ti.it.s.hist - ti.t * kTile, ti.part, 0);
+        mbar_arrive_expect_tx(full, np * page * (L::Q8 ? D + 1 : 2 * D));
+      }
+      __syncwarp();
+      if (lane < np) {
+        const int z = min(max(id, 0), p.num_pages - 1) * p.Hkv + hkv;
+        if (!L::Q8) {
 #pragma unroll
           for (int c = 0; c < L::CH; ++c)
             tma_load_3d(sb + L::KV + slot * L::TILE + c * L::CHUNK + lane * page * 128,
-                        x.isv ? &tv : &tk, full, 64 * c, 0, id * p.Hkv + hkv);
-      } else {
-        const int slot = idx % (L::Q8 ? L::NR : 1);
-        const uint32_t round = idx / (L::Q8 ? L::NR : 1);
-        if (round > 0) ok = uwait(bar(L::B_RE + slot), (round - 1) & 1);
-        if (!ok) break;
-        const uint32_t full = bar(L::B_RF + slot);
-        if (lane == 0) {
-          *reinterpret_cast<int4*>(smem + L::NOTE + slot * 16) =
-              make_int4(x.s.len() - x.kb, x.s.hist - x.kb, x.part, 0);
-          mbar_arrive_expect_tx(full, np * page * (D + 1));
-        }
-        __syncwarp();
-        if (lane < np) {
-          const size_t row = (static_cast<size_t>(id) * p.Hkv + hkv) << p.log_page;
+                        isv ? &tv : &tk, full, 64 * c, 0, z);
+        } else {
+          const size_t row = static_cast<size_t>(z) << p.log_page;
           bulk_load(sb + L::RW + slot * L::RAW + lane * page * D,
-                    static_cast<const uint8_t*>(x.isv ? p.vc : p.kc) + row * D, page * D, full);
-          bulk_load(sb + L::SC + slot * kTile + lane * page, (x.isv ? p.vs : p.ks) + row, page,
-                    full);
+                    static_cast<const uint8_t*>(isv ? p.vc : p.kc) + row * D, page * D, full);
+          bulk_load(sb + L::SC + slot * kTile + lane * page, (isv ? p.vs : p.ks) + row, page, full);
         }
       }
-      ++idx;
+      ++g;
+      have = ti.next(p);
+      if (have) look_up();
     }
     // let copies still in flight land before the CTA can exit
-    for (int i = max(0, parts - (PAIR ? 1 : 2)); i < parts; ++i)
-      drain_bar(bar(L::B_QF + (PAIR ? 0 : i & 1)), (PAIR ? i : i >> 1) & 1, p.wait_ns);
-    constexpr uint32_t n = L::Q8 ? L::NR : L::NS;
-    for (uint32_t j = idx > n ? idx - n : 0; j < idx; ++j)
-      drain_bar(bar((L::Q8 ? L::B_RF : L::B_KVF) + j % n), (j / n) & 1, p.wait_ns);
+    for (int i = max(0, parts - L::QB); i < parts; ++i)
+      drain_bar(bar(L::B_QF + (L::QB == 1 ? 0 : i & 1)), (L::QB == 1 ? i : i >> 1) & 1, p.wait_ns);
+    for (uint32_t j = g > N ? g - N : 0; j < g; ++j) {
+      const uint32_t idx = ring_place<PAIR>(j, run.left, isv);
+      // (an earlier load has been replaced in its slot, so it has landed)
+      if (idx + N >= 2 * g) drain_bar(bar(B_FULL + idx % N), (idx / N) & 1, p.wait_ns);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
     auto ecommit = [&](uint32_t b) {
@@ -350,7 +308,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       return uwait(bar(L::B_KVF + idx % L::NS), (idx / L::NS) & 1);
     };
     auto wait_q = [&](int part) {
-      return PAIR ? uwait(bar(L::B_QF), part & 1) : uwait(bar(L::B_QF + (part & 1)), (part >> 1) & 1);
+      return L::QB == 1 ? uwait(bar(L::B_QF), part & 1)
+                        : uwait(bar(L::B_QF + (part & 1)), (part >> 1) & 1);
     };
     // which warpgroups a pair tile serves
     auto members = [&](const TileIter& x) {
@@ -368,14 +327,14 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
       if (ok) {
         tc_fence_after();
         const int slot = idx % L::NS;
-        issue_s(0, PAIR ? 0 : part & 1, slot);
+        issue_s(0, L::QB == 1 ? 0 : part & 1, slot);
         ecommit(bar(L::B_SF));
         if (PAIR && (mem & 2)) {
           issue_s(1, 1, slot);
           ecommit(bar(L::B_SF + 1));
         }
         ecommit(bar(L::B_KVE + slot));
-        if (last) ecommit(bar(L::B_QE + (PAIR ? 0 : part & 1)));
+        if (last) ecommit(bar(L::B_QE + (L::QB == 1 ? 0 : part & 1)));
         ++idx;
       }
     }
@@ -390,10 +349,10 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const int slot = idx % L::NS;
-          issue_s(s ^ 1, ti.part & 1, slot);
+          issue_s(s ^ 1, L::QB == 1 ? 0 : ti.part & 1, slot);
           ecommit(bar(L::B_SF + (s ^ 1)));
           ecommit(bar(L::B_KVE + slot));
-          if (ti.last) ecommit(bar(L::B_QE + (ti.part & 1)));
+          if (ti.last) ecommit(bar(L::B_QE + (L::QB == 1 ? 0 : ti.part & 1)));
           ++idx;
         }
         ok = wait_kv() && uwait(bar(L::B_PF + s), (g >> 1) & 1);
@@ -485,16 +444,22 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
         if (PAIR ? !mine_all : static_cast<int>(g & 1) != s) continue;
         const int kb = tile * kTile;
         const bool tail = kb + kTile > it.s.hist;  // drafts or the end in this tile
-        ok = uwait(bar(L::B_SF + s), cnt & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (busy) {
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          if (tail) {
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        auto look = [&]() {
+          if (tail && busy) {
 #pragma unroll
             for (int w = 0; w < 4; ++w)
               vis[w] = valid ? seen_bits(p, mask_row, it.s, t, kb + 32 * w) : 0u;
           }
+        };
+        // bf16: the mask's words come while the scores are formed (8 bits:
+        // there are no registers for them)
+        if (!L::Q8) look();
+        ok = uwait(bar(L::B_SF + s), cnt & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (L::Q8) look();
+        if (busy) {
           // the scores of a row: all 128 in registers (bf16), or a quarter at
           // a time, read again for the weights (8-bit: the widening warps
           // leave fewer registers)
@@ -595,18 +560,23 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
           if (pos >= it.s.hist) {
             const bool past = pos >= it.s.len();
 #pragma unroll 1
-            for (int c = 0; c < L::CH * 8; ++c) {
-              const uint32_t a = v0 + (c >> 3) * L::CHUNK + sw128_offset(r, c & 7);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (!past) {
-                v = ld_shared_v4(a);
-                if (!(not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) ||
-                      not_finite2(v.w)))
-                  continue;
-                bad_parts[part & 7] = part;
-                v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+            for (int c0 = 0; c0 < L::CH * 8; c0 += 4) {
+              uint4 v[4];
+              uint32_t at[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                at[k] = v0 + (c0 >> 3) * L::CHUNK + sw128_offset(r, (c0 & 7) + k);
+                v[k] = past ? make_uint4(0, 0, 0, 0) : ld_shared_v4(at[k]);
               }
-              st_shared_v4(a, v.x, v.y, v.z, v.w);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool bad = not_finite2(v[k].x) || not_finite2(v[k].y) ||
+                                 not_finite2(v[k].z) || not_finite2(v[k].w);
+                if (bad) bad_parts[part & 7] = part;
+                if (bad || past)
+                  st_shared_v4(at[k], finite2(v[k].x), finite2(v[k].y), finite2(v[k].z),
+                               finite2(v[k].w));
+              }
             }
           }
           fence_async_smem();
@@ -675,7 +645,47 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(x[j]), a1, o[j]);
           }
-          if (row < p.rows) {
+          if (!L::Q8) {
+            // through shared memory, so that a store writes whole pieces of
+            // rows: 4 rows of 128 bytes (parts) or 8 of 64 (results)
+            const uint32_t out = sb + L::OUT + (warp - 2) * 4096;
+            const int rows_here = min(32, p.rows - row0 - q4 * 32);
+            if (whole) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const float* y = &o[8 * v];
+                st_shared_v4(out + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4),
+                             has ? pack_bf16(y[0] * inv, y[1] * inv) : 0u,
+                             has ? pack_bf16(y[2] * inv, y[3] * inv) : 0u,
+                             has ? pack_bf16(y[4] * inv, y[5] * inv) : 0u,
+                             has ? pack_bf16(y[6] * inv, y[7] * inv) : 0u);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const int j = 8 * v + (lane >> 2), piece = lane & 3;
+                const uint4 y = ld_shared_v4(out + j * 64 + ((piece ^ ((j >> 1) & 3)) << 4));
+                if (j < rows_here)
+                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (orow - lane + j) * D +
+                                            32 * c + 8 * piece) = y;
+              }
+            } else {
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                st_shared_v4(out + sw128_offset(lane, v), __float_as_uint(o[4 * v]),
+                             __float_as_uint(o[4 * v + 1]), __float_as_uint(o[4 * v + 2]),
+                             __float_as_uint(o[4 * v + 3]));
+              __syncwarp();
+#pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                const int j = 4 * v + (lane >> 3), piece = lane & 7;
+                const uint4 y = ld_shared_v4(out + sw128_offset(j, piece));
+                if (j < rows_here)
+                  *reinterpret_cast<uint4*>(p.part_o + (prow - lane + j) * D + 32 * c + 4 * piece) = y;
+              }
+            }
+            __syncwarp();
+          } else if (row < p.rows) {
             if (whole) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * D + 32 * c);
 #pragma unroll
@@ -701,6 +711,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
           else
             p.part_ml[prow] = make_float2(valid ? m : -INFINITY, valid ? l : 0.f);
         }
+        __syncwarp();  // rows were written by other lanes of the warp
         if (valid && bad_parts[part & 7] == part)
           add_not_finite<D, FMT>(p, it.b, hkv, it.s, t, max(it.s.hist, it.t0 * kTile),
                                  min(it.s.len(), it.t1 * kTile),
@@ -721,19 +732,13 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT>::THREADS, 1)
     // of an access fall on different banks.
     constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per row, rows per step
     constexpr int BATCH = 4;                     // rows of a lane on their way together
-    const int cw = (warp - 10) % kConvTeam, u = lane % LPR, rl = lane / LPR;
-    const bool isv = warp - 10 >= kConvTeam;
+    const int cw = (warp - 11) % kConvTeam, u = lane % LPR, rl = lane / LPR;
+    const bool isv = warp - 11 >= kConvTeam;
     bool ok = true;
     constexpr uint32_t NR = L::Q8 ? L::NR : 1;
     const uint32_t total = run.left;
     for (uint32_t g = 0; ok && g < total; ++g) {
-      // place in the rings (see LoadIter).  The tile before this one in either
-      // slot has been consumed: a team's own last tile waited for it or for a
-      // later one, so the parities tell the right loads apart.
-      const uint32_t idx = PAIR  ? 2 * g + (isv ? 1 : 0)
-                           : isv ? (g + 1 == total ? 2 * g + 1 : 2 * g + 2)
-                           : g   ? 2 * g - 1
-                                 : 0;
+      const uint32_t idx = ring_place<PAIR>(g, total, isv);
       const uint32_t rs = idx % NR, ds = idx % L::NS, dr = idx / L::NS;
       ok = uwait(bar(L::B_RF + rs), (idx / NR) & 1);
       if (ok && dr > 0) ok = uwait(bar(L::B_KVE + ds), (dr - 1) & 1);
@@ -894,7 +899,7 @@ cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t strea
 template <int D, int FMT, bool PAIR>
 cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t stream) {
-  using L = TreeSmem<D, FMT>;
+  using L = TreeSmem<D, FMT, PAIR>;
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(
       attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT, PAIR>), L::ALLOC);
