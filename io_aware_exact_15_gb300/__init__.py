@@ -64,6 +64,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libfa_gb300.so (building it with nvcc when absent or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -134,6 +136,10 @@ def _p(x):
 def _s(stream):
     if stream is None:
         import torch
+        # the handle itself: a Stream object costs 3 us a call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -985,7 +985,7 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   if (static_cast<long long>(B) * Hkv * p.groups > (1LL << 31) / (most_tiles(p) + 1))
     return FA_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
-  if (p.rows <= kFewRows) {
+  if (tree_few_rows(p.rows, format)) {
     if (!make_cache_map(&tk, k_cache, num_pages * Hkv, page_size, d, format != kCacheBf16) ||
         !make_cache_map(&tv, v_cache, num_pages * Hkv, page_size, d, format != kCacheBf16))
       return FA_ERR_CUDA;

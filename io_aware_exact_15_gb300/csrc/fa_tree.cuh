@@ -241,9 +241,16 @@ static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, i
   }
 }
 
-// Few query rows (p.rows <= kFewRows): fa_tree_few.cu.  tk, tv: maps of
-// 16-row boxes (make_cache_map).
-constexpr int kFewRows = 32;
+// Few query rows per key/value head: fa_tree_few.cu (warp MMAs) is faster up
+// to 16 rows for bf16 and up to 24 for 8 bits.  16 sequences of 8192 keys,
+// 4 heads, us by fa_tree_few.cu | fa_tree.cu:
+//   d = 128   bf16  8 rows 52.3 | 56.0   16: 57.2 | 56.5   24: 73.2 | 56.8
+//             e4m3  8 rows 36.1 | 67.4   24: 62.1 | 68.4   32: 149  | 69.0
+//             int8  8 rows 40.2 | 68.3   24: 65.7 | 69.5   32: 157  | 70.1
+//   d = 64    bf16  8 rows 32.8 | 39.1   16: 36.4 | 39.5   24: 50.8 | 40.0
+//             e4m3  8 rows 25.9 | 54.0   24: 45.9 | 55.2   32: 55.6 | 55.7
+// tk, tv: maps of whole pages (make_cache_map).
+inline bool tree_few_rows(int rows, int format) { return rows <= (format == kCacheBf16 ? 16 : 24); }
 cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream);
 

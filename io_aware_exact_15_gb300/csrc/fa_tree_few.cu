@@ -1,5 +1,6 @@
 // Tree attention for few query rows per key/value head (a decode step, a
-// small tree): R = G T <= 32 rows.
+// small tree): R = G T up to 16 rows, 24 for 8-bit caches (fa_tree.cuh has the
+// rule and both sides' times).
 //
 // With so few rows the work is reading the cache: per 128 keys a
 // 128-row tensor-core tile would compute (and its softmax walk) mostly
@@ -633,12 +634,10 @@ cudaError_t launch_few_rows(const TreeParams& p, const CUtensorMap& tk,
 template <int D, int FMT>
 cudaError_t launch_few_fmt(const TreeParams& p, const CUtensorMap& tk,
                            const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  switch ((p.rows + 7) / 8) {
-    case 1: return launch_few_rows<D, FMT, 1>(p, tk, tv, grid, stream);
-    case 2: return launch_few_rows<D, FMT, 2>(p, tk, tv, grid, stream);
-    case 3: return launch_few_rows<D, FMT, 3>(p, tk, tv, grid, stream);
-    case 4: return launch_few_rows<D, FMT, 4>(p, tk, tv, grid, stream);
-  }
+  if (p.rows <= 8) return launch_few_rows<D, FMT, 1>(p, tk, tv, grid, stream);
+  if (p.rows <= 16) return launch_few_rows<D, FMT, 2>(p, tk, tv, grid, stream);
+  if constexpr (FMT != kCacheBf16)
+    if (p.rows <= 24) return launch_few_rows<D, FMT, 3>(p, tk, tv, grid, stream);
   return cudaErrorInvalidValue;
 }
 
