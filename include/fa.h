@@ -342,8 +342,8 @@ fa_status fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const
  *                     null) for FA_CACHE_BF16
  *   page_table        int32 [B, max_pages]: position p of sequence b is row
  *                     p mod page_size of page page_table[b][p / page_size]
- * page_size 16, 32, 64 or 128; max_pages * page_size and num_pages * Hkv
- * below 2^31; caches and scales 16-byte aligned.  Sequences may share pages
+ * page_size 16, 32, 64 or 128; max_pages * page_size <= 2^30 and
+ * num_pages * Hkv < 2^31; caches and scales 16-byte aligned.  Sequences may share pages
  * that they only read.
  *
  * Formats: FA_CACHE_BF16 keeps rows as they are.  FA_CACHE_E4M3 and
@@ -372,7 +372,7 @@ typedef enum fa_cache_format {
  * Positions below 0 or from max_pages * page_size on, and page ids outside
  * [0, num_pages), are skipped.  Nothing else of the cache is touched.  Two
  * tokens for the same row of a page: one of them is kept, element by
- * element undefined which.
+ * element undefined which.  B*Hkv*(N + 1) < 2^31, B*Hkv <= 2^28.
  */
 fa_status fa_cache_append(const void* k, const void* v, const int* page_table, const int* start,
                           const int* counts, void* k_cache, void* v_cache, uint8_t* k_scale,
@@ -412,7 +412,9 @@ size_t fa_tree_attention_workspace_size(int B, int H, int Hkv, int T, int d);
  * rows of a page past the last draft, pages of other sequences) have no
  * influence on it, whatever they hold.  Lengths are clamped to [0, T] and
  * the table's capacity, page ids to the pool: bad ones give unspecified
- * values but no access outside the cache.  T <= 1024; B*H*T*d < 2^31.
+ * values but no access outside the cache.  T <= 1024; B*H*T*d < 2^31; the
+ * tiles of 128 positions of all B tables, times Hkv, times the groups of 256
+ * rows of H / Hkv * T, less than 2^31.
  * The result for an 8-bit cache is that for a bf16 cache of the values that
  * fa_cache_read returns, up to rounding.
  */

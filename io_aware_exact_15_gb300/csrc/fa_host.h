@@ -55,7 +55,8 @@ inline int log2_page(int page_size) {
 }
 
 // Arguments that describe a paged key/value cache.  A row index
-// (page, head, row) stays below 2^42; positions stay below 2^31.
+// (page, head, row) stays below 2^38; a sequence's positions stay below 2^30,
+// so that sums of two of them, and a tile more, fit in 32 bits.
 inline fa_status check_cache(const void* k_cache, const void* v_cache, const void* k_scale,
                              const void* v_scale, const void* page_table, int format, int Hkv,
                              int d, int num_pages, int page_size, int max_pages) {
@@ -63,7 +64,7 @@ inline fa_status check_cache(const void* k_cache, const void* v_cache, const voi
   if (format < FA_CACHE_BF16 || format > FA_CACHE_INT8) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (log2_page(page_size) < 0) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_pages) * page_size >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_pages) * Hkv >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   FA_TRY(check_ptr16(k_cache));
   FA_TRY(check_ptr16(v_cache));

@@ -949,9 +949,6 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   if (draft_lens) FA_TRY(check_ptr4(draft_lens));
   if (tree_mask) FA_TRY(check_ptr4(tree_mask));
   FA_TRY(check_ws(workspace, workspace_bytes, tree_ws_bytes(H, Hkv, T, d)));
-  fa_status st = FA_OK;
-  int* err = status_word(&st);
-  if (!err) return st;
   TreeParams p = {};
   p.kc = k_cache;
   p.vc = v_cache;
@@ -980,10 +977,13 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.max_pages = max_pages;
   p.words = (T + 31) / 32;
   p.scale = scale;
-  p.err = err;
-  p.wait_ns = wait_limit_ns();
-  if (static_cast<long long>(B) * Hkv * p.groups > (1LL << 31) / (most_tiles(p) + 1))
+  // units (TreeParams, find_run) are counted in 32 bits
+  if (static_cast<long long>(B) * Hkv * p.groups > ((1LL << 31) - 1) / most_tiles(p))
     return FA_ERR_UNSUPPORTED;
+  fa_status st = FA_OK;
+  p.err = status_word(&st);
+  if (!p.err) return st;
+  p.wait_ns = wait_limit_ns();
   CUtensorMap tq, tk, tv;
   if (tree_few_rows(p.rows, format)) {
     if (!make_cache_map(&tk, k_cache, num_pages * Hkv, page_size, d, format != kCacheBf16) ||

@@ -78,6 +78,7 @@ SIZES = [
     (dict(B=0), BAD), (dict(N=0), BAD), (dict(Hkv=0), BAD), (dict(num=0), BAD), (dict(most=0), BAD),
     (dict(fmt=-1), BAD), (dict(fmt=3), BAD), (dict(d=32), UNSUP), (dict(page=8), UNSUP),
     (dict(page=48), UNSUP), (dict(page=256), UNSUP), (dict(most=1 << 27), UNSUP),
+    (dict(most=(1 << 26) + 1), UNSUP),
     (dict(num=1 << 30), UNSUP), (dict(B=1 << 20, N=1 << 20), UNSUP), (dict(B=1 << 28), UNSUP),
 ]
 
@@ -119,6 +120,10 @@ def tree(fmt=0, B=2, H=4, Hkv=2, T=4, d=64, num=8, page=16, most=4, scale=0.1, p
     (dict(scale=0.0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=-1.0), BAD),
     (dict(d=80), UNSUP), (dict(page=24), UNSUP), (dict(T=1025), UNSUP),
     (dict(B=1 << 16, H=64, T=64, d=64), UNSUP), (dict(most=1 << 27), UNSUP),
+    (dict(most=(1 << 26) + 1), UNSUP),
+    # 2^23 tiles in a table, 256 (sequence, head) pairs: 2^31 units; with 512
+    # rows per key/value head twice as many again
+    (dict(B=128, Hkv=2, most=1 << 26), UNSUP), (dict(B=64, H=256, Hkv=2, most=1 << 26), UNSUP),
     (dict(ws=None), BAD), (dict(ws=A + 128), ALIGN), (dict(size=0), WS),
 ])
 def test_tree_refuses(kw, want):
