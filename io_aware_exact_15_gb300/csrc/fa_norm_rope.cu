@@ -24,8 +24,17 @@
 // at a time.  Loads go through a queue in shared memory (asynchronous
 // copies, each lane its own 16 bytes, so nothing has to be synchronised):
 // loads that wait in registers kept at most 64 KB of an SM in flight and
-// lost the time between a block's loads (39.0 us for 4 x 4096 tokens of 20
-// heads of 128, where a plain copy of the bytes takes 29.0).
+// lost the time between a block's loads.
+//
+// Measured, packed input, 16 + 4 heads of 128: forward of 4 x 4096 tokens
+// 34.5 us, 5.1 TB/s (8 x 8192: 122.6 us, 5.5 TB/s; a plain copy of the 4 x
+// 4096 tokens' bytes takes 29.0); backward of 4 x 4096 tokens 49.3 us,
+// 5.3 TB/s.  What is left is the instructions: without the arithmetic, the
+// same loads and stores take 32.5 us, and a warp's step is a chain (load,
+// sum over the lanes, scale, store) that 4 warps of a scheduler do not
+// cover; a third block per SM has no registers.  Addresses are stepped, not
+// formed anew, and pieces behind the last head left out (39.2 us without
+// both); 16 elements a lane took 35.4 us forward, and the backward spilled.
 #include <math.h>
 #include <stdint.h>
 
@@ -212,14 +221,24 @@ FA_DEV void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Where a warp is in its tokens: token, its place (b, n), and the step (group
-// of U * RPW heads, of q first).
+// Where a warp is in its tokens, `stride` apart: token (b, n), and the step
+// (group of U * RPW heads, of q first).
 struct Walk {
-  uint32_t token;
-  int b, n, step;
-  FA_DEV void place(const RopeParams& p) {
+  uint32_t token, stride;
+  int b, n, db, dn, step;
+  FA_DEV Walk(const RopeParams& p)
+      : token(blockIdx.x * kWarps + (threadIdx.x >> 5)), stride(gridDim.x * kWarps), step(0) {
     b = token / p.N;
     n = token - static_cast<uint32_t>(b) * p.N;
+    db = stride / p.N;
+    dn = stride - static_cast<uint32_t>(db) * p.N;
+  }
+  FA_DEV void advance(int N) {
+    // (the sum stays below 2^32: tokens and grid are far smaller)
+    token += stride;
+    b += db;
+    n += dn;
+    if (n >= N) n -= N, ++b;
   }
 };
 
@@ -234,18 +253,19 @@ struct Queue {
   const RopeParams& p;
   uint32_t at;     // shared memory of this lane
   int nq, steps, lane, e0, sub;
-  uint32_t tokens, stride;
+  uint32_t tokens;
   Walk next;       // step to send
   uint32_t sent = 0, turn = 0;
-  int pos_next;    // position of the next token to send
+  int pos_next = 0;            // position of the next token to send (given ones)
+  int left = 0;                // heads of q or of k from this step on
+  const uint16_t *x, *g;       // this lane's first piece of the step; RPW heads
+  long long xh, gh;            // further on is `xh` (gradients `gh`) elements away
 
   FA_DEV int position(uint32_t token) const {
-    if (token >= tokens) return 0;
-    return p.t.positions ? __ldg(p.t.positions + token)
-                         : static_cast<int>(token % static_cast<uint32_t>(p.N));
+    return p.t.positions && token < tokens ? __ldg(p.t.positions + token) : 0;
   }
 
-  FA_DEV Queue(const RopeParams& p_, uint32_t smem) : p(p_) {
+  FA_DEV Queue(const RopeParams& p_, uint32_t smem) : p(p_), next(p_) {
     lane = threadIdx.x & 31;
     at = smem + (threadIdx.x >> 5) * BYTES + lane * 16;
     e0 = 8 * (lane % LPR);
@@ -253,10 +273,6 @@ struct Queue {
     nq = (p.H + GRP - 1) / GRP;
     steps = nq + (p.Hkv + GRP - 1) / GRP;
     tokens = static_cast<uint32_t>(p.B) * p.N;
-    stride = gridDim.x * kWarps;
-    next.token = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    next.step = 0;
-    if (next.token < tokens) next.place(p);
     pos_next = position(next.token);
 #pragma unroll 1
     for (int i = 0; i < kQueue - 1; ++i) send();
@@ -267,43 +283,56 @@ struct Queue {
   }
   FA_DEV uint32_t tables(uint32_t t) const { return at + (kQueue * PIECES + (t & 1) * TAB) * 512; }
 
+  FA_DEV void send_tables() {
+    const int pos = min(max(p.t.positions ? pos_next : next.n, 0), p.t.rows - 1);
+    pos_next = position(tokens - next.token > next.stride ? next.token + next.stride : tokens);
+    if (e0 < p.t.rot) {
+      const size_t row = static_cast<size_t>(pos) * (p.t.rot / 2);
+      const int i0 = INTER ? e0 / 2 : e0 >= p.t.rot / 2 ? e0 - p.t.rot / 2 : e0;
+#pragma unroll
+      for (int i = 0; i < TAB / 2; ++i) {
+        copy16(tables(turn) + i * 512, p.t.cos + row + i0 + 4 * i, true);
+        copy16(tables(turn) + (TAB / 2 + i) * 512, p.t.sin + row + i0 + 4 * i, true);
+      }
+    }
+    ++turn;
+  }
+
   // sends one step (or an empty one behind the last)
   FA_DEV void send() {
     if (next.token < tokens) {
-      if (next.step == 0) {
-        const int pos = min(max(pos_next, 0), p.t.rows - 1);
-        pos_next = position(tokens - next.token > stride ? next.token + stride : tokens);
-        if (e0 < p.t.rot) {
-          const size_t row = static_cast<size_t>(pos) * (p.t.rot / 2);
-          const int i0 = INTER ? e0 / 2 : e0 >= p.t.rot / 2 ? e0 - p.t.rot / 2 : e0;
-#pragma unroll
-          for (int i = 0; i < TAB / 2; ++i) {
-            copy16(tables(turn) + i * 512, p.t.cos + row + i0 + 4 * i, true);
-            copy16(tables(turn) + (TAB / 2 + i) * 512, p.t.sin + row + i0 + 4 * i, true);
-          }
+      if (next.step == 0) send_tables();
+      if (next.step == 0 || next.step == nq) {
+        const bool isq = next.step == 0;
+        left = isq ? p.H : p.Hkv;
+        const Strides s = isq ? p.sq : p.sk;
+        x = static_cast<const uint16_t*>(isq ? p.q : p.k) + next.b * s.b + next.n * s.n + e0 +
+            sub * s.h;
+        xh = RPW * s.h;
+        if (BACK) {
+          gh = static_cast<long long>(p.N) * D;
+          g = static_cast<const uint16_t*>(isq ? p.gq : p.gk) +
+              (static_cast<size_t>(next.b) * left * p.N + next.n) * D + e0 + sub * gh;
+          gh *= RPW;
         }
-        ++turn;
       }
-      const bool isq = next.step < nq;
-      const int h0 = (isq ? next.step : next.step - nq) * GRP, H = isq ? p.H : p.Hkv;
-      const Strides s = isq ? p.sq : p.sk;
-      const uint16_t* x0 =
-          static_cast<const uint16_t*>(isq ? p.q : p.k) + next.b * s.b + next.n * s.n + e0;
-      const uint16_t* g0 = static_cast<const uint16_t*>(isq ? p.gq : p.gk) +
-                           (static_cast<size_t>(next.b) * H * p.N + next.n) * D + e0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * RPW + sub;
-        const bool real = h < H;
-        copy16(piece(sent, u), x0 + (real ? h : 0) * s.h, real);
-        if (BACK)
-          copy16(piece(sent, U + u), g0 + static_cast<size_t>(real ? h : 0) * p.N * D, real);
+        if (!BACK && u * RPW >= left) break;  // nobody takes the pieces behind the last head
+        const bool real = u * RPW + sub < left;
+        if (BACK) {  // heads past the last: zeros, for the sums
+          copy16(piece(sent, u), real ? x + u * xh : p.q, real);
+          copy16(piece(sent, U + u), real ? g + u * gh : p.q, real);
+        } else if (real) {
+          copy16(piece(sent, u), x + u * xh, true);
+        }
       }
+      x += U * xh;
+      if (BACK) g += U * gh;
+      left -= GRP;
       if (++next.step == steps) {
         next.step = 0;
-        // (the sum stays below 2^32: tokens and grid are far smaller)
-        next.token += stride;
-        if (next.token < tokens) next.place(p);
+        next.advance(p.N);
       }
     }
     ++sent;
@@ -311,6 +340,35 @@ struct Queue {
   }
   FA_DEV uint4 take(uint32_t step, int i) const { return ld_shared_v4(piece(step, i)); }
 };
+
+// C pieces of a step, from piece u0: their heads' rows normed and turned.
+// `o` is this lane's place in the first one's result, `oh` RPW heads.
+template <int C, class Q, class T>
+FA_DEV void norm_pieces(const Q& q, const T& turn, uint32_t step, int u0, uint16_t* o, size_t oh,
+                        int left, float inv_d, float eps) {
+  uint4 raw[C];
+  uint64_t x[C][4], y[C][4];
+  float r[C];
+#pragma unroll
+  for (int u = 0; u < C; ++u) raw[u] = q.take(step, u0 + u);
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    widen(raw[u], x[u]);
+    r[u] = dot8(x[u], x[u]);
+    widen(turn.swap(raw[u]), y[u]);
+  }
+  row_sums<Q::LPR>(r);
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    r[u] = rsqrtf(r[u] * inv_d + eps);
+    const uint64_t r2 = f2_pack(r[u], r[u]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[u][i] = f2_mul(f2_fma(y[u][i], turn.s[i], f2_mul(x[u][i], turn.c[i])), r2);
+    if ((u0 + u) * Q::RPW + q.sub < left)
+      *reinterpret_cast<uint4*>(o + (u0 + u) * oh) = narrow(x[u]);
+  }
+}
 
 template <int D, bool INTER, int U>
 __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopeParams p) {
@@ -322,46 +380,35 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_kernel(const RopePar
   Q q(p, smem_u32(rope_smem));
   stage_weights(weights, p.wq, p.wk);
   Turn<D, INTER> turn(p.t.rot, q.lane);
-  Walk w;
-  w.token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Walk w(p);
   uint32_t step = 0, token_no = 0;
-  for (; w.token < q.tokens; w.token += q.stride, ++token_no) {
-    w.place(p);
+  const size_t oh = static_cast<size_t>(p.N) * D;
+  for (; w.token < q.tokens; w.advance(p.N), ++token_no) {
+    uint16_t* o = nullptr;
+    int left = 0;
 #pragma unroll 1
     for (w.step = 0; w.step < q.steps; ++w.step, ++step) {
       q.send();
       copy_wait<kQueue - 1>();  // this step has come
-      const bool isq = w.step < q.nq;
       // the weights go into the rotation's factors: out = r (c w x + s w' x')
       if (w.step == 0 || w.step == q.nq) {
+        const bool isq = w.step == 0;
         turn.template load<false>(q.tables(token_no), 512);
         turn.weigh(smem_u32(weights[isq ? 0 : 1]), q.e0);
+        left = isq ? p.H : p.Hkv;
+        o = static_cast<uint16_t*>(isq ? p.oq : p.ok) + static_cast<size_t>(w.b) * left * oh +
+            static_cast<size_t>(w.n) * D + q.e0 + q.sub * oh;
       }
-      const int h0 = (isq ? w.step : w.step - q.nq) * Q::GRP, H = isq ? p.H : p.Hkv;
-      uint16_t* o0 = static_cast<uint16_t*>(isq ? p.oq : p.ok) +
-                     (static_cast<size_t>(w.b) * H * p.N + w.n) * D + q.e0;
-      uint4 raw[U];
-      uint64_t x[U][4], y[U][4];
-      float r[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = q.take(step, u);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        widen(raw[u], x[u]);
-        r[u] = dot8(x[u], x[u]);
-        widen(turn.swap(raw[u]), y[u]);
+      constexpr float inv_d = 1.f / D;
+      if (left > (U - 1) * Q::RPW) {
+        norm_pieces<U>(q, turn, step, 0, o, Q::RPW * oh, left, inv_d, p.eps);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u * Q::RPW < left; u += 2)
+          norm_pieces<2>(q, turn, step, u, o, Q::RPW * oh, left, inv_d, p.eps);
       }
-      row_sums<Q::LPR>(r);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * Q::RPW + q.sub;
-        r[u] = rsqrtf(r[u] * (1.f / D) + p.eps);
-        const uint64_t r2 = f2_pack(r[u], r[u]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[u][i] = f2_mul(f2_fma(y[u][i], turn.s[i], f2_mul(x[u][i], turn.c[i])), r2);
-        if (h < H) *reinterpret_cast<uint4*>(o0 + static_cast<size_t>(h) * p.N * D) = narrow(x[u]);
-      }
+      o += Q::GRP * oh;
+      left -= Q::GRP;
     }
   }
 }
@@ -378,8 +425,7 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const Ro
   Q q(p, smem_u32(rope_smem));
   stage_weights(staged, p.wq, p.wk);
   Turn<D, INTER> turn(p.t.rot, q.lane);
-  Walk w;
-  w.token = blockIdx.x * kWarps + warp;
+  Walk w(p);
   uint32_t step = 0, token_no = 0;
   uint64_t acc[2][4] = {};  // dwq, dwk of this warp's rows: pairs of fp32 zeros
   uint64_t weights[4];
@@ -422,8 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32) fa_norm_rope_back_kernel(const Ro
       if (h < H) *reinterpret_cast<uint4*>(d0 + h * sh) = narrow(g[u]);
     }
   };
-  for (; w.token < q.tokens; w.token += q.stride, ++token_no) {
-    w.place(p);
+  for (; w.token < q.tokens; w.advance(p.N), ++token_no) {
 #pragma unroll 1
     for (w.step = 0; w.step < q.steps; ++w.step, ++step) {
       q.send();

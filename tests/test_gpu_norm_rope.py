@@ -39,6 +39,9 @@ CASES = [  # B, H, Hkv, N, d, rot, interleaved, positions, table rows
     (2, 3, 7, 33, 64, 48, True, "mixed", 100),
     (2, 16, 4, 1030, 128, 128, False, "mixed", 131072),
     (1, 12, 12, 1500, 64, 32, True, None, 1500),
+    # more tokens than warps: a warp's next token is in another sequence
+    (5, 2, 1, 1031, 64, 64, False, None, 1031),
+    (2501, 1, 3, 3, 128, 96, True, "mixed", 77),
 ]
 
 
