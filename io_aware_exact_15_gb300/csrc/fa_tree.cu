@@ -63,14 +63,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the max grew by more than 2^8
 
-// Place of K or V of the run's tile g of `total` in the rings, which is the
-// order in which the MMAs consume them.  pair: K0 V0 K1 V1 ...; split, where a
-// tile's scores are formed before the previous tile's weights are used:
-// K0 K1 V0 K2 V1 ... V(n-1).
-// K and V of the same kind of step are handled by warps of their own.  Such a
-// warp never meets a slot two loads late, which a barrier's parity could not
-// tell: its own last tile needed the consumption of one at most two places
-// before the load in question, and tiles are consumed in order.
+// Place of K or V of the run's tile g of `total` in the ring of bf16 tiles,
+// which is the order in which the MMAs consume them.  pair: K0 V0 K1 V1 ...;
+// split, where a tile's scores are formed before the previous tile's weights
+// are used: K0 K1 V0 K2 V1 ... V(n-1).
+// K and V are brought by warps of their own.  A barrier's parity tells one
+// load of a slot from the next, not from the one after it, so nobody may wait
+// two loads ahead of the slot's state.  A bringer waits for the consumption
+// of the slot's last tile, NS places back; for its own previous tile, at most
+// two places back, it had waited for the place NS before that one, and the
+// MMAs consume in order, so everything 2 NS places back is gone.  The MMAs
+// take every place in turn.  (The ring of stored 8-bit tiles has no such
+// order, two teams empty it, so it is a ring for K and one for V.)
 template <bool PAIR>
 FA_DEV uint32_t ring_place(uint32_t g, uint32_t total, bool isv) {
   if (PAIR) return 2 * g + (isv ? 1 : 0);
@@ -86,7 +90,7 @@ struct TreeSmem {
   static constexpr int TILE = CH * CHUNK;       // one 128 x D bf16 tile
   static constexpr int RAW = kTile * D;         // one 128 x D tile of stored bytes
   static constexpr int NS = D == 64 ? (Q8 ? 6 : 8) : Q8 && PAIR ? 3 : 4;  // bf16 K/V tiles
-  static constexpr int NR = !Q8 ? 0 : D == 64 ? 8 : 4;                    // stored tiles
+  static constexpr int NR = !Q8 ? 0 : D == 64 ? 8 : 4;  // stored tiles, half K and half V
   // Q: pair: two row tiles; split: the tiles of two parts, or of one where
   // the stored tiles need the room
   static constexpr int QB = PAIR || Q8 ? 1 : 2;  // parts whose Q has a place
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         id = p.page_table[static_cast<size_t>(ti.it.b) * p.max_pages + (kb >> p.log_page) + lane];
     };
     if (have) look_up();
-    constexpr uint32_t N = L::Q8 ? L::NR : L::NS;
+    constexpr uint32_t N = L::Q8 ? L::NR / 2 : L::NS;
     constexpr int B_FULL = L::Q8 ? L::B_RF : L::B_KVF, B_FREE = L::Q8 ? L::B_RE : L::B_KVE;
     while (have) {
       const int hkv = ti.it.hr / p.groups;
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
                           64 * c, r0 + i * kTile, ti.it.b * p.Hkv + hkv);
         }
       }
-      const uint32_t idx = ring_place<PAIR>(g, run.left, isv), slot = idx % N;
+      const uint32_t idx = L::Q8 ? g : ring_place<PAIR>(g, run.left, isv);
+      const uint32_t slot = idx % N + (L::Q8 && isv ? N : 0);
       if (idx >= N) ok = uwait(bar(B_FREE + slot), (idx / N - 1) & 1);
       if (!ok) break;
       const uint32_t full = bar(B_FULL + slot);
@@ -268,9 +273,10 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     for (int i = max(0, parts - L::QB); i < parts; ++i)
       drain_bar(bar(L::B_QF + (L::QB == 1 ? 0 : i & 1)), (L::QB == 1 ? i : i >> 1) & 1, p.wait_ns);
     for (uint32_t j = g > N ? g - N : 0; j < g; ++j) {
-      const uint32_t idx = ring_place<PAIR>(j, run.left, isv);
+      const uint32_t idx = L::Q8 ? j : ring_place<PAIR>(j, run.left, isv);
       // (an earlier load has been replaced in its slot, so it has landed)
-      if (idx + N >= 2 * g) drain_bar(bar(B_FULL + idx % N), (idx / N) & 1, p.wait_ns);
+      if (L::Q8 || idx + N >= 2 * g)
+        drain_bar(bar(B_FULL + idx % N + (L::Q8 && isv ? N : 0)), (idx / N) & 1, p.wait_ns);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
@@ -735,12 +741,12 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     const int cw = (warp - 11) % kConvTeam, u = lane % LPR, rl = lane / LPR;
     const bool isv = warp - 11 >= kConvTeam;
     bool ok = true;
-    constexpr uint32_t NR = L::Q8 ? L::NR : 1;
+    constexpr uint32_t N = L::Q8 ? L::NR / 2 : 1;
     const uint32_t total = run.left;
     for (uint32_t g = 0; ok && g < total; ++g) {
       const uint32_t idx = ring_place<PAIR>(g, total, isv);
-      const uint32_t rs = idx % NR, ds = idx % L::NS, dr = idx / L::NS;
-      ok = uwait(bar(L::B_RF + rs), (idx / NR) & 1);
+      const uint32_t rs = g % N + (isv ? N : 0), ds = idx % L::NS, dr = idx / L::NS;
+      ok = uwait(bar(L::B_RF + rs), (g / N) & 1);
       if (ok && dr > 0) ok = uwait(bar(L::B_KVE + ds), (dr - 1) & 1);
       if (!ok) break;
       const uint32_t raw = sb + L::RW + rs * L::RAW, sc = sb + L::SC + rs * kTile;

@@ -305,3 +305,98 @@ def test_streams_graphs_and_a_shared_workspace():
     graphs[0].replay()
     status_ok()
     assert all(torch.equal(a, b) for a, b in zip(outs[0], want))
+
+
+EDGES = [  # G, T: query rows per key/value head on both sides of every change of form
+    (1, 8), (3, 3), (1, 16), (1, 17), (2, 12), (5, 5), (4, 8), (3, 11), (2, 64), (3, 43), (4, 64),
+    (1, 257), (1, 513), (2, 1024),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", EDGES)
+def test_numbers_of_rows(G, T, d):
+    for fmt in FORMATS:
+        p = Problem(fmt, 2, 2 * G, 2, T, d, 32, [190, 31], [T, (T + 1) // 2], "tree",
+                    seed=G + T + fmt, dev=device())
+        o, lse = p.run()
+        status_ok()
+        p.check(o, lse)
+
+
+@pytest.mark.parametrize("T", [1, 4, 12, 80])
+def test_bad_queries(T):
+    """NaN and infinities in one draft's queries are that draft's alone."""
+    for fmt in FORMATS:
+        p = Problem(fmt, 2, 4, 2, T, 128, 64, [300, 20], None, None, seed=T, dev=device())
+        p.q[0, :, T // 2, 5] = float("nan")
+        p.q[1, :, 0, 9] = float("inf")
+        p.q[1, :, T - 1] = 0  # every key the same weight
+        if T > 1:
+            p.q[0, :, 0] *= 2.0 ** -100
+        p.q_d.copy_(p.q)
+        o, lse = p.run()
+        status_ok()
+        bad = {(0, T // 2)} | ({(1, 0)} if T > 1 else set())
+        p.check(o, lse, rows={(b, t) for b in range(2) for t in range(T)} - bad)
+        assert torch.isnan(o[0, :, T // 2]).all() and torch.isnan(lse[0, :, T // 2]).all()
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_offsets_past_32_bits(T):
+    """Pages more than 2^32 elements into the pool give what pages at its
+    front give (16384 + 8 pages of 2^18 elements)."""
+    dev = device()
+    Hkv, page, d, num = 16, 128, 128, 16384 + 8
+    for fmt in (R.BF16, R.E4M3):
+        p = Problem(fmt, 2, Hkv, Hkv, T, d, page, [200, 310], None, "tree", seed=T, dev=dev)
+        want = p.run()
+        kc, vc = (torch.empty(num, Hkv, page, d, dtype=p.kc.dtype, device=dev) for _ in range(2))
+        ks, vs = (torch.empty(num, Hkv, page, dtype=torch.uint8, device=dev) for _ in range(2))
+        p.kc, p.vc, p.ks, p.vs = kc, vc, ks, vs
+        p.table_d = num - 1 - p.table_d
+        p.fill()
+        got = p.run()
+        status_ok()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        zero = torch.zeros(2, dtype=torch.int32, device=dev)
+        k, v = fa.cache_read(kc, vc, p.table_d, zero, 200, None, ks, vs)
+        for b in range(2):
+            n = min(200, p.k[b].shape[1])
+            assert np.array_equal(R.f64(k)[b, :, :n], R.quantise(R.f64(p.k[b]), fmt)[:, :n])
+        del kc, vc, p
+        torch.cuda.empty_cache()
+
+
+def test_two_streams_at_once():
+    """Different problems on two streams, their workspaces the wrapper's."""
+    dev = device()
+    ps = [Problem(f, 8, 8, 2, T, 128, 64, many(8, 1000, 5000, T), None, "tree", seed=T, dev=dev)
+          for f, T in ((R.E4M3, 2), (R.BF16, 30))]
+    want = [p.run() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = [[p.run(stream=s) for p, s in zip(ps, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    status_ok()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("T,H", [(16, 8), (70, 8), (9, 2), (23, 6)])
+def test_same_bits_every_time(T, H):
+    """Long runs whose loads, conversions and products race each other: one
+    result, over many calls with other work in between."""
+    dev = device()
+    noise = torch.empty(1 << 26, device=dev)
+    for fmt in FORMATS:
+        p = Problem(fmt, 2, H, 2, T, 128, 128, [40001, 23456], None, "tree", seed=T, dev=dev)
+        want = p.run()
+        p.check(*want)
+        for k in range(60):
+            if k % 3 == 0:
+                noise.fill_(k)
+            got = p.run()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (fmt, k)
+        status_ok()
