@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
     if (lane == 0) *run_slot = r;
   } else if (warp == 1 && lane == 0) {
     for (int i = 0; i < L::R; ++i) {
-      mbar_init(full(i), 2);   // K and V
-      mbar_init(empty(i), 8);  // chunks
+      mbar_init(full(i), 2);  // K and V
+      mbar_init(empty(i), L::NC);
     }
     *abort_flag = 0;
     bad_parts[0] = bad_parts[1] = -1;
@@ -319,17 +319,15 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
 #pragma unroll 1
     for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
      const int stage = n % L::R;
-     // every tile is waited for in turn, also those without a chunk of this
-     // warp: a barrier's parity tells two loads of a stage apart, not three
+     // every warp waits for every tile and gives every stage back, also
+     // without a chunk of its own there: a barrier's parity tells two loads of
+     // a stage apart, not three, so nobody may fall two loads behind
      ok = ok && __all_sync(0xffffffffu, wait_bar(full(stage), (n / L::R) & 1, wc));
      if (!ok) continue;
 #pragma unroll 1
      for (; chunk < 8 * (tile - it.t0 + 1); chunk += L::NC) {
       const int sub = chunk & 7, pos = tile * kTile + sub * kFewKeys;
-      if (pos >= it.s.len()) {  // nothing there
-        if (lane == 0) mbar_arrive(empty(stage));
-        continue;
-      }
+      if (pos >= it.s.len()) continue;  // nothing there
       const uint32_t ka = sb + L::RING + stage * L::STAGE + sub * kFewKeys * (Q8 ? D : 128);
       const uint32_t va = ka + L::KBYTES;
       const bool tail = pos + kFewKeys > it.s.hist;
@@ -514,9 +512,9 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
                              a[1][2 * x + 1], pf[rt][0], pf[rt][1]);
         }
       }
-      __syncwarp();  // every lane has read the chunk
-      if (lane == 0) mbar_arrive(empty(stage));
      }
+     __syncwarp();  // every lane has read this warp's chunks
+     if (lane == 0) mbar_arrive(empty(stage));
     }
     // ---- end of the part: the warps' rows are added in a fixed order
     if (bad) bad_parts[part & 1] = part;
