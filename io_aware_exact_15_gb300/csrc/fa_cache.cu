@@ -13,9 +13,12 @@
 // a shuffle reduction, and a warp's rows are consecutive positions of one
 // (sequence, head), so that data and scale bytes land next to each other.
 // Measured: 16 x 4096 tokens of 4 heads of 128, appended as int8 and read
-// back, 59.7 us, 4.4 TB/s (the bytes at a plain copy's rate: 39.1 us).  What
-// is left is latency: lengths, then the page, then rows, one wave of blocks
-// after the other.
+// back, ragged: 56.6 us, 4.6 TB/s (the bytes at a plain copy's rate: 39.1
+// us).  Full rows: append bf16 6.4, e4m3 and int8 4.9 TB/s, read 6.3 and 5.8:
+// finding the scale and rounding is what the 8-bit append adds (int8 by
+// conversions to integers: 4.3), the rest latency: lengths, then the page,
+// then rows, one wave of blocks after the other.  Persistent warps that ask
+// for the next rows before they finish these took 60 instead of 47 us.
 #include <stdint.h>
 
 #include "../../include/fa.h"
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
         if (row[u] >= 0) *reinterpret_cast<uint4*>(cache + (row[u] * D + 8 * l) * EB) = x[u];
         continue;
       }
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
       // |x| as bf16 bits orders like an integer, NaN above infinity
       uint32_t m2 = 0;
 #pragma unroll
@@ -95,10 +98,13 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
       uint2 y = make_uint2(0, 0);
       if (byte != kScaleNan) {
         const float f = inverse_scale(byte);
-        y.x = quantise4<FMT>(bf16_lo(w[0]) * f, bf16_hi(w[0]) * f, bf16_lo(w[1]) * f,
-                             bf16_hi(w[1]) * f);
-        y.y = quantise4<FMT>(bf16_lo(w[2]) * f, bf16_hi(w[2]) * f, bf16_lo(w[3]) * f,
-                             bf16_hi(w[3]) * f);
+        // bf16's largest number is 127.5 steps of int8's largest scale
+        if (FMT == kCacheInt8 && m == 0x7F7Fu)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = __vminu2(w[i] & 0x7FFF7FFFu, 0x7F7E7F7Eu) | (w[i] & 0x80008000u);
+        y.x = quantise4<FMT>(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), f);
+        y.y = quantise4<FMT>(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), f);
       } else {
         // any number times the NaN scale is NaN; a one keeps the byte a number
         y = make_uint2(0x01010101u, 0x01010101u);
@@ -145,8 +151,9 @@ cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   constexpr int RPW = 32 / (D / 8);
   // Up to 8 RPW tokens (a decode step, a tree): one block per (sequence, k or
   // v, head), one row per lane.  More: blocks of 4 warps of eight rows in
-  // flight per lane (16 x 4096 tokens, int8, append and read: 59.7 us; 8
-  // warps 62.0, 2 warps 60.7, four rows per lane 65.7).
+  // flight per lane (16 x 4096 tokens, int8, append and read, before the
+  // rounding by addition: 59.7 us; 8 warps 62.0, 2 warps 60.7, four rows per
+  // lane 65.7).
   const bool wide = p.N > 8 * RPW;
   const int warps = wide ? 4 : (p.N + RPW - 1) / RPW, per = warps * RPW * (wide ? 8 : 1);
   const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N + per - 1) / per);

@@ -38,9 +38,10 @@ FA_DEV uint32_t row_scale(uint32_t amax) {
 // 2^-e for the scale byte e + 127 of row_scale (27 .. 248)
 FA_DEV float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// four fp32 numbers, already scaled, as four stored bytes (x0 lowest)
+// four numbers times f = 2^-e (exact), as four stored bytes (x0 lowest);
+// int8: at most 127 then
 template <int FMT>
-FA_DEV uint32_t quantise4(float x0, float x1, float x2, float x3) {
+FA_DEV uint32_t quantise4(float x0, float x1, float x2, float x3, float f) {
   if (FMT == kCacheE4m3) {
     uint32_t w;
     asm("{\n\t.reg .b16 lo, hi;\n\t"
@@ -48,15 +49,13 @@ FA_DEV uint32_t quantise4(float x0, float x1, float x2, float x3) {
         "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
         "mov.b32 %0, {lo, hi};\n\t}"
         : "=r"(w)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+        : "f"(x0 * f), "f"(x1 * f), "f"(x2 * f), "f"(x3 * f));
     return w;
   }
-  // |x| <= 127.5 by the scale rule; 127.5 is bf16's largest at the largest scale
-  const auto q = [](float x) {
-    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x))));
-  };
-  const uint32_t a = q(x0), b = q(x1), c = q(x2), d = q(x3);
-  return (a & 0xFFu) | (b & 0xFFu) << 8 | (c & 0xFFu) << 16 | d << 24;
+  // Added to 1.5 x 2^23, whose last place is 1, a number is rounded to an
+  // integer (ties to even) whose two's complement is the sum's low byte.
+  const auto q = [f](float x) { return __float_as_uint(fmaf(x, f, 12582912.f)); };
+  return __byte_perm(__byte_perm(q(x0), q(x1), 0x0040), __byte_perm(q(x2), q(x3), 0x0040), 0x5410);
 }
 
 // The scale of a row, prepared for widening its numbers.

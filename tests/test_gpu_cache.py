@@ -191,3 +191,26 @@ def test_strided_rows():
         out.append([host_bytes(t) for t in (kc, vc, ks, vs)])
     status_ok()
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+def test_largest_numbers_saturate(fmt):
+    """bf16's largest number, of either sign, among others: the largest
+    stored number at the largest scale, and finite."""
+    dev = device()
+    big = 2.0 ** 128 - 2.0 ** 120
+    x = torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16)
+    x[..., 0], x[..., 1], x[..., 2], x[..., 3] = big, -big, big / 2, 2.0 ** 121
+    x = x.to(dev)
+    kc, vc, ks, vs = empty_cache(1, 1, 16, 64, fmt, dev)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=dev)
+    zero = torch.zeros(1, dtype=torch.int32, device=dev)
+    for n in (1, 16):
+        fa.cache_append(x[:, :, :n], x[:, :, :n], kc, vc, table, zero, None, ks, vs)
+    y, _ = fa.cache_read(kc, vc, table, zero, 16, None, ks, vs)
+    status_ok()
+    most = 127 * 2.0 ** 121 if fmt == R.INT8 else 448 * 2.0 ** 119
+    # half of it: 63.75 steps of 2^121, or 255 of 2^119 in steps of 16
+    half = 64 * 2.0 ** 121 if fmt == R.INT8 else 256 * 2.0 ** 119
+    want = torch.tensor([most, -most, half, 2.0 ** 121] + [0.0] * 60, dtype=torch.float64)
+    assert torch.equal(y[0, 0].double().cpu(), want.expand(16, 64))
