@@ -879,13 +879,16 @@ int slot_rows(int rows) {
   return rows < most ? rows : most;
 }
 
-constexpr size_t kJoinBytes = kMaxGrid * sizeof(int2);  // a multiple of 256
+int most_ctas(int rows) { return rows <= 8 ? 2 * kMaxGrid : kMaxGrid; }
+
+constexpr size_t kJoinBytes = 2 * kMaxGrid * sizeof(int2);  // a multiple of 256
 size_t tree_ml_bytes(int rows) {
-  return align256(2ull * kMaxGrid * slot_rows(rows) * sizeof(float2));
+  return align256(2ull * most_ctas(rows) * slot_rows(rows) * sizeof(float2));
 }
 size_t tree_ws_bytes(int H, int Hkv, int T, int d) {
   const int rows = H / Hkv * T;
-  return kJoinBytes + tree_ml_bytes(rows) + align256(2ull * kMaxGrid * slot_rows(rows) * d * sizeof(float));
+  return kJoinBytes + tree_ml_bytes(rows) +
+         align256(2ull * most_ctas(rows) * slot_rows(rows) * d * sizeof(float));
 }
 
 // Tiles of the longest sequence that the page table can hold.
@@ -893,11 +896,11 @@ long long most_tiles(const TreeParams& p) {
   return ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
 }
 
-// CTAs: one per SM, no more than there can be units (0 on error).
-int tree_grid(const TreeParams& p) {
-  const int sms = sm_count();
+// CTAs: `per_sm` per SM, no more than there can be units (0 on error).
+int tree_grid(const TreeParams& p, int per_sm) {
+  const int sms = sm_count() * per_sm;
   const long long most = static_cast<long long>(p.B) * p.Hkv * p.groups * most_tiles(p);
-  const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+  const int grid = sms < most_ctas(p.rows) ? sms : most_ctas(p.rows);
   return most < grid ? static_cast<int>(most) : grid;
 }
 
@@ -917,7 +920,7 @@ cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap& tq, const C
   cudaError_t e = smem_attr_once(
       attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT, PAIR>), L::ALLOC);
   if (e != cudaSuccess) return e;
-  const int grid = tree_grid(p);
+  const int grid = tree_grid(p, 1);
   if (grid <= 0) return cudaErrorInvalidDevice;
   e = launch_pdl(fa_tree_kernel<D, FMT, PAIR>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream, tq,
                  tk, tv, p);
@@ -1002,7 +1005,7 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
     if (!make_cache_map(&tk, k_cache, num_pages * Hkv, page_size, d, format != kCacheBf16) ||
         !make_cache_map(&tv, v_cache, num_pages * Hkv, page_size, d, format != kCacheBf16))
       return FA_ERR_CUDA;
-    const int grid = tree_grid(p);
+    const int grid = tree_grid(p, few_ctas(p.rows, format, d));
     if (grid <= 0) return FA_ERR_CUDA;
     FA_CUDA(launch_tree_few(p, format, d, tk, tv, grid, stream));
     FA_CUDA(launch_join(p, d, grid, stream));

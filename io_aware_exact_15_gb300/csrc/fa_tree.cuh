@@ -10,7 +10,9 @@
 
 namespace fa {
 
-constexpr int kMaxGrid = 192;     // CTAs, at most (the workspace holds two parts of each)
+// CTAs, at most (the workspace holds two parts of each); up to 8 rows twice
+// as many
+constexpr int kMaxGrid = 192;
 
 struct TreeParams {
   const void* q;           // bf16 [B, H, T, d]
@@ -251,6 +253,10 @@ static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, i
 //             e4m3  8 rows 25.9 | 54.0   24: 45.9 | 55.2   32: 55.6 | 55.7
 // tk, tv: maps of whole pages (make_cache_map).
 inline bool tree_few_rows(int rows, int format) { return rows <= (format == kCacheBf16 ? 16 : 24); }
+// CTAs of it on an SM
+constexpr int few_ctas(int rows, int format, int d) {
+  return rows <= 8 && (format != kCacheBf16 || d == 64) ? 2 : 1;
+}
 cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream);
 

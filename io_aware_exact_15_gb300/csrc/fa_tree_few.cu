@@ -65,20 +65,23 @@ constexpr float kLift = 7.0f;  // f16 weights: 2^7 above the max, 2^15 at most
 template <int D, int FMT, int RT>
 struct FewSmem {
   static constexpr bool Q8 = FMT != kCacheBf16;
+  static constexpr int ROWS = 8 * RT;
   static constexpr int EB = Q8 ? 1 : 2;
   static constexpr int CH = Q8 ? 1 : D / 64;            // column chunks of a tile
   static constexpr int CHUNK = kTile * (Q8 ? D : 128);  // bytes of one: [128 rows x 128 or D B]
   static constexpr int KBYTES = CH * CHUNK;             // 128 keys or values
   static constexpr int STAGE = 2 * KBYTES;
-  static constexpr int R = Q8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);  // stages
+  static constexpr int CTAS = few_ctas(ROWS, FMT, D);   // per SM
+  static constexpr int R = CTAS == 2 ? (STAGE == 16384 ? 6 : 3)  // stages
+                           : Q8      ? (D == 128 ? 6 : 8)
+                                     : (D == 128 ? 3 : 6);
   // Warps that load.  With four each stage belongs to one pair of them (an
   // even number of stages), so that no warp waits for a stage whose last
   // load but one is another warp's.
-  static constexpr int NL = RT == 1 && R % 2 == 0 ? 4 : 2;
+  static constexpr int NL = CTAS == 1 && RT == 1 && R % 2 == 0 ? 4 : 2;
   // warps that compute; 128, 168 or 255 registers for each of the CTA's
-  static constexpr int NC = RT == 1 ? 16 - NL : RT == 2 ? 10 : 6;
+  static constexpr int NC = CTAS == 2 ? 6 : RT == 1 ? 16 - NL : RT == 2 ? 10 : 6;
   static constexpr int THREADS = 32 * (NC + NL);
-  static constexpr int ROWS = 8 * RT;
   // columns added up at a time: at most 32 KB of the warps' rows
   static constexpr int CW = RT == 1 ? 64 : 32;
   static constexpr int RING = 0;
@@ -89,7 +92,7 @@ struct FewSmem {
   static constexpr int RUN = BAR + R * 16;
   static constexpr int MISC = RUN + 32;                   // abort flag, bad parts
   static constexpr int ALLOC = MISC + 16 + 1024;          // + slack for 1024-byte alignment
-  static_assert(ALLOC <= 232448, "shared memory budget");
+  static_assert((ALLOC + 1024) * CTAS <= 233472, "shared memory budget");
 };
 
 template <bool F16>
@@ -148,7 +151,7 @@ FA_DEV float lanes_sum(float v) {
 }
 
 template <int D, int FMT, int RT>
-__global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, 1)
+__global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, RT>::CTAS)
     fa_tree_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const TreeParams p) {
   using L = FewSmem<D, FMT, RT>;
