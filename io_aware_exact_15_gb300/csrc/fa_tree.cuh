@@ -247,13 +247,16 @@ static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, i
 // to 16 rows for bf16 and up to 24 for 8 bits.  16 sequences of 8192 keys,
 // 4 heads, us by fa_tree_few.cu | fa_tree.cu:
 //   d = 128   bf16  8 rows 52.3 | 56.0   16: 57.2 | 56.5   24: 73.2 | 56.8
-//             e4m3  8 rows 36.1 | 67.4   24: 62.1 | 68.4   32: 149  | 69.0
-//             int8  8 rows 40.2 | 68.3   24: 65.7 | 69.5   32: 157  | 70.1
-//   d = 64    bf16  8 rows 32.8 | 39.1   16: 36.4 | 39.5   24: 50.8 | 40.0
-//             e4m3  8 rows 25.9 | 54.0   24: 45.9 | 55.2   32: 55.6 | 55.7
+//             e4m3  8 rows 36.7 | 67.4   24: 60.0 | 68.4   32: 149  | 69.6
+//             int8  8 rows 39.4 | 68.3   24: 64.8 | 69.5   32: 157  | 71.0
+//   d = 64    bf16  8 rows 32.0 | 39.1   16: 36.2 | 39.5   24: 50.8 | 40.0
+//             e4m3  8 rows 25.8 | 54.0   24: 44.6 | 55.2   32: 55.6 | 55.6
 // tk, tv: maps of whole pages (make_cache_map).
 inline bool tree_few_rows(int rows, int format) { return rows <= (format == kCacheBf16 ? 16 : 24); }
-// CTAs of it on an SM
+// CTAs of it on an SM: two up to 8 rows, but for bf16 of d = 128, whose ring
+// takes the whole shared memory.  Two (8 warps each) | one (16 warps), e4m3,
+// 4 rows of 4 heads of 128, us: 4096 sequences of 60 keys 298 | 455, 256 of
+// 500 keys 48.1 | 55.4, 32 of up to 8192 keys 40.9 | 41.2.
 constexpr int few_ctas(int rows, int format, int d) {
   return rows <= 8 && (format != kCacheBf16 || d == 64) ? 2 : 1;
 }

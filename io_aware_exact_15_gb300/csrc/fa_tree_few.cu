@@ -9,13 +9,14 @@
 // already cost more than the memory), and every warp keeps its own running
 // softmax over its own keys:
 //   A CTA has a run of units as in fa_tree.cu (a unit is 128 keys of a
-//   (sequence, key/value head)).  Some warps load whole units into a ring of
-//   stages (K and V apart, up to 8 rows also odd and even units apart: a unit
-//   costs such a warp 1700 cycles, the memory 1540 at 8 bits); the others
-//   take the units' 16-key chunks in turn and meet only at the end of a
-//   problem, where their O and (m, l) are added.  A chunk is a chain of
-//   dependent steps of some 1500 cycles, so many warps (12 where registers
-//   allow) are needed to follow the memory.
+//   (sequence, key/value head)).  Two warps load whole units into a ring of
+//   stages, one K and one V; the others take the units' 16-key chunks in turn
+//   and meet only at the end of a problem, where their O and (m, l) are
+//   added.  A chunk is a chain of dependent steps of some 1500 cycles and a
+//   unit costs a loading warp 1700, so many warps of both kinds are needed to
+//   follow the memory: two CTAs per SM where their rings and registers fit
+//   (few_ctas), which also hides the ends of short problems, a chain of
+//   barriers and sums, behind each other.
 //   S^T = K Q^T (16 keys x 8 rows) and O^T += V^T P^T (16 columns x 8 rows)
 //   stay in registers; P^T becomes an operand by an 8 x 8 transpose.
 //
@@ -41,8 +42,9 @@
 // operations per two elements against one or two.
 //
 // Measured: 32 sequences x 1 token, 16 + 4 heads of 128, up to 8192 e4m3
-// keys: 41.3 us, 4.2 TB/s (the bytes at a plain copy's rate: 25.8).  Issue
-// slots are 49 % busy, the ALU 50 %; the rest is the chain of a chunk.
+// keys: 40.7 us, 4.2 TB/s (the bytes at a plain copy's rate: 25.8); 256
+// sequences of 500 keys 47.8 (20.0).  Issue slots are about half busy, the
+// ALU too; the rest is the chain of a chunk and the ends of problems.
 #include <math.h>
 #include <stdint.h>
 
@@ -75,12 +77,9 @@ struct FewSmem {
   static constexpr int R = CTAS == 2 ? (STAGE == 16384 ? 6 : 3)  // stages
                            : Q8      ? (D == 128 ? 6 : 8)
                                      : (D == 128 ? 3 : 6);
-  // Warps that load.  With four each stage belongs to one pair of them (an
-  // even number of stages), so that no warp waits for a stage whose last
-  // load but one is another warp's.
-  static constexpr int NL = CTAS == 1 && RT == 1 && R % 2 == 0 ? 4 : 2;
-  // warps that compute; 128, 168 or 255 registers for each of the CTA's
-  static constexpr int NC = CTAS == 2 ? 6 : RT == 1 ? 16 - NL : RT == 2 ? 10 : 6;
+  static constexpr int NL = 2;  // warps that load
+  // warps that compute; 128, 168 or 255 registers for each of an SM's
+  static constexpr int NC = CTAS == 2 ? 6 : RT == 1 ? 14 : RT == 2 ? 10 : 6;
   static constexpr int THREADS = 32 * (NC + NL);
   // columns added up at a time: at most 32 KB of the warps' rows
   static constexpr int CW = RT == 1 ? 64 : 32;
@@ -94,6 +93,8 @@ struct FewSmem {
   static constexpr int ALLOC = MISC + 16 + 1024;          // + slack for 1024-byte alignment
   static_assert((ALLOC + 1024) * CTAS <= 233472, "shared memory budget");
 };
+
+FA_DEV void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 template <bool F16>
 FA_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -196,24 +197,16 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
 
   if (warp < L::NL) {
     // ------------------------------------------------------ loads
-    // warp 0: K, warp 1: V; with four warps 2, 3 the same of the odd tiles
-    constexpr uint32_t STEP = L::NL / 2;
-    const bool isv = warp & 1;
+    // warp 0: K, warp 1: V
+    const bool isv = warp == 1;
     const CUtensorMap* map = isv ? &tv : &tk;
     const uint8_t* sc = isv ? p.vs : p.ks;
     const int psize = 1 << p.log_page;
     TileIter ti;
     ti.it.init(p, run);
-    const uint32_t n0 = warp >> 1;
-    uint32_t n = n0;
+    uint32_t n = 0;
     bool ok = true;
-    auto next = [&]() {
-      bool have = ti.next(p);
-      for (uint32_t i = 1; i < STEP && have; ++i) have = ti.next(p);
-      return have;
-    };
     bool have = ti.next(p);
-    if (n0 > 0 && have) have = ti.next(p);
     // pages of the next tile that hold a token, one per lane
     int np = 0, id = 0;
     auto look_up = [&]() {
@@ -226,6 +219,11 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
     if (have) look_up();
     while (have) {
       const int stage = n % L::R;
+      if (!isv && ti.first) {  // Q of a part that the others are still to begin
+        const char* q = static_cast<const char*>(p.q) +
+                        (static_cast<size_t>(ti.it.b) * p.Hkv + ti.it.hr) * p.rows * (2 * D);
+        if (lane < p.rows * (D / 64)) prefetch_l1(q + 128 * lane);
+      }
       if (n >= L::R) ok = __all_sync(0xffffffffu, wait_bar(empty(stage), (n / L::R - 1) & 1, wc));
       if (!ok) break;
       if (lane == 0)
@@ -242,13 +240,13 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
           bulk_load(sb + L::SC + stage * 256 + (isv ? 128 : 0) + lane * psize,
                     sc + (static_cast<size_t>(z) << p.log_page), psize, full(stage));
       }
-      n += STEP;
-      have = next();
+      ++n;
+      have = ti.next(p);
       if (have) look_up();
     }
     // let copies still in flight land before the CTA can exit
-    for (uint32_t j = n0; j < n; j += STEP)
-      if (j + L::R >= n) drain_bar(full(j % L::R), (j / L::R) & 1, p.wait_ns);
+    for (uint32_t j = n > L::R ? n - L::R : 0; j < n; ++j)
+      drain_bar(full(j % L::R), (j / L::R) & 1, p.wait_ns);
     return;
   }
 
