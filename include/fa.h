@@ -13,9 +13,9 @@
  * Conventions shared by every call
  *   Tensors      bf16, contiguous [B, H, N, d] (each (b, h) slice is the
  *                pages' N x d matrix); lse and D are fp32 [B, H, N].
- *   Pointers     device pointers.  q, k, v, o, dO, dq, dk, dv and the
- *                workspace must be 16-byte aligned (TMA / vector access);
- *                lse 4-byte aligned.  Misalignment -> FA_ERR_MISALIGNED.
+ *   Pointers     device pointers.  q, k, v, o, dO, dq, dk, dv must be
+ *                16-byte aligned (TMA / vector access), workspaces 256-byte,
+ *                lse 4-byte.  Misalignment -> FA_ERR_MISALIGNED.
  *   Sizes        B, H, N >= 1; d in {64, 128} (else FA_ERR_UNSUPPORTED);
  *                B*H*N*d < 2^31.  scale finite and > 0.
  *   Masks        causal != 0 keeps key j for query i iff j <= i.  Block
@@ -351,9 +351,9 @@ fa_status fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const
  * head, key or value), the value being number * 2^(s - 127): the smallest
  * power of two that keeps the row within +-448 (+-127), at least 2^-100,
  * then round to nearest, ties to even.  (The power is at most 2^119, 2^121,
- * where the largest number is still finite in bf16; larger values saturate.)  What reads back is exact in bf16,
- * and storing it again gives the same values, so tokens can be moved by
- * reading and appending them.  A row that holds a NaN or an infinity is
+ * where the largest number is still finite in bf16; larger values saturate.)
+ * What reads back is exact in bf16, and storing it again gives the same
+ * values, so tokens can be moved by reading and appending them.  A row that holds a NaN or an infinity is
  * stored with s = 255 and reads back as NaN in all its elements.  The e4m3
  * code of NaN (0x7f, 0xff) is never written; what it stands for in a cache
  * filled by other means is not specified.
@@ -391,7 +391,8 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const uint8_t*
                         int d, int num_pages, int page_size, int max_pages, cudaStream_t stream);
 
 /* Bytes of workspace fa_tree_attention needs, whatever the lengths of the
- * histories. */
+ * histories.  Its contents on entry do not matter; calls that may run at the
+ * same time need workspaces of their own. */
 size_t fa_tree_attention_workspace_size(int B, int H, int Hkv, int T, int d);
 
 /*
