@@ -37,7 +37,7 @@
 // brackets): 8 x 23 drafts of 16 + 4 heads over up to 16384 keys, bf16, 92
 // rows: 48.0 us (27.0), 3.8 TB/s; what is left are the ends of parts and the
 // join.  2 x 16 drafts over up to 131072 keys, e4m3, 64 rows: 115 us (33.0);
-// 16 x 64 drafts over up to 8192 keys, int8, 256 rows: 80.2 us (15.2, by the
+// 16 x 64 drafts over up to 8192 keys, int8, 256 rows: 79.0 us (15.2, by the
 // products); both wait for widened tiles: issue slots 52 and 40 % busy.
 //
 // Keys that nobody may see are never left to chance: scores are replaced by
@@ -96,8 +96,11 @@ struct TreeSmem {
   static constexpr int CHUNK = kTile * 128;     // [128 rows x 128 B] = 16 KB
   static constexpr int TILE = CH * CHUNK;       // one 128 x D bf16 tile
   static constexpr int RAW = kTile * D;         // one 128 x D tile of stored bytes
-  static constexpr int NS = D == 64 ? (Q8 ? 6 : 8) : Q8 && PAIR ? 3 : 4;  // bf16 K/V tiles
-  static constexpr int NR = !Q8 ? 0 : D == 64 ? 8 : 4;  // stored tiles, half K and half V
+  // bf16 K/V tiles, and stored tiles (half K, half V).  d = 128, pair, 256
+  // rows: 4 and 2 take 106.6 us where 3 and 4 take 110.4 (16 x 8192 e4m3
+  // keys, 4 heads); split, 64 rows, 4 and 4 take 115 where 5 and 2 take 142.
+  static constexpr int NS = D == 64 ? (Q8 ? 6 : 8) : 4;
+  static constexpr int NR = !Q8 ? 0 : D == 64 ? 8 : PAIR ? 2 : 4;
   // Q: pair: two row tiles; split: the tiles of two parts, or of one where
   // the stored tiles need the room
   static constexpr int QB = PAIR || Q8 ? 1 : 2;  // parts whose Q has a place
