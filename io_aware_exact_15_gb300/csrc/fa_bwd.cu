@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tdq, const BwdParams p) {
   using L = BwdSmem<D>;
-  // with dQ reduce-adds, no early grid_dep_launch: the next kernel may be a
-  // preprocess that zeroes the accumulator before its own wait
+  // with dQ reduce-adds, no early grid_dep_launch: with it here and in the
+  // dQ conversion, 8 x 16 x 2048 rows of 128 took 744 us instead of 709
   if (!DQ) grid_dep_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &

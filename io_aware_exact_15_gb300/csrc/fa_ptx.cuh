@@ -87,13 +87,14 @@ FA_DEV void drain_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
 // Kernels of the library are launched with programmatic stream serialization:
 // a kernel may be scheduled while the previous kernel in the stream is still
 // finishing, so each kernel waits (grid_dep_wait) before its first access to
-// global memory, which makes everything the previous kernel wrote visible,
-// and then lets the next kernel be scheduled (grid_dep_launch).  Without that
-// launch attribute both are no-ops.  Two exceptions: the backward preprocess
-// zeroes the dQ accumulator before its wait (that work depends on nothing
-// the forward writes and can overlap its last wave), and so the kernels that
-// read or add into that accumulator (the backward main kernel, the dQ
-// conversion) let the next kernel start only when they have finished.
+// global memory, which makes everything the previous kernel wrote visible
+// and means that it reads nothing any more, and then lets the next kernel be
+// scheduled (grid_dep_launch).  Without that launch attribute both are no-ops.
+// There is no exception: a kernel that writes before its wait, were it only
+// zeros into its own workspace, races with a previous kernel that still uses
+// that memory (the same workspace, or a tensor freed after its launch).  A
+// kernel may leave grid_dep_launch out; the next one then starts when it is
+// done.
 FA_DEV void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 FA_DEV void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
