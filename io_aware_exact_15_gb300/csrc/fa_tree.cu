@@ -116,7 +116,8 @@ struct TreeSmem {
   static constexpr int BAR = ML + (PAIR ? 0 : kTile * 8);
   static constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + NS, B_RF = B_KVE + NS,
                        B_RE = B_RF + NR, B_SF = B_RE + NR, B_PF = B_SF + 2, B_OF = B_PF + 2,
-                       B_X1 = B_OF + 1, B_X2 = B_X1 + 1, B_DONE = B_X2 + 1, NBAR = B_DONE + 1;
+                       B_X1 = B_OF + 1, B_X2 = B_X1 + 1, B_DONE = B_X2 + 1,
+                       B_OF1 = B_DONE + 1, NBAR = B_OF1 + (PAIR ? 1 : 0);
   static constexpr int RUN = BAR + NBAR * 8;    // Run
   static constexpr int MISC = RUN + 32;
   static constexpr int ALLOC = MISC + 40 + 1024;  // + slack for 1024-byte alignment
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         mbar_init(bar(L::B_RE + i), kConvTeam);
       }
       mbar_init(bar(L::B_OF), 1);
+      if (PAIR) mbar_init(bar(L::B_OF1), 1);
       mbar_init(bar(L::B_X1), 4);
       mbar_init(bar(L::B_X2), 4);
       mbar_init(bar(L::B_DONE), 1);
@@ -416,7 +418,12 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         }
       }
       if (last) {
+        // pair: a barrier for each warpgroup, and only for parts in which it
+        // has rows.  The issuer needs nothing of the second one for the
+        // others, and on a shared barrier it could be two phases ahead of a
+        // warp that still waits for the part before.
         ecommit(bar(L::B_OF));
+        if (PAIR && (mem & 2)) ecommit(bar(L::B_OF1));
         acc0 = acc1 = false;
       }
       ++g;
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     const float sl2 = p.scale * kLog2e;
     float2* ml = reinterpret_cast<float2*>(smem + L::ML);
     PartIter it = tiles0.it;
-    uint32_t g = 0, cnt = 0;
+    uint32_t g = 0, cnt = 0;  // tiles; parities of own tiles (bit 0) and parts (bit 1)
     const uint32_t total = run.left;
     int part = -1;
     bool ok = true, owe_x2 = false;
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::B_PF + s));
-        ++cnt;
+        cnt ^= 1;
         ++mine;
       }
       if (!ok) break;
@@ -619,7 +626,12 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         owe_x2 = true;
         continue;
       }
-      ok = uwait(bar(L::B_OF), part & 1);
+      if (!PAIR) {
+        ok = uwait(bar(L::B_OF), part & 1);
+      } else if (mine_all) {
+        ok = uwait(bar(s ? L::B_OF1 : L::B_OF), (cnt >> 1) & 1);
+        cnt ^= 2;
+      }
       if (ok && !PAIR) ok = uwait(bar(L::B_X1), part & 1);
       if (!ok) break;
       tc_fence_after();

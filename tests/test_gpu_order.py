@@ -119,3 +119,42 @@ def test_freed_inputs_handed_to_the_next_call():
         fa.attention_backward(q, k, v, want_o, do, want_l)
         assert torch.equal(o, want_o) and torch.equal(lse, want_l)
     status_ok()
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.INT8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(3, 100), (1, 257), (5, 120)])
+def test_last_groups_of_at_most_128_rows(G, T, d, fmt):
+    """300, 257 and 600 rows: the last group of a head occupies one of the two
+    softmax warpgroups, the other goes on to the next head's.  Many problems
+    of a tile or two, the same bits every time, no wait runs out."""
+    dev = device()
+    B, Hkv, page = 24, 3, 32
+    g = torch.Generator().manual_seed(G + T + d)
+    hist = torch.randint(0, 260, (B,), generator=g).int()
+    hist[::5] = 0
+    pages = -(-(260 + T) // page)
+    table = torch.randperm(B * pages, generator=g).int().view(B, pages).to(dev)
+    kc, vc = (torch.empty(B * pages, Hkv, page, d, dtype=R.DTYPES[fmt], device=dev)
+              for _ in range(2))
+    ks, vs = (torch.empty(B * pages, Hkv, page, dtype=torch.uint8, device=dev) for _ in range(2))
+    k, v = (torch.randn(B, Hkv, 260 + T, d, generator=g).bfloat16() for _ in range(2))
+    zero = torch.zeros(B, dtype=torch.int32, device=dev)
+    fa.cache_append(k.to(dev), v.to(dev), kc, vc, table, zero, None, ks, vs)
+    q = torch.randn(B, Hkv * G, T, d, generator=g).bfloat16()
+    run = lambda: fa.tree_attention(q.to(dev), kc, vc, table, hist.to(dev), k_scale=ks, v_scale=vs)
+    o, lse = run()
+    status_ok()
+    for b in (0, 1, B - 1):  # the values, where every draft sees those before it
+        h = int(hist[b])
+        kk, vv = (R.quantise(R.f64(x[b, :, :h + T]), fmt) for x in (k, v))
+        ref, ref_l, size, score = R.attention(R.f64(q[b]), kk, vv, R.sees(h, T, T, None), d ** -0.5)
+        # one rounding of each weight and of the result to bf16, scores in fp32
+        off = 2.0 ** -20 * (1 + score)
+        tol = (R.HALF_BF16 + 2 * off[..., None]) * size + R.HALF_BF16 * abs(ref) + 1e-30
+        assert (abs(R.f64(o[b]) - ref) <= tol).all()
+        assert (abs(R.f64(lse[b]) - ref_l) <= off + 2.0 ** -20 * abs(ref_l)).all()
+    for _ in range(30):
+        again = run()
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    status_ok()
