@@ -127,7 +127,9 @@ FA_DEV void stage_weights(float (&w)[2][D], const float* wq, const float* wk) {
 // is the other element of the pair and s carries the sign.  Adjacent pairs:
 // x' is the neighbour in the same packed word.  Half pairs (i, i + rot / 2):
 // x' sits `hop` lanes away (rot is a multiple of 16, so a half is a whole
-// number of lanes).  Elements from `rot` on have c = 1, s = 0.
+// number of lanes).  Elements from `rot` on are their own x' with
+// c = s = 1/2 (x w / 2 twice is x w to the bit; with s = 0 an infinite x'
+// would make them NaN).
 template <int D, bool INTER>
 struct Turn {
   uint64_t c[4], s[4];
@@ -149,7 +151,7 @@ struct Turn {
   template <bool BACK>
   FA_DEV void load(uint32_t at, uint32_t pitch) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = f2_pack(1.f, 1.f), s[i] = f2_pack(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) c[i] = s[i] = f2_pack(0.5f, 0.5f);
     if (!in) return;
     auto four = [&](int i, uint64_t& a, uint64_t& b) {
       const uint4 v = ld_shared_v4(at + i * pitch);
@@ -183,9 +185,11 @@ struct Turn {
 
   // x' of a packed piece; all lanes of the warp
   FA_DEV uint4 swap(const uint4& v) const {
-    if (INTER)
-      return make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032),
-                        __byte_perm(v.z, 0, 0x1032), __byte_perm(v.w, 0, 0x1032));
+    if (INTER) {
+      const uint32_t sel = in ? 0x1032u : 0x3210u;
+      return make_uint4(__byte_perm(v.x, 0, sel), __byte_perm(v.y, 0, sel),
+                        __byte_perm(v.z, 0, sel), __byte_perm(v.w, 0, sel));
+    }
     return make_uint4(__shfl_sync(0xffffffffu, v.x, partner), __shfl_sync(0xffffffffu, v.y, partner),
                       __shfl_sync(0xffffffffu, v.z, partner),
                       __shfl_sync(0xffffffffu, v.w, partner));
@@ -199,7 +203,7 @@ struct Turn {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       c[i] = f2_mul(c[i], own[i]);
-      if (INTER) {
+      if (INTER && in) {
         float a, b;
         f2_unpack(own[i], a, b);
         others[i] = f2_pack(b, a);

@@ -172,3 +172,72 @@ def test_two_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def places(n):
+    """Where a test puts its infinities: in the rotated part, on both sides
+    of its end, in the same pair of elements, in the last ones."""
+    return [n - 1, n, n + 1, n + 2, n + 9]
+
+
+@pytest.mark.parametrize("d,rot", [(64, 16), (64, 48), (128, 32), (128, 64), (128, 112)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_infinities_beside_elements_that_are_not_rotated(d, rot, inter):
+    """Elements from `rot` on are only normed: an infinite neighbour leaves
+    them as the formula has them (forward: zeros beside a NaN; gradients and
+    the sums of their columns: finite)."""
+    dev = device()
+    B, H, N = 1, len(places(rot)), 5
+    g = torch.Generator().manual_seed(rot)
+    x = torch.randn(B, H, N, d, generator=g).bfloat16()
+    gq = torch.randn(B, H, N, d, generator=g).bfloat16()
+    w = (1 + 0.3 * torch.randn(d, generator=g))
+    cos, sin = R.tables(N, rot)
+    bad, gbad = x.clone(), gq.clone()
+    for h, at in enumerate(places(rot)):
+        bad[0, h, 2, at] = float("inf") * (-1) ** h
+        gbad[0, h, 3, at] = float("inf") * (-1) ** h
+    c, s = angles(cos, sin, None, B, N)
+    y, _ = fa.qk_norm_rope(bad.to(dev), x.to(dev), w.to(dev), w.to(dev), cos.to(dev), sin.to(dev),
+                           eps=EPS, interleaved=inter)
+    status_ok()
+    with np.errstate(invalid="ignore"):
+        want = R.norm_rope(R.f64(bad), R.f64(w), c, s, rot, inter, EPS)
+    got = R.f64(y)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    fine = ~np.isnan(want)
+    # as test_forward; a pair's turn keeps its length
+    tol = R.HALF_BF16 * np.abs(want) + 2.0 ** -18 * 2 * np.nanmax(np.abs(want), -1, keepdims=True)
+    assert (np.abs(got - want) <= tol)[fine].all()
+    dq, _, dwq, _ = fa.qk_norm_rope_backward(gbad.to(dev), gq.to(dev), x.to(dev), x.to(dev),
+                                             w.to(dev), w.to(dev), cos.to(dev), sin.to(dev),
+                                             eps=EPS, interleaved=inter)
+    status_ok()
+    with np.errstate(invalid="ignore"):
+        want, want_w, _, size_w = R.norm_rope_backward(R.f64(gbad), R.f64(x), R.f64(w), c, s, rot,
+                                                       inter, EPS)
+    # a row with an infinite gradient has a NaN or infinite mean and is no
+    # number anywhere; the columns of dw that no infinity reaches are
+    got_w = R.f64(dwq)
+    assert np.array_equal(np.isnan(got_w), np.isnan(want_w))
+    fine = np.isfinite(want_w)
+    assert fine.sum() >= d - 2 * H
+    assert np.array_equal(got_w[np.isinf(want_w)], want_w[np.isinf(want_w)])
+    assert (np.abs(got_w[fine] - want_w[fine]) <= 2.0 ** -15 * size_w[fine] + 1e-30).all()
+    rows = [n for n in range(N) if n != 3]
+    assert np.isfinite(R.f64(dq)[:, :, rows]).all() and not np.isfinite(R.f64(dq)[:, :, 3]).any()
+
+
+def test_infinite_weights_stay_in_their_columns():
+    """An infinite or NaN weight of an element that is not rotated reaches
+    that column alone."""
+    dev = device()
+    for inter in (False, True):
+        x = torch.ones(1, 1, 3, 64, dtype=torch.bfloat16, device=dev)
+        w = torch.ones(64, device=dev)
+        w[40], w[51] = float("inf"), float("nan")
+        cos, sin = (t.to(dev) for t in R.tables(3, 32))
+        y, _ = fa.qk_norm_rope(x, x, w, w, cos, sin, interleaved=inter)
+        status_ok()
+        assert torch.isposinf(y[..., 40]).all() and torch.isnan(y[..., 51]).all()
+        assert torch.isfinite(y).sum() == 3 * 62
