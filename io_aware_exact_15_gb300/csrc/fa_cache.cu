@@ -40,7 +40,8 @@ struct CacheParams {
 
 // Index of (page, head, row) for token n of sequence b, or -1: past the
 // sequence's count, outside the table, or a page id outside the pool.
-FA_DEV long long cache_row(const CacheParams& p, int b, int h, int n, int start, int count) {
+FA_DEV long long cache_row(const CacheParams& p, int b, int h, uint32_t n, int start,
+                           uint32_t count) {
   const long long pos = static_cast<long long>(start) + n;
   if (n >= count || start < 0 || (pos >> p.log_page) >= p.max_pages) return -1;
   const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (pos >> p.log_page)];
@@ -57,13 +58,15 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
   grid_dep_launch();
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = warps * RPW * U, chunks = (p.N + per - 1) / per;
+  const int per = warps * RPW * U, chunks = (p.N - 1) / per + 1;
   const int bkh = blockIdx.x / chunks, chunk = blockIdx.x - bkh * chunks;
   const int b = bkh / (2 * p.Hkv), kh = bkh - b * 2 * p.Hkv;
   const bool isk = kh < p.Hkv;
   const int h = isk ? kh : kh - p.Hkv;
-  const int start = p.start[b], count = p.counts ? min(p.counts[b], p.N) : p.N;
-  const int n0 = chunk * per + warp * RPW * U + lane / LPR, l = lane % LPR;
+  const int start = p.start[b], l = lane % LPR;
+  // (unsigned: N may be close to 2^31, and the last block reaches past it)
+  const uint32_t count = p.counts ? max(min(p.counts[b], p.N), 0) : p.N;
+  const uint32_t n0 = static_cast<uint32_t>(chunk) * per + warp * RPW * U + lane / LPR;
   const Strides s = isk ? p.sk : p.sv;
   uint16_t* x0 = static_cast<uint16_t*>(isk ? p.k : p.v) + b * s.b + h * s.h + 8 * l;
   uint8_t* cache = static_cast<uint8_t*>(isk ? p.kc : p.vc);
@@ -156,7 +159,7 @@ cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   // lane 65.7).
   const bool wide = p.N > 8 * RPW;
   const int warps = wide ? 4 : (p.N + RPW - 1) / RPW, per = warps * RPW * (wide ? 8 : 1);
-  const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N + per - 1) / per);
+  const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N - 1) / per + 1);
   if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(warps * 32);
   return wide ? launch_pdl(fa_cache_kernel<D, FMT, WRITE, 8>, grid, block, 0, stream, p)

@@ -214,3 +214,34 @@ def test_largest_numbers_saturate(fmt):
     half = 64 * 2.0 ** 121 if fmt == R.INT8 else 256 * 2.0 ** 119
     want = torch.tensor([most, -most, half, 2.0 ** 121] + [0.0] * 60, dtype=torch.float64)
     assert torch.equal(y[0, 0].double().cpu(), want.expand(16, 64))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_row_counts_next_to_the_largest(fmt, d):
+    """N = 2^31 - 2 for one head (the largest that is accepted), its rows one
+    row of memory: the tokens that exist are written, up to the table's end,
+    and nothing else."""
+    dev = device()
+    N, page, num = 2 ** 31 - 2, 16, 6
+    g = torch.Generator().manual_seed(d)
+    k, v = (torch.randn(1, 1, 1, d, generator=g).bfloat16() for _ in range(2))
+    kd, vd = (t.to(dev).expand(1, 1, N, d) for t in (k, v))
+    table = torch.tensor([[4, 2, 0, 5]], dtype=torch.int32, device=dev)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+    for start, count, most in ((5, 41, 46), (3, None, 64), (0, 0, 0), (50, N, 64)):
+        kc, vc, ks, vs = empty_cache(num, 1, page, d, fmt, dev)
+        before = [host_bytes(t) for t in (kc, vc, ks, vs)]
+        fa.cache_append(kd, vd, kc, vc, table, i32(start), None if count is None else i32(count),
+                        ks, vs)
+        back = fa.cache_read(kc, vc, table, i32(start), 70, i32(max(most - start, 0)), ks, vs)
+        status_ok()
+        for x, y in zip((k, v), back):
+            want = R.quantise(R.f64(x), fmt)[0, 0, 0]
+            n = max(most - start, 0)
+            assert np.array_equal(R.f64(y)[0, 0, :n], np.tile(want, (n, 1)))
+        own = torch.zeros(num, 1, page, dtype=torch.bool)
+        R.place(own, table.cpu(), 0, start, torch.ones(1, max(most - start, 0), dtype=torch.bool))
+        for t, was in zip((kc, vc), before[:2]):
+            now = host_bytes(t).reshape(num, 1, page, -1)
+            assert torch.equal(now[~own], was.reshape(now.shape)[~own])
