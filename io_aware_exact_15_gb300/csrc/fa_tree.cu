@@ -130,17 +130,6 @@ struct TreeSmem {
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
-FA_DEV uint32_t ld_shared_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-FA_DEV uint2 ld_shared_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 template <int D, int FMT, bool PAIR>
 __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,

@@ -193,6 +193,17 @@ FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const S
   return (w & low_bits(s.nd - d0)) | low_bits(-d0);
 }
 
+FA_DEV uint32_t ld_shared_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+FA_DEV uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // untiled bulk copy (16-byte aligned, a multiple of 16 bytes)
 FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(

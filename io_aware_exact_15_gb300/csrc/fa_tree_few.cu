@@ -128,17 +128,6 @@ FA_DEV uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-FA_DEV uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-FA_DEV uint2 lds_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 // over the eight lanes of a row (the same lane % 4)
 FA_DEV float lanes_max(float v) {
 #pragma unroll
@@ -378,8 +367,8 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
         const uint32_t sc = sb + L::SC + stage * 256 + sub * kFewKeys;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          fk[x] = scale_value(lds_u8(sc + 8 * x + k_own));
-          ev[x] = scale_exponent(lds_u8(sc + 128 + 8 * x + k_own));
+          fk[x] = scale_value(ld_shared_u8(sc + 8 * x + k_own));
+          ev[x] = scale_exponent(ld_shared_u8(sc + 128 + 8 * x + k_own));
         }
       }
       uint32_t pf[RT][2];  // P^T operands: keys 0-7, 8-15
@@ -493,7 +482,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
             v[x][0] = y.x, v[x][1] = y.y, v[x][WV - 2] = y.z, v[x][WV - 1] = y.w;
           } else {
             const int u = (g & 1) + 4 * ((g >> 1) & 1) + 2 * (g >> 2);
-            const uint2 y = lds_v2(va + row * 64 + (((u >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (u & 1));
+            const uint2 y = ld_shared_v2(va + row * 64 + (((u >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (u & 1));
             v[x][0] = y.x, v[x][1] = y.y;
           }
           if (tail && row >= nval)
