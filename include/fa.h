@@ -290,7 +290,9 @@ fa_status fa_blocksparse_backward(const void* q, const void* k, const void* v, c
  *     elements; c, s = row `position` of cos, sin
  * pairs: (i, i + rot/2) with interleaved = 0, (2i, 2i + 1) otherwise, i the
  * column of the tables.  Elements from `rot` on are only normed.  Sums and
- * products are fp32 with one rounding to bf16 at the end.
+ * products are fp32 with one rounding to bf16 at the end; where a row's
+ * squares add up to more than fp32 holds (finite elements from about 1.8e19
+ * on), its factor 1 / sqrt is 0.
  *   q, k          bf16 [B, H, N, d] and [B, Hkv, N, d], any strides (below)
  *   wq, wk        fp32 [d]
  *   cos, sin      fp32 [table_rows, rot/2]
@@ -325,6 +327,7 @@ size_t fa_qk_norm_rope_workspace_size(int d);
  *        dwq, dwk        fp32 [d], sums over every row, written whole; in a
  *        fixed order (the same bits from call to call on one device)
  *   workspace / workspace_bytes: as fa_backward.  Enqueues two kernels.
+ * Outputs must not overlap inputs or each other.
  */
 fa_status fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,
                                    const void* k, const float* wq, const float* wk,
@@ -343,20 +346,22 @@ fa_status fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const
  *   page_table        int32 [B, max_pages]: position p of sequence b is row
  *                     p mod page_size of page page_table[b][p / page_size]
  * page_size 16, 32, 64 or 128; max_pages * page_size <= 2^30 and
- * num_pages * Hkv < 2^31; caches and scales 16-byte aligned.  Sequences may share pages
- * that they only read.
+ * num_pages * Hkv < 2^31; caches and scales 16-byte aligned.  Sequences may
+ * share pages that they only read.
  *
  * Formats: FA_CACHE_BF16 keeps rows as they are.  FA_CACHE_E4M3 and
  * FA_CACHE_INT8 keep 8-bit numbers and one scale byte s per row (token,
  * head, key or value), the value being number * 2^(s - 127): the smallest
  * power of two that keeps the row within +-448 (+-127), at least 2^-100,
  * then round to nearest, ties to even.  (The power is at most 2^119, 2^121,
- * where the largest number is still finite in bf16; larger values saturate.)
+ * where the largest number is still finite in bf16; larger values saturate.
+ * At 2^-100 numbers below half of 2^-109 (e4m3) or of 2^-100 (int8) become
+ * zero, and rows of little more than that keep fewer bits.)
  * What reads back is exact in bf16, and storing it again gives the same
- * values, so tokens can be moved by reading and appending them.  A row that holds a NaN or an infinity is
- * stored with s = 255 and reads back as NaN in all its elements.  The e4m3
- * code of NaN (0x7f, 0xff) is never written; what it stands for in a cache
- * filled by other means is not specified.
+ * values, so tokens can be moved by reading and appending them.  A row that
+ * holds a NaN or an infinity is stored with s = 255 and reads back as NaN in
+ * all its elements.  The e4m3 code of NaN (0x7f, 0xff) is never written; what
+ * it stands for in a cache filled by other means is not specified.
  */
 typedef enum fa_cache_format {
   FA_CACHE_BF16 = 0,
@@ -369,10 +374,11 @@ typedef enum fa_cache_format {
  * start[b] + n, for n < counts[b].
  *   k, v     bf16 [B, Hkv, N, d], strides as in fa_qk_norm_rope (6: k, v)
  *   start    int32 [B];  counts  int32 [B], or null for N in every sequence
- * Positions below 0 or from max_pages * page_size on, and page ids outside
- * [0, num_pages), are skipped.  Nothing else of the cache is touched.  Two
- * tokens for the same row of a page: one of them is kept, element by
- * element undefined which.  B*Hkv*(N + 1) < 2^31, B*Hkv <= 2^28.
+ * Sequences with start[b] < 0 (all their tokens), positions from max_pages *
+ * page_size on, and page ids outside [0, num_pages), are skipped.  Nothing
+ * else of the cache is touched.  Two tokens of one call for the same row of a
+ * page leave that row undefined (each element is one token's, in the 8-bit
+ * formats with the scale of either).  B*Hkv*(N + 1) < 2^31, B*Hkv <= 2^28.
  */
 fa_status fa_cache_append(const void* k, const void* v, const int* page_table, const int* start,
                           const int* counts, void* k_cache, void* v_cache, uint8_t* k_scale,

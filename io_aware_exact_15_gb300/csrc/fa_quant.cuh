@@ -8,8 +8,10 @@
 // byte is e + 127.  A power of two scales
 // without rounding, so there is one rounding per element, the same in any
 // precision, and what reads back is exact in bf16 (e4m3 has 4 significant
-// bits, int8 at most 7; e >= -100 keeps numbers and scales
-// far from the ends of fp32's range).  Storing what was read back gives the same numbers
+// bits, int8 at most 7).  e >= -100 keeps numbers, scales and the products
+// of a score's factors far from the ends of fp32's range; it costs rows whose
+// largest number is below 2^-91 (e4m3) or 2^-93 (int8) bits, and all of them
+// from 2^-110 (2^-101) on.  Storing what was read back gives the same numbers
 // again.  A row with a NaN or an infinity gets the scale byte 255 and reads
 // back as NaN whole.
 #pragma once
