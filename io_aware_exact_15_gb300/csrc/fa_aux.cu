@@ -252,12 +252,14 @@ cudaError_t launch_build_lists(const uint8_t* mask, int mask_heads, int nT, int*
 // items of 8 consecutive elements of a row (16-byte loads of O and dO); the
 // D/8 threads of a row reduce with shuffles.  Every thread keeps
 // kUnroll grid-stride items in flight, and the grid is sized so that each
-// thread has about that many; the zeros are stored while they come (8 x 16 x
-// 512 rows of 64, forward + backward: 62.7 us, zeros first 63.8).
+// thread has about that many; the zeros are stored while they come.
 // Nothing is written before the wait: this memory may be what the previous
 // kernel still reads, another call's workspace or a tensor freed after that
-// call (zeros before the wait: 61.3 us, and a norm backward's partial sums
-// could be cleared before they were added).
+// call.  dO is only asked for into L2, which is coherent whoever writes it.
+// 8 x 16 x 512 rows of 64, forward + backward, us in a loop | with L2 flushed
+// before each step: 61.9 | 69.2; without the prefetch 62.7 | 71.3; zeros
+// before the rows' loads as well 63.8; zeros before the wait, which is not
+// sound, 61.3 | 69.3.
 constexpr int kUnroll = 4;
 
 template <int D>
@@ -267,11 +269,18 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const uint4* __restrict
                                                          float4* __restrict__ dq_acc,
                                                          int* __restrict__ zero_i, long long nzero,
                                                          long long rows) {
-  grid_dep_wait();  // the previous kernels' accesses are over from here on
-  grid_dep_launch();
   constexpr int TPR = D / 8;  // threads per row: 8 or 16
   const long long total = rows * TPR;
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  if ((threadIdx.x & 7) == 0)  // one per 128 bytes
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long t =
+          static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x + u * stride;
+      if (t < total) asm volatile("prefetch.global.L2 [%0];" ::"l"(dO + t));
+    }
+  grid_dep_wait();  // the previous kernels' accesses are over from here on
+  grid_dep_launch();
   for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < nzero;
        t += stride)
     zero_i[t] = 0;  // counters of the backward's split last round

@@ -92,9 +92,9 @@ FA_DEV void drain_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
 // scheduled (grid_dep_launch).  Without that launch attribute both are no-ops.
 // There is no exception: a kernel that writes before its wait, were it only
 // zeros into its own workspace, races with a previous kernel that still uses
-// that memory (the same workspace, or a tensor freed after its launch).  A
-// kernel may leave grid_dep_launch out; the next one then starts when it is
-// done.
+// that memory (the same workspace, or a tensor freed after its launch).  (A
+// prefetch into L2 returns nothing and may come before the wait.)  A kernel
+// may leave grid_dep_launch out; the next one then starts when it is done.
 FA_DEV void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 FA_DEV void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
