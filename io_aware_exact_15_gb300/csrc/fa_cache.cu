@@ -13,8 +13,8 @@
 // a shuffle reduction, and a warp's rows are consecutive positions of one
 // (sequence, head), so that data and scale bytes land next to each other.
 // Measured: 16 x 4096 tokens of 4 heads of 128, appended as int8 and read
-// back, ragged: 56.6 us, 4.6 TB/s (the bytes at a plain copy's rate: 39.1
-// us).  Full rows: append bf16 6.4, e4m3 and int8 4.9 TB/s, read 6.3 and 5.8:
+// back, ragged: 54.9 us, 4.8 TB/s (the bytes at a plain copy's rate: 39.1
+// us).  Full rows: append bf16 6.5, e4m3 5.2, int8 4.9 TB/s, read 6.4, 6.1, 6.0:
 // finding the scale and rounding is what the 8-bit append adds (int8 by
 // conversions to integers: 4.3), the rest latency: lengths, then the page,
 // then rows, one wave of blocks after the other.  Persistent warps that ask

@@ -27,8 +27,8 @@
 // lost the time between a block's loads.
 //
 // Measured, packed input, 16 + 4 heads of 128: forward of 4 x 4096 tokens
-// 34.5 us, 5.1 TB/s (8 x 8192: 122.6 us, 5.5 TB/s; a plain copy of the 4 x
-// 4096 tokens' bytes takes 29.0); backward of 4 x 4096 tokens 49.3 us,
+// 34.6 us, 5.1 TB/s (8 x 8192: 122.6 us, 5.5 TB/s; a plain copy of the 4 x
+// 4096 tokens' bytes takes 29.0); backward of 4 x 4096 tokens 49.6 us,
 // 5.3 TB/s.  What is left is the instructions: without the arithmetic, the
 // same loads and stores take 32.5 us, and a warp's step is a chain (load,
 // sum over the lanes, scale, store) that 4 warps of a scheduler do not

@@ -35,9 +35,9 @@
 //
 // Measured (ragged lengths, heads of 128; the bytes at a plain copy's rate in
 // brackets): 8 x 23 drafts of 16 + 4 heads over up to 16384 keys, bf16, 92
-// rows: 48.0 us (27.0), 3.8 TB/s; what is left are the ends of parts and the
+// rows: 47.6 us (27.0), 3.8 TB/s; what is left are the ends of parts and the
 // join.  2 x 16 drafts over up to 131072 keys, e4m3, 64 rows: 115 us (33.0);
-// 16 x 64 drafts over up to 8192 keys, int8, 256 rows: 79.0 us (15.2, by the
+// 16 x 64 drafts over up to 8192 keys, int8, 256 rows: 79.1 us (15.2, by the
 // products); both wait for widened tiles: issue slots 52 and 42 % busy.
 //
 // Keys that nobody may see are never left to chance: scores are replaced by

@@ -42,8 +42,8 @@
 // operations per two elements against one or two.
 //
 // Measured: 32 sequences x 1 token, 16 + 4 heads of 128, up to 8192 e4m3
-// keys: 40.7 us, 4.2 TB/s (the bytes at a plain copy's rate: 25.8); 256
-// sequences of 500 keys 47.8 (20.0).  Issue slots are 44 % busy, the
+// keys: 40.8 us, 4.2 TB/s (the bytes at a plain copy's rate: 25.8); 256
+// sequences of 500 keys 47.7 (20.0).  Issue slots are 44 % busy, the
 // ALU 46 %; the rest is the chain of a chunk and the ends of problems.
 #include <math.h>
 #include <stdint.h>
