@@ -195,6 +195,42 @@ fa_status fa_backward_varlen(const void* q, const void* k, const void* v, const 
                              size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Causal attention over a sliding window with a few first tokens that stay
+ * visible ("sinks"): query i sees key j when j <= i and (i - j < window or
+ * j < sinks); window 1 is the token itself, window >= the length plain causal
+ * attention.  Tiles without a visible pair are not visited.
+ *   equal lengths  cu_seqlens null, total 0; tensors [B, H, N, d], k, v, dk,
+ *                  dv [B, Hkv, N, d], lse [B, H, N]
+ *   packed         cu_seqlens int32 [B+1] as in fa_forward_varlen, N the
+ *                  longest length (1 <= N <= total); tensors [H, total, d] and
+ *                  [Hkv, total, d], lse [H, total].  The sequences need not
+ *                  reach `total`: rows in front of the first and behind the
+ *                  last are neither used nor written, whatever they hold.
+ *                  total = 0 returns FA_OK with nothing launched
+ * Grouped heads as in fa_forward_gqa.  A row's results depend on the rows that
+ * it sees (dk, dv: that see it) alone: a NaN or an infinity anywhere else does
+ * not reach it.  window >= 1, 0 <= sinks <= 1024 (more: FA_ERR_UNSUPPORTED);
+ * B * H times the 128-row tiles (with those of the sinks, counted once per
+ * 8 tiles or window) below 2^23.  Other rules as fa_forward / fa_backward;
+ * outputs must not overlap inputs or each other.
+ * The backward enqueues three kernels; dq is summed with fp32 atomics, dk and
+ * dv in a fixed order.  Workspace: fa_backward_window_workspace_size bytes for
+ * the same sizes (0 for sizes that the calls refuse): D and the fp32 dQ
+ * accumulator as in fa_backward, a bit per key row, and, where sequences are
+ * longer than 8 tiles and the window, fp32 sums of the sinks' tiles.
+ */
+fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o, float* lse,
+                            const int* cu_seqlens, int B, int H, int Hkv, int N, int total, int d,
+                            float scale, int window, int sinks, cudaStream_t stream);
+size_t fa_backward_window_workspace_size(int B, int H, int Hkv, int N, int total, int d,
+                                         int window, int sinks);
+fa_status fa_backward_window(const void* q, const void* k, const void* v, const void* o,
+                             const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                             const int* cu_seqlens, int B, int H, int Hkv, int N, int total, int d,
+                             float scale, int window, int sinks, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Deterministic backward: dQ, dK, dV identical bit for bit from run to run
  * (fa_backward sums dQ with unordered fp32 atomic adds, so its dQ may differ
  * in the last bits between runs).  Two passes after the D preprocess:

@@ -43,6 +43,7 @@ EXPORTS = (
     "fa_forward_dropout", "fa_backward_dropout", "fa_backward_deterministic",
     "fa_qk_norm_rope", "fa_qk_norm_rope_workspace_size", "fa_qk_norm_rope_backward",
     "fa_cache_append", "fa_cache_read", "fa_tree_attention_workspace_size", "fa_tree_attention",
+    "fa_forward_window", "fa_backward_window_workspace_size", "fa_backward_window",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -115,6 +116,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "fa_cache_read": ([P] * 9 + [I] * 8 + [P], I),
             "fa_tree_attention_workspace_size": ([I] * 5, Z),
             "fa_tree_attention": ([P] * 11 + [I] * 9 + [F, P, Z, P], I),
+            "fa_forward_window": ([P] * 6 + [I] * 6 + [F, I, I, P], I),
+            "fa_backward_window_workspace_size": ([I] * 8, Z),
+            "fa_backward_window": ([P] * 10 + [I] * 6 + [F, I, I, P, Z, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -332,6 +336,24 @@ def fa_tree_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_le
         page_size, max_pages, float(scale), _p(workspace), int(workspace_bytes), _s(stream))
 
 
+def fa_forward_window(q, k, v, o, lse, cu_seqlens, B, H, Hkv, N, total, d, scale, window, sinks,
+                      stream=None) -> int:
+    return load().fa_forward_window(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_seqlens), B, H, Hkv,
+                                    N, total, d, float(scale), window, sinks, _s(stream))
+
+
+def fa_backward_window_workspace_size(B, H, Hkv, N, total, d, window, sinks) -> int:
+    return load().fa_backward_window_workspace_size(B, H, Hkv, N, total, d, window, sinks)
+
+
+def fa_backward_window(q, k, v, o, dO, lse, dq, dk, dv, cu_seqlens, B, H, Hkv, N, total, d, scale,
+                       window, sinks, workspace, workspace_bytes, stream=None) -> int:
+    return load().fa_backward_window(_p(q), _p(k), _p(v), _p(o), _p(dO), _p(lse), _p(dq), _p(dk),
+                                     _p(dv), _p(cu_seqlens), B, H, Hkv, N, total, d, float(scale),
+                                     window, sinks, _p(workspace), int(workspace_bytes),
+                                     _s(stream))
+
+
 def fa_get_device_status(stream=None) -> int:
     return load().fa_get_device_status(_s(stream))
 
@@ -387,15 +409,52 @@ def _varlen_shape(q, k, cu_seqlens, max_seqlen):
     return B, H, int(k.shape[0]), T, d, int(max_seqlen)
 
 
+def _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen):
+    """(B, H, Hkv, N, total, d) of a call with a window, its tensors checked."""
+    import torch
+    if not causal or block_mask is not None or dropout_p:
+        raise ValueError("a window needs causal=True and goes without block masks and dropout")
+    bf16 = (torch.bfloat16,)
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1:
+            raise ValueError("cu_seqlens: expected [B + 1]")
+        _want("cu_seqlens", cu_seqlens, cu_seqlens.shape, (torch.int32,), q)
+        B, H, Hkv, total, d, N = _varlen_shape(q, k, cu_seqlens, max_seqlen)
+        N = max(N, 1) if total else 0  # (every sequence may be empty)
+        lead, rows = (), total
+    else:
+        B, H, N, d = _shape(q)
+        Hkv, total = int(k.shape[1]) if k.dim() == 4 else 0, 0
+        lead, rows = (B,), N
+    _want("q", q, (*lead, H, rows, d), bf16, q)
+    _want("k", k, (*lead, Hkv, rows, d), bf16, q)
+    _want("v", v, (*lead, Hkv, rows, d), bf16, q)
+    return B, H, Hkv, N, total, d
+
+
 def attention_forward(q, k, v, scale=None, causal=False, block_mask=None, workspace=None,
                       stream=None, cu_seqlens=None, max_seqlen=None, dropout_p=0.0, seed=0,
-                      offset=0):
+                      offset=0, window=None, sinks=0):
     """(o, lse) for bf16 CUDA tensors q [B, H, N, d] and k, v [B, Hkv, N, d]
     (Hkv = H, or a divisor of H for grouped heads).  With cu_seqlens (int32
     CUDA tensor [B+1]) the batch is packed: q [H, total, d], k, v
     [Hkv, total, d], lse [H, total].  dropout_p > 0: dropout on P with the
-    Philox keep rule of (seed, offset); the backward must get the same."""
+    Philox keep rule of (seed, offset); the backward must get the same.
+    window (with causal=True): each query sees the last `window` keys, itself
+    included, and the first `sinks` keys of its sequence; the packed sequences
+    may then end before `total` (rows that belong to none are not written)."""
     import torch
+    if window is not None:
+        sizes = _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen)
+        scale = (1.0 / sizes[-1] ** 0.5) if scale is None else scale
+        with _launch_on(q, stream) as s:
+            o = torch.empty_like(q)
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+            _check(fa_forward_window(q, k, v, o, lse, cu_seqlens, *sizes, scale, window, sinks, s),
+                   "fa_forward_window")
+        return o, lse
+    if sinks:
+        raise ValueError("sinks apply to a window")
     if cu_seqlens is not None:
         if block_mask is not None:
             raise ValueError("block masks apply to equal-length batches only")
@@ -437,9 +496,26 @@ def attention_forward(q, k, v, scale=None, causal=False, block_mask=None, worksp
 
 def attention_backward(q, k, v, o, dO, lse, scale=None, causal=False, block_mask=None,
                        workspace=None, stream=None, cu_seqlens=None, max_seqlen=None,
-                       dropout_p=0.0, seed=0, offset=0):
+                       dropout_p=0.0, seed=0, offset=0, window=None, sinks=0):
     """(dq, dk, dv) of sum(O * dO); shapes and options as attention_forward."""
     import torch
+    if window is not None:
+        sizes = _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen)
+        _want("o", o, q.shape, (torch.bfloat16,), q)
+        _want("dO", dO, q.shape, (torch.bfloat16,), q)
+        _want("lse", lse, q.shape[:-1], (torch.float32,), q)
+        scale = (1.0 / sizes[-1] ** 0.5) if scale is None else scale
+        with _launch_on(q, stream) as s:
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+            if workspace is None:
+                workspace = torch.empty(fa_backward_window_workspace_size(*sizes, window, sinks),
+                                        dtype=torch.uint8, device=q.device)
+            _check(fa_backward_window(q, k, v, o, dO, lse, dq, dk, dv, cu_seqlens, *sizes, scale,
+                                      window, sinks, workspace, _bytes(workspace, q), s),
+                   "fa_backward_window")
+        return dq, dk, dv
+    if sinks:
+        raise ValueError("sinks apply to a window")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if cu_seqlens is not None:
         if block_mask is not None:

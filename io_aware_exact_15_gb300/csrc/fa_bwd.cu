@@ -32,6 +32,11 @@
 // CTAs round-robin in zig-zag (dense, causal) or, with a block mask, handed
 // out at run time from a counter (their lengths can differ by dozens of
 // times).
+// Sliding windows (kind kWindow): a key tile's walk ends where the windows no
+// longer reach back to it; the tiles of the first keys that stay visible are
+// walked to the end of the sequence, in parts of about a window's length (one
+// such walk would outlast everything else), whose fp32 dV, dK the last kernel
+// adds up (fa_window.cu).
 // TMEM: S [0,128) dP [128,256) dV [256,256+d) dK [256+d,256+2d);
 //       dQ at [384,448) for d = 64 and over the dP columns for d = 128.
 #include <math.h>
@@ -106,15 +111,25 @@ struct BwdUnit {
   int bq0;      // first query slice of the group
   int bh_base;  // b * H when query slices are heads (variable-length batch)
   int nT;       // tiles of the sequence
+  int bkv;      // b * Hkv + key/value head
+  int q0, q1;   // window: query tiles
+  int slot;     // window: where a part of a first tile leaves its sums, or -1
 };
 
 // Unit u -> its geometry.  False when the key tile lies past the end of its
 // (variable-length) sequence; every role of the CTA skips such a unit alike.
-template <bool GQA, bool SPARSE>
+template <bool GQA, bool SPARSE, bool WIN>
 FA_DEV bool bwd_unit(int u, const BwdParams& p, int Hkv, int G, int ntmax, bool varlen,
                      int nlong, BwdUnit& w) {
   int bkv;
-  if (SPARSE) {
+  int part = 0;
+  if (WIN) {
+    // the first tiles' parts, then the other tiles, all heads of one together
+    const int v = u / (p.B * Hkv), sunk = p.sink_tiles * p.sink_parts;
+    bkv = u - v * (p.B * Hkv);
+    w.kt = v < sunk ? v / p.sink_parts : p.sink_tiles + v - sunk;
+    part = v < sunk ? v - w.kt * p.sink_parts : 0;
+  } else if (SPARSE) {
     // block mask, key tiles of each head ordered longest first: the nlong
     // long ones of every head come first, rank-major (a kept column of every
     // query tile is a unit as long as dozens of others: started late it
@@ -154,6 +169,19 @@ FA_DEV bool bwd_unit(int u, const BwdParams& p, int Hkv, int G, int ntmax, bool 
     w.bh_base = b * p.H;
   }
   w.nT = (w.N + kTile - 1) / kTile;
+  if (WIN) {
+    w.bkv = bkv;
+    w.slot = -1;
+    w.q0 = w.kt;
+    w.q1 = window_end(w.kt, w.nT, p.window);
+    if (w.kt < p.sink_tiles) {
+      w.q0 = w.kt + part * p.part_tiles;
+      w.q1 = min(w.nT, w.q0 + p.part_tiles);
+      if (w.kt + p.part_tiles < w.nT)
+        w.slot = (bkv * p.sink_tiles + w.kt) * p.sink_parts + part;
+      return w.q0 < w.nT;
+    }
+  }
   return w.kt * kTile < w.N;
 }
 
@@ -194,7 +222,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // (the plain instantiation carries no group arithmetic)
   const int Hkv = GQA ? p.Hkv : p.H;
   const int G = GQA ? p.H / p.Hkv : 1;
-  const int nunits = p.B * Hkv * ntmax;
+  constexpr bool WIN = KIND == kWindow;
+  const int nunits =
+      p.B * Hkv * (WIN ? ntmax + p.sink_tiles * (p.sink_parts - 1) : ntmax);
   constexpr bool DROP = KIND == kGeneralDropout;
   const bool varlen = KIND >= kGeneral && p.cu_seqlens != nullptr;
   const size_t slice_rows = varlen ? static_cast<size_t>(p.total) : static_cast<size_t>(p.N);
@@ -210,7 +240,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // every role of every CTA), read once the lists are visible (below)
   int nlong = 0;
   auto unit_at = [&](int u, BwdUnit& w) {
-    return bwd_unit<GQA, SPARSE>(u, p, Hkv, G, ntmax, varlen, nlong, w);
+    return bwd_unit<GQA, SPARSE, WIN>(u, p, Hkv, G, ntmax, varlen, nlong, w);
   };
   // Split last round: when the last round's units fill at most half the
   // grid, each runs as two halves of its query-tile walk on two CTAs.  Only
@@ -223,7 +253,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int nround = (nunits + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int last0 = (nround - 1) * static_cast<int>(gridDim.x);  // first unit of the last round
   const int mlast = nunits - last0;
-  const bool split = D == 128 && !DYN && p.part != nullptr && !varlen && nround > 1 &&
+  const bool split = D == 128 && !DYN && !WIN && p.part != nullptr && !varlen && nround > 1 &&
                      2 * mlast <= static_cast<int>(gridDim.x) && mlast <= p.nslot &&
                      G * (p.causal ? 1 : ntmax) >= 8;
   // Block mask: units are handed out at run time.  A CTA's first unit is
@@ -280,9 +310,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // the query-tile walk of item (unit w, half uh): half 0 takes the first
   // half of the unit's steps, half 1 the rest (no block mask here, so a
   // unit has G x (nT, or nT - kt when causal) steps)
-  using Sched0 = typename std::conditional<GQA, BwdGroupSchedule, BwdSingleSchedule>::type;
+  using Sched0 = typename std::conditional<
+      WIN, BwdWindowSchedule,
+      typename std::conditional<GQA, BwdGroupSchedule, BwdSingleSchedule>::type>::type;
   auto start = [&](const BwdUnit& w, int uh, BwdPartSchedule<Sched0>& ps) {
-    ps.s.init(w.kt, w.nT, p.causal != 0, p.lists, w.bq0 % p.H, G);
+    if constexpr (WIN)
+      ps.s.init(w.q0, w.q1, G);
+    else
+      ps.s.init(w.kt, w.nT, p.causal != 0, p.lists, w.bq0 % p.H, G);
     ps.left = INT_MAX;
     if (uh >= 0) {
       const int ns = G * (p.causal ? w.nT - w.kt : w.nT);
@@ -601,7 +636,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const size_t idx =
           static_cast<size_t>(w.bq0 + gg) * slice_rows + w.row0 + (row < w.N ? row : 0);
       l_ = p.lse[idx];
-      d_ = p.delta[idx];
+      d_ = WIN && row >= w.N ? 0.f : p.delta[idx];
     };
     // dQ of query tile t (step m): TMEM -> registers, release the columns,
     // then add this thread's D/2 columns into the fp32 accumulator
@@ -760,7 +795,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld_wait();
         reg_fence(sv[0]);
         reg_fence(sv[1]);
-        const bool need_mask = (kcol0 + 64 > N) || (p.causal && kcol0 + 63 > qt * kTile);
+        bool need_mask = (kcol0 + 64 > N) || (p.causal && kcol0 + 63 > qt * kTile);
+        if (WIN)  // some row's window begins behind the first key, not all are sinks
+          need_mask |= kcol0 < qt * kTile + kTile - p.window && kcol0 + 64 > p.sinks;
         // keys kcol0 + i with i >= lim are masked (past N, or after this row
         // when causal)
         int lim = N - kcol0;
@@ -775,7 +812,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 __uint_as_float(sv[i >> 4][(2 * i + 1) & 31])),
                         sl2x2, nlse2x2);
         };
-        if (need_mask) {  // (warp-uniform) the tile crosses N or the diagonal
+        if (WIN && need_mask) {
+          const int lo = qrow - p.window + 1 - kcol0, first = p.sinks - kcol0;
+          const uint32_t vis[2] = {reach_bits(lim, lo, first),
+                                   reach_bits(lim - 32, lo - 32, first - 32)};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float a, b;
+            f2_unpack(arg2(i), a, b);
+            a = (vis[i >> 4] >> ((2 * i) & 31)) & 1u ? ex2(a) : 0.f;
+            b = (vis[i >> 4] >> ((2 * i + 1) & 31)) & 1u ? ex2(b) : 0.f;
+            pw[i] = pack_bf16(a, b);
+          }
+        } else if (need_mask) {  // (warp-uniform) the tile crosses N or the diagonal
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float a, b;
@@ -931,7 +980,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int order = -1;
         float* prow = nullptr;  // this thread's row in the slot
         int* ready = nullptr;
-        if (uh >= 0) {
+        float odd = 0.f;  // WIN: NaN once a number of the row is not finite
+        if (WIN && un.slot >= 0) {  // a part of a first tile's walk
+          order = 0;
+          prow = p.part + (static_cast<size_t>(un.slot) * 2 + (dv_side ? 0 : 1)) * kTile * D +
+                 static_cast<size_t>(r) * D;
+        } else if (!WIN && uh >= 0) {
           const int slot = u - last0;
           ready = p.part_cnt + p.nslot + slot;
           prow = p.part + (static_cast<size_t>(slot) * 2 + (dv_side ? 0 : 1)) * kTile * D +
@@ -977,7 +1031,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                   __uint_as_float(a[v >> 3][4 * (v & 7) + 3]));
             continue;
           }
-          if (order == 1) {  // add the parked half
+          if (WIN)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              odd = fmaf(__uint_as_float(a[0][j]), 0.f, odd);
+              odd = fmaf(__uint_as_float(a[1][j]), 0.f, odd);
+            }
+          if (!WIN && order == 1) {  // add the parked half
             const float4* pr = reinterpret_cast<const float4*>(prow + 64 * c);
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
@@ -1008,7 +1068,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
           __syncwarp();
         }
-        if (ok && order == 0) {  // phase 1: every row parked, then the flag
+        if (WIN && ok && order < 0) {
+          const uint32_t rows = __ballot_sync(0xffffffffu, odd != 0.f && lane < nrows);
+          if (lane == 0)
+            p.bad[((static_cast<size_t>(un.bkv) * ntmax + un.kt) * 2 + (dv_side ? 0 : 1)) * 4 + q4] =
+                rows;
+        }
+        if (!WIN && ok && order == 0) {  // phase 1: every row parked, then the flag
           mbar_arrive(bar(L::B_SPL));
           if (threadIdx.x == 128) {
             if (wait_bar(bar(L::B_SPL), 1, wc)) {
@@ -1053,7 +1119,9 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtens
       L::ALLOC);
   if (e != cudaSuccess) return e;
   const int nT = (p.N + kTile - 1) / kTile;
-  const long long units = static_cast<long long>(nT) * p.B * (p.Hkv > 0 ? p.Hkv : p.H);
+  const long long units =
+      static_cast<long long>(KIND == kWindow ? nT + p.sink_tiles * (p.sink_parts - 1) : nT) * p.B *
+      (p.Hkv > 0 ? p.Hkv : p.H);
   // persistent: one CTA per SM (the CTA holds the SM's TMEM and most of its
   // shared memory), each walking units blockIdx.x, blockIdx.x + grid, ...
   const int sms = sm_count();
@@ -1068,6 +1136,11 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtens
 cudaError_t launch_backward_main(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const CUtensorMap& tdo,
                                  const CUtensorMap& tdq, cudaStream_t stream) {
+  if (p.window) {
+    if (p.d == 64) return launch_bwd_d<64, kWindow>(p, tq, tk, tv, tdo, tdq, stream);
+    if (p.d == 128) return launch_bwd_d<128, kWindow>(p, tq, tk, tv, tdo, tdq, stream);
+    return cudaErrorInvalidValue;
+  }
   const int kind = p.drop.t ? kGeneralDropout
                    : p.cu_seqlens ? kGeneral
                    : (p.Hkv > 0 && p.Hkv != p.H) ? kGrouped : kPlain;

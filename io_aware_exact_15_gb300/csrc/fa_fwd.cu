@@ -38,6 +38,7 @@
 #include "fa_ptx.cuh"
 #include "fa_philox.cuh"
 #include "fa_sched.cuh"
+#include "fa_window.cuh"
 
 namespace fa {
 namespace {
@@ -139,8 +140,10 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
   const size_t slice_rows = varlen ? static_cast<size_t>(p.total) : static_cast<size_t>(p.N);
   const int nT = (N + kTile - 1) / kTile;
 
-  FwdScheduleT<BC> sch;
+  constexpr bool WIN = KIND == kWindow;
+  FwdScheduleT<BC, WIN> sch;
   sch.init(pair, nT, p.causal != 0, p.lists, head, single, (N + BC - 1) / BC);
+  if (WIN) sch.reach(p.window, p.sinks, N);
   // K_j or V_j into ring slot `pos`: CH column chunks of BC / KBOX boxes
   auto load_kv = [&](int pos, const CUtensorMap* m, int kt) {
 #pragma unroll
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
       if (L::QT == 2)
         tma_load_3d(sb + L::Q + L::TILE + c * L::CHUNK, &tq, bar(L::B_Q), 64 * c, row0 + y1, zq);
     }
-    FwdScheduleT<BC> first = sch;  // the first key tile, without advancing sch
+    FwdScheduleT<BC, WIN> first = sch;  // the first key tile, without advancing sch
     int kt0, mem0;
     if (first.next(kt0, mem0)) {
 #pragma unroll
@@ -367,7 +370,9 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
       constexpr int NG = BC / GW;
       constexpr int GC = GW / 32;
       const int kbase = kt * BC;
-      const bool need_mask = (kbase + BC > N) || (p.causal && kbase + BC - 1 > qt * kTile);
+      bool need_mask = (kbase + BC > N) || (p.causal && kbase + BC - 1 > qt * kTile);
+      if (WIN)  // some row's window begins behind the tile's first key, not all are sinks
+        need_mask |= kbase < qt * kTile + kTile - p.window && kbase + BC > p.sinks;
       uint32_t sr[GC][32];
       auto load_group = [&](int g) {
 #pragma unroll
@@ -380,6 +385,18 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
           // row when causal)
           int lim = N - kbase;
           if (p.causal && qrow - kbase + 1 < lim) lim = qrow - kbase + 1;
+          if (WIN) {
+#pragma unroll
+            for (int c = 0; c < GC; ++c) {
+              const int at = g * GW + 32 * c;
+              const uint32_t vis = reach_bits(lim - at, qrow - p.window + 1 - kbase - at,
+                                              p.sinks - kbase - at);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((vis >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
+            }
+            return;
+          }
 #pragma unroll
           for (int c = 0; c < GC; ++c)
 #pragma unroll
@@ -501,6 +518,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
       // warp's rows of Q_s (free: the tile's last S product has completed),
       // then each store writes 4 whole 128-byte row pieces.
       const uint32_t stg = sb + L::Q + s * L::TILE + q4 * 4096;
+      float odd = 0.f;  // NaN once a number of the row is not finite
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t o[2][32];
@@ -514,6 +532,12 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[0][j] = o[1][j] = 0u;
         }
+        if (WIN)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            odd = fmaf(__uint_as_float(o[0][j]) * inv, 0.f, odd);
+            odd = fmaf(__uint_as_float(o[1][j]) * inv, 0.f, odd);
+          }
         const uint32_t st = stg + c * L::CHUNK;
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -536,6 +560,18 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
       if (store)
         p.lse[static_cast<size_t>(zq) * slice_rows + row0 + qrow] =
             has ? (m + lg2(l)) * kLn2 : -INFINITY;
+      if (WIN) {
+        // (a NaN logsumexp: the row sees a key whose score is one)
+        const float lse2 = m + lg2(l);
+        uint32_t again = __ballot_sync(0xffffffffu, store && has && odd != 0.f && lse2 == lse2);
+        for (; again; again &= again - 1) {  // the rows were written by all lanes
+          const int j = __ffs(again) - 1;
+          __syncwarp();
+          window_row_o<D>(p.q, p.k, p.v, p.o, static_cast<size_t>(zq) * slice_rows + row0,
+                          static_cast<size_t>(zkv) * slice_rows + row0, qrow0 + j, p.window,
+                          p.sinks, sl2, __shfl_sync(0xffffffffu, lse2, j));
+        }
+      }
     }
   }
   tc_fence_before();
@@ -613,6 +649,7 @@ cudaError_t launch_forward_kind(int kind, const FwdParams& p, const CUtensorMap&
                                 cudaStream_t stream) {
   if (kind == kGeneralDropout)
     return launch_fwd_d<D, kGeneralDropout, 0, kTile, CMP>(p, tq, tk, tv, stream);
+  if (kind == kWindow) return launch_fwd_d<D, kWindow, 0, kTile, CMP>(p, tq, tk, tv, stream);
   if (kind == kGeneral) return launch_fwd_d<D, kGeneral, 0, kTile, CMP>(p, tq, tk, tv, stream);
   if (kind == kGrouped) return launch_fwd_d<D, kGrouped, 0, kTile, CMP>(p, tq, tk, tv, stream);
   return launch_fwd_d<D, kPlain, 0, kTile, CMP>(p, tq, tk, tv, stream);
@@ -620,7 +657,8 @@ cudaError_t launch_forward_kind(int kind, const FwdParams& p, const CUtensorMap&
 
 cudaError_t launch_forward(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, cudaStream_t stream) {
-  const int kind = p.drop.t ? kGeneralDropout
+  const int kind = p.window ? kWindow
+                   : p.drop.t ? kGeneralDropout
                    : p.cu_seqlens ? kGeneral
                    : (p.Hkv > 0 && p.Hkv != p.H) ? kGrouped : kPlain;
   // Small grids (at most four waves of two-tile CTAs: BERT- or GPT-2-sized

@@ -104,6 +104,10 @@ struct FwdParams {
   const int* cu_seqlens = nullptr;
   int total = 0;
   DropoutParams drop;     // dropout on P (kernels of kind kGeneralDropout)
+  // kind kWindow: causal, key j only where i - j < window or j < sinks; q, k, v
+  // for the rows that are computed again (fa_window.cuh)
+  int window = 0, sinks = 0;  // window 0: another kind
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
   int* err = nullptr;     // device status word
   uint64_t wait_ns = 0;
 };
@@ -133,14 +137,29 @@ struct BwdParams {
   int nslot = 0;
   // block mask: next-unit counter (zero on entry; the preprocess zeroes it)
   int* unit_counter = nullptr;
+  // kind kWindow (as FwdParams).  The first sink_tiles key tiles hold keys
+  // that every later query sees: their walk over the query tiles is cut into
+  // sink_parts units of part_tiles query tiles (of each head of the group),
+  // which leave fp32 dV, dK ([2][128][d] per slot) in `part` when a sequence
+  // has more than one of them.  bad: [B * Hkv][key tiles][dV, dK][4], a bit
+  // per row of a tile that came out with a NaN or an infinity.
+  int window = 0, sinks = 0;
+  int sink_tiles = 0, sink_parts = 0, part_tiles = 0;
+  uint32_t* bad = nullptr;
   int* err = nullptr;
   uint64_t wait_ns = 0;
 };
 
 // Kernel instantiations: plain, grouped K/V, the general one (variable-length
-// or equal-length batch, grouped K/V allowed) and the general one with
-// dropout on P.
-enum KernelKind : int { kPlain = 0, kGrouped = 1, kGeneral = 2, kGeneralDropout = 3 };
+// or equal-length batch, grouped K/V allowed), the general one with dropout
+// on P, and the general one with a sliding window.
+enum KernelKind : int {
+  kPlain = 0,
+  kGrouped = 1,
+  kGeneral = 2,
+  kGeneralDropout = 3,
+  kWindow = 4
+};
 
 // 3-D bf16 view {d, N, B*H} of a [B, H, N, d] tensor, box_rows x 64-column
 // boxes (128 rows except the 64-key tiles of the block-size sweep) with
@@ -183,6 +202,15 @@ struct DqParams {
 cudaError_t launch_backward_dq(const DqParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, const CUtensorMap& tdo,
                                cudaStream_t stream);
+
+// The window backward's last kernel: dq from its accumulator, sums of the
+// parts of the first key tiles, rows computed again (fa_window.cu).
+struct WindowFinish {
+  const void *q = nullptr, *k = nullptr, *v = nullptr, *dO = nullptr;
+  void* dq = nullptr;
+  BwdParams b;
+};
+cudaError_t launch_window_finish(const WindowFinish& w, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const void* o, const void* dO, float* delta, float* dq_acc,
                                   int* zero_i, long long nzero,

@@ -379,6 +379,9 @@ FA_DEV void red_add_v4(float* p, float a, float b, float c, float d) {
                : "memory");
 }
 
+// bits 0 .. n-1
+FA_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // Byte offset of the 16-byte chunk `c16` (0..7) of row `r` inside a 128B-
 // swizzled [rows x 128 B] region.
 FA_DEV uint32_t sw128_offset(int r, int c16) {

@@ -9,10 +9,13 @@
 //   causal    : kt = 0 .. qt1 (tile qt0 stops at kt = qt0): k-tile j holds an
 //               allowed element of query tile i iff j <= i (Br = Bc), which
 //               gives n(n+1)/2 tiles per head for n query tiles
+//   window    : causal, from the first key tile that a row's window reaches;
+//               before it the tiles of the first `sinks` keys
 //   sparse    : merge of the two ascending CSR lists of the block mask,
 //               intersected with the causal rule when both apply
 // Backward CTA = one head x one key tile kt; the query tiles it visits are
-// kt .. nT-1 (causal), 0 .. nT-1 (dense) or the ascending CSC list.
+// kt .. nT-1 (causal), 0 .. nT-1 (dense), kt .. the last whose windows reach
+// back to kt (window) or the ascending CSC list.
 #pragma once
 
 #include <limits.h>
@@ -26,7 +29,7 @@ namespace fa {
 // tile width differs from 128 only in the block-size sweep (dense and causal
 // batches): key tile j of width BC holds an allowed key of query tile i iff
 // j * BC <= 128 * i + 127.  Block masks (128 x 128 tiles) need BC = 128.
-template <int BC>
+template <int BC, bool WIN = false>
 struct FwdScheduleT {
   int qt[2];
   bool act[2];
@@ -35,6 +38,7 @@ struct FwdScheduleT {
   const int* lb;
   int na, nb, ia, ib;
   int next_dense, end_dense;
+  int sink_end, win_lo[2];  // WIN: tiles with sinks, first tile of each query tile's windows
 
   // last key tile that query tile t reaches under the causal rule
   static FA_DEV int causal_last(int t) {
@@ -80,7 +84,24 @@ struct FwdScheduleT {
     }
   }
 
+  // WIN, after init: N rows, key j for query i where i - j < window or j < sinks
+  FA_DEV void reach(int window, int sinks, int N) {
+    sink_end = (min(sinks, N) + kTile - 1) / kTile;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) win_lo[s] = max(qt[s] * kTile - window + 1, 0) / kTile;
+  }
+
   FA_DEV bool next(int& kt, int& mem) {
+    if constexpr (WIN) {
+      if (next_dense >= sink_end && next_dense < win_lo[0]) next_dense = win_lo[0];
+      if (next_dense >= end_dense) return false;
+      kt = next_dense++;
+      mem = 0;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (act[s] && kt <= qt[s] && (kt < sink_end || kt >= win_lo[s])) mem |= 1 << s;
+      return true;
+    }
     if (!sparse) {
       if (next_dense >= end_dense) return false;
       kt = next_dense++;
@@ -170,6 +191,36 @@ struct BwdGroupSchedule {
     }
   }
 };
+
+// Backward schedule of a window unit: query tiles [q0, q1) of G query heads.
+struct BwdWindowSchedule {
+  int q0, q1, next_qt, g, G;
+  FA_DEV void init(int q0_, int q1_, int G_) {
+    q0 = next_qt = q0_;
+    q1 = q1_;
+    G = G_;
+    g = 0;
+  }
+  FA_DEV bool next(int& qt, int& gout, const TileLists&) {
+    if (next_qt >= q1) {
+      if (++g >= G) return false;
+      next_qt = q0;
+    }
+    qt = next_qt++;
+    gout = g;
+    return true;
+  }
+};
+
+// Query tiles behind the last one that sees a key of tile kt (window >= 1).
+FA_DEV int window_end(int kt, int nT, int window) {
+  return min(nT, (kt * kTile + kTile - 1 + window - 1) / kTile + 1);
+}
+// Which of the 32 keys from one on a row sees: those before `lim` that are
+// not before `lo` or are before `first` (all relative to that key).
+FA_DEV uint32_t reach_bits(int lim, int lo, int first) {
+  return low_bits(lim) & (~low_bits(lo) | low_bits(first));
+}
 
 // The plain schedule behind the grouped interface (a group of one).
 struct BwdSingleSchedule {

@@ -173,9 +173,6 @@ struct TileIter {
   }
 };
 
-// bits 0 .. n-1
-FA_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
 // Which of the 32 keys from position `pos` on draft t of a sequence sees.
 FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const SeqLen& s, int t,
                           int pos) {
