@@ -468,6 +468,30 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
                             int num_pages, int page_size, int max_pages, float scale,
                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * fa_tree_attention with a sliding window and first tokens that stay visible:
+ * of what it would see there, a draft at position x sees the positions above
+ * x - window and those below `sinks`.  A draft's position is hist_lens[b]
+ * plus the number of other drafts that its mask row has (its depth in a
+ * tree), without a mask hist_lens[b] + i; so a chain of tokens sees what
+ * fa_forward_window's last rows see.  Pages that hold no visible position
+ * are not read, and their table entries may be anything (-1, say): they can be
+ * given back (fa_cache_plan).  Positions outside a draft's reach have no
+ * influence on it, whatever they hold.
+ * window >= 1, 0 <= sinks <= 1024, and with a mask window >= T (else
+ * FA_ERR_UNSUPPORTED: a draft could lose its own ancestors).  Workspace and
+ * everything else as fa_tree_attention (of the tables' tiles, those that a
+ * window can touch count).
+ */
+fa_status fa_tree_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                                   const uint8_t* k_scale, const uint8_t* v_scale,
+                                   const int* page_table, const int* hist_lens,
+                                   const int* draft_lens, const uint32_t* tree_mask, void* o,
+                                   float* lse, int format, int B, int H, int Hkv, int T, int d,
+                                   int num_pages, int page_size, int max_pages, float scale,
+                                   int window, int sinks, void* workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the status word of the
  * current device.  FA_OK, FA_ERR_TIMEOUT (a device wait gave up; outputs of
  * the calls since the last check are undefined) or FA_ERR_CUDA. */

@@ -44,6 +44,7 @@ EXPORTS = (
     "fa_qk_norm_rope", "fa_qk_norm_rope_workspace_size", "fa_qk_norm_rope_backward",
     "fa_cache_append", "fa_cache_read", "fa_tree_attention_workspace_size", "fa_tree_attention",
     "fa_forward_window", "fa_backward_window_workspace_size", "fa_backward_window",
+    "fa_tree_attention_window",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -116,6 +117,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "fa_cache_read": ([P] * 9 + [I] * 8 + [P], I),
             "fa_tree_attention_workspace_size": ([I] * 5, Z),
             "fa_tree_attention": ([P] * 11 + [I] * 9 + [F, P, Z, P], I),
+            "fa_tree_attention_window": ([P] * 11 + [I] * 9 + [F, I, I, P, Z, P], I),
             "fa_forward_window": ([P] * 6 + [I] * 6 + [F, I, I, P], I),
             "fa_backward_window_workspace_size": ([I] * 8, Z),
             "fa_backward_window": ([P] * 10 + [I] * 6 + [F, I, I, P, Z, P], I),
@@ -334,6 +336,17 @@ def fa_tree_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_le
         _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(page_table), _p(hist_lens),
         _p(draft_lens), _p(tree_mask), _p(o), _p(lse), int(format), B, H, Hkv, T, d, num_pages,
         page_size, max_pages, float(scale), _p(workspace), int(workspace_bytes), _s(stream))
+
+
+def fa_tree_attention_window(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_lens,
+                             draft_lens, tree_mask, o, lse, format, B, H, Hkv, T, d, num_pages,
+                             page_size, max_pages, scale, window, sinks, workspace,
+                             workspace_bytes, stream=None) -> int:
+    return load().fa_tree_attention_window(
+        _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(page_table), _p(hist_lens),
+        _p(draft_lens), _p(tree_mask), _p(o), _p(lse), int(format), B, H, Hkv, T, d, num_pages,
+        page_size, max_pages, float(scale), window, sinks, _p(workspace), int(workspace_bytes),
+        _s(stream))
 
 
 def fa_forward_window(q, k, v, o, lse, cu_seqlens, B, H, Hkv, N, total, d, scale, window, sinks,
@@ -746,13 +759,18 @@ def cache_read(k_cache, v_cache, page_table, start, N, counts=None, k_scale=None
 
 
 def tree_attention(q, k_cache, v_cache, page_table, hist_lens, draft_lens=None, tree_mask=None,
-                   scale=None, k_scale=None, v_scale=None, workspace=None, stream=None):
+                   scale=None, k_scale=None, v_scale=None, workspace=None, stream=None,
+                   window=None, sinks=0):
     """(o, lse) of drafted tokens q [B, H, T, d] over the paged cache, their
     own keys and values appended behind the hist_lens[b] accepted tokens.
     tree_mask: int32 [B, T, ceil(T / 32)], bit j of row i set when draft i
     sees draft j; None: a chain (T = 1: a plain decode step).  draft_lens
-    (int32 [B], None: T): rows behind get o = 0, lse = -inf."""
+    (int32 [B], None: T): rows behind get o = 0, lse = -inf.  window: each
+    draft sees the last `window` positions up to its own and the first `sinks`
+    ones; pages that hold neither are not read."""
     import torch
+    if sinks and window is None:
+        raise ValueError("sinks apply to a window")
     if q.dim() != 4:
         raise ValueError("expected q [B, H, T, d]")
     B, H, T, d = q.shape
@@ -771,7 +789,12 @@ def tree_attention(q, k_cache, v_cache, page_table, hist_lens, draft_lens=None, 
         if workspace is None:
             workspace = torch.empty(fa_tree_attention_workspace_size(B, H, Hkv, T, d),
                                     dtype=torch.uint8, device=q.device)
-        _check(fa_tree_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_lens,
-                                 draft_lens, tree_mask, o, lse, fmt, B, H, Hkv, T, d, *pages,
-                                 scale, workspace, _bytes(workspace, q), s), "fa_tree_attention")
+        args = (q, k_cache, v_cache, k_scale, v_scale, page_table, hist_lens, draft_lens, tree_mask,
+                o, lse, fmt, B, H, Hkv, T, d, *pages, scale)
+        if window is None:
+            _check(fa_tree_attention(*args, workspace, _bytes(workspace, q), s),
+                   "fa_tree_attention")
+        else:
+            _check(fa_tree_attention_window(*args, window, sinks, workspace,
+                                            _bytes(workspace, q), s), "fa_tree_attention_window")
     return o, lse

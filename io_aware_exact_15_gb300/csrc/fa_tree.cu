@@ -111,8 +111,8 @@ struct TreeSmem {
   // tiles leave no room)
   static constexpr int OUT = RW + NR * RAW;
   static constexpr int SC = OUT + (Q8 ? 0 : 8 * 4096);  // scale bytes of the stored tiles
-  static constexpr int NOTE = SC + NR * kTile;  // what a stored tile holds: int4 each
-  static constexpr int ML = NOTE + NR * 16;     // (m, l) of the second warpgroup's rows
+  static constexpr int NOTE = SC + NR * kTile;  // what a stored tile holds: two int4 each
+  static constexpr int ML = NOTE + NR * 32;     // (m, l) of the second warpgroup's rows
   static constexpr int BAR = ML + (PAIR ? 0 : kTile * 8);
   static constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + NS, B_RF = B_KVE + NS,
                        B_RE = B_RF + NR, B_SF = B_RE + NR, B_PF = B_SF + 2, B_OF = B_PF + 2,
@@ -130,7 +130,7 @@ struct TreeSmem {
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
-template <int D, int FMT, bool PAIR>
+template <int D, int FMT, bool PAIR, bool WIN>
 __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const TreeParams p) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0) {
-    const Run r = find_run(p, blockIdx.x, gridDim.x, lane);
+    const Run r = find_run<WIN>(p, blockIdx.x, gridDim.x, lane);
     if (lane == 0) {
       *run_slot = r;
       for (int i = 0; i < 2; ++i) {
@@ -196,27 +196,31 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
   auto uwait = [&](uint32_t b, uint32_t ph) {
     return __all_sync(0xffffffffu, wait_bar(b, ph, wc));
   };
-  TileIter tiles0;
+  TileIter<WIN> tiles0;
   if (run.left > 0) tiles0.it.init(p, run);
   else tiles0.it.left = 0;
 
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------ loads
     const bool isv = warp == 10;
-    TileIter ti = tiles0;
+    TileIter<WIN> ti = tiles0;
     uint32_t g = 0;
     int parts = 0;
     bool ok = true;
     const int page = 1 << p.log_page;
-    // pages of the next tile that hold a token, one per lane: looked up one
-    // tile ahead
+    // pages of the next tile that hold a token (that a draft sees), one per
+    // lane: looked up one tile ahead
     bool have = ti.next(p);
     int np = 0, id = 0;
+    bool want = false;
     auto look_up = [&]() {
-      const int kb = ti.t * kTile, nval = min(max(ti.it.s.len() - kb, 0), kTile);
+      const int kb = ti.it.s.key_tile(ti.t) * kTile;
+      const int nval = min(max(ti.it.s.len() - kb, 0), kTile);
       np = (nval + page - 1) >> p.log_page;
+      want = lane < np && !(WIN && ti.it.s.nothing(kb + lane * page, page));
+      if (WIN) np = __popc(__ballot_sync(0xffffffffu, want));
       id = 0;
-      if (lane < np)
+      if (want)
         id = p.page_table[static_cast<size_t>(ti.it.b) * p.max_pages + (kb >> p.log_page) + lane];
     };
     if (have) look_up();
@@ -246,13 +250,17 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
       if (!ok) break;
       const uint32_t full = bar(B_FULL + slot);
       if (lane == 0) {
-        if (L::Q8)
-          *reinterpret_cast<int4*>(smem + L::NOTE + slot * 16) =
-              make_int4(ti.it.s.len() - ti.t * kTile, ti.it.s.hist - ti.t * kTile, ti.part, 0);
+        if (L::Q8) {
+          const int kb = ti.it.s.key_tile(ti.t) * kTile;
+          int4* note = reinterpret_cast<int4*>(smem + L::NOTE + slot * 32);
+          note[0] = make_int4(ti.it.s.len() - kb, ti.it.s.hist - kb, ti.part, 0);
+          if (WIN)
+            note[1] = make_int4(ti.it.s.sinks - kb, ti.it.s.lo - kb, ti.it.s.edge - kb, 0);
+        }
         mbar_arrive_expect_tx(full, np * page * (L::Q8 ? D + 1 : 2 * D));
       }
       __syncwarp();
-      if (lane < np) {
+      if (want) {
         const int z = min(max(id, 0), p.num_pages - 1) * p.Hkv + hkv;
         if (!L::Q8) {
 #pragma unroll
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
                       (acc || kk > 0) ? 1u : 0u);
       }
     };
-    TileIter ti = tiles0;
+    TileIter<WIN> ti = tiles0;
     uint32_t idx = 0;  // tiles taken from the ring
     auto wait_kv = [&]() {
       return uwait(bar(L::B_KVF + idx % L::NS), (idx / L::NS) & 1);
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
                         : uwait(bar(L::B_QF + (part & 1)), (part >> 1) & 1);
     };
     // which warpgroups a pair tile serves
-    auto members = [&](const TileIter& x) {
+    auto members = [&](const TileIter<WIN>& x) {
       return (x.it.hr % p.groups) * 2 * kTile + kTile < p.rows ? 3 : 1;
     };
     bool ok = true;
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     const uint32_t tP = tS + L::T_P;
     const float sl2 = p.scale * kLog2e;
     float2* ml = reinterpret_cast<float2*>(smem + L::ML);
-    PartIter it = tiles0.it;
+    PartIter<WIN> it = tiles0.it;
     uint32_t g = 0, cnt = 0;  // tiles; parities of own tiles (bit 0) and parts (bit 1)
     const uint32_t total = run.left;
     int part = -1;
@@ -450,18 +458,22 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
       const bool valid = row < p.rows && t < it.s.nd;
       const uint32_t* mask_row =
           p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words : nullptr;
+      int begin = 0;  // WIN: where the row's window begins
+      if constexpr (WIN)
+        if (valid) begin = window_begin(p, mask_row, it.s, t);
       float m = -INFINITY, l = 0.f;
       int mine = 0;               // tiles of this part done by this warpgroup
       for (int tile = it.t0; tile < it.t1 && ok; ++tile, ++g) {
         if (PAIR ? !mine_all : static_cast<int>(g & 1) != s) continue;
-        const int kb = tile * kTile;
-        const bool tail = kb + kTile > it.s.hist;  // drafts or the end in this tile
+        const int kb = it.s.key_tile(tile) * kTile;
+        // drafts or the end in this tile (WIN: or an edge of the window)
+        const bool tail = it.s.mixed(kb, kTile);
         uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
         auto look = [&]() {
           if (tail && busy) {
 #pragma unroll
             for (int w = 0; w < 4; ++w)
-              vis[w] = valid ? seen_bits(p, mask_row, it.s, t, kb + 32 * w) : 0u;
+              vis[w] = valid ? seen_bits<WIN>(p, mask_row, it.s, t, kb + 32 * w, begin) : 0u;
           }
         };
         // bf16: the mask's words come while the scores are formed (8 bits:
@@ -569,8 +581,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
           if (!ok) break;
           const uint32_t v0 = sb + L::KV + (vi % L::NS) * L::TILE;
           const int pos = kb + r;
-          if (pos >= it.s.hist) {
-            const bool past = pos >= it.s.len();
+          if (!it.s.everybody(pos)) {
+            const bool past = it.s.nobody(pos);
 #pragma unroll 1
             for (int c0 = 0; c0 < L::CH * 8; c0 += 4) {
               uint4 v[4];
@@ -730,10 +742,9 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         }
         __syncwarp();  // rows were written by other lanes of the warp
         if (valid && bad_parts[part & 7] == part)
-          add_not_finite<D, FMT>(p, it.b, hkv, it.s, t, max(it.s.hist, it.t0 * kTile),
-                                 min(it.s.len(), it.t1 * kTile),
-                                 whole ? static_cast<uint16_t*>(p.o) + orow * D : nullptr,
-                                 whole ? nullptr : p.part_o + prow * D);
+          add_not_finite<D, FMT, WIN>(p, it.b, hkv, it.s, t, it.t0, it.t1,
+                                      whole ? static_cast<uint16_t*>(p.o) + orow * D : nullptr,
+                                      whole ? nullptr : p.part_o + prow * D);
       }
       if (!PAIR) {
         tc_fence_before();
@@ -762,10 +773,15 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
       if (!ok) break;
       const uint32_t raw = sb + L::RW + rs * L::RAW, sc = sb + L::SC + rs * kTile;
       const uint32_t dst = sb + L::KV + ds * L::TILE + (D == 128 ? (u >> 2) * L::CHUNK : 0);
-      const uint4 note = ld_shared_v4(sb + L::NOTE + rs * 16);
+      const uint4 note = ld_shared_v4(sb + L::NOTE + rs * 32);
+      uint4 edges = make_uint4(0, 0, 0, 0);  // sinks, lo, edge (see SeqLen) from the tile's first key
+      if (WIN) edges = ld_shared_v4(sb + L::NOTE + rs * 32 + 16);
+      const int sinks = static_cast<int>(edges.x), lo = static_cast<int>(edges.y),
+                edge = static_cast<int>(edges.z);
       const int nval = static_cast<int>(note.x), ndraft = static_cast<int>(note.y);
       const int part = static_cast<int>(note.z), c0 = 2 * (u & 3);
-      const bool check = isv && ndraft < kTile;  // drafts or the end in this tile
+      // drafts or the end in this tile (WIN: or an edge of the window)
+      const bool check = isv && (ndraft < kTile || (WIN && edge > 0 && sinks < kTile));
 #pragma unroll 1
       for (int r0 = cw * RPI; r0 < kTile; r0 += BATCH * kConvTeam * RPI) {
         uint2 w[BATCH][2];
@@ -789,10 +805,11 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
           widen4<FMT>(w[i][0].y, scale, y0.z, y0.w);
           widen4<FMT>(w[i][1].x, scale, y1.x, y1.y);
           widen4<FMT>(w[i][1].y, scale, y1.z, y1.w);
-          if (check && row >= ndraft) {
-            const bool bad = row < nval && byte[i] == kScaleNan;
+          if (check && (row >= ndraft || (WIN && row >= sinks && row < edge))) {
+            const bool past = row >= nval || (WIN && row >= sinks && row < lo);
+            const bool bad = !past && byte[i] == kScaleNan;
             if (bad) bad_parts[part & 7] = part;
-            if (bad || row >= nval) y0 = y1 = make_uint4(0, 0, 0, 0);
+            if (bad || past) y0 = y1 = make_uint4(0, 0, 0, 0);
           }
           st_shared_v4(dst + sw128_offset(row, c0 + sel), y0.x, y0.y, y0.z, y0.w);
           st_shared_v4(dst + sw128_offset(row, c0 + (sel ^ 1)), y1.x, y1.y, y1.z, y1.w);
@@ -895,9 +912,14 @@ size_t tree_ws_bytes(int H, int Hkv, int T, int d) {
          align256(2ull * most_ctas(rows) * slot_rows(rows) * d * sizeof(float));
 }
 
-// Tiles of the longest sequence that the page table can hold.
+// Tiles of the longest sequence that the page table can hold (with a window:
+// the sinks', and those that window + T - 1 positions can touch).
 long long most_tiles(const TreeParams& p) {
-  return ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
+  const long long all = ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
+  if (!p.window) return all;
+  const long long near = (static_cast<long long>(p.window) + p.T + kTile - 3) / kTile + 1 +
+                         (p.sinks + kTile - 1) / kTile;
+  return near < all ? near : all;
 }
 
 // CTAs: `per_sm` per SM, no more than there can be units (0 on error).
@@ -916,18 +938,18 @@ cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t strea
                  : launch_pdl(fa_tree_join_kernel<128>, blocks, dim3(256), 0, stream, p);
 }
 
-template <int D, int FMT, bool PAIR>
+template <int D, int FMT, bool PAIR, bool WIN>
 cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t stream) {
   using L = TreeSmem<D, FMT, PAIR>;
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(
-      attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT, PAIR>), L::ALLOC);
+      attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT, PAIR, WIN>), L::ALLOC);
   if (e != cudaSuccess) return e;
   const int grid = tree_grid(p, 1);
   if (grid <= 0) return cudaErrorInvalidDevice;
-  e = launch_pdl(fa_tree_kernel<D, FMT, PAIR>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream, tq,
-                 tk, tv, p);
+  e = launch_pdl(fa_tree_kernel<D, FMT, PAIR, WIN>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream,
+                 tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   return launch_join(p, D, grid, stream);
 }
@@ -935,8 +957,11 @@ cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap& tq, const C
 template <int D, int FMT>
 cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t stream) {
-  return p.pair ? launch_tree_mode<D, FMT, true>(p, tq, tk, tv, stream)
-                : launch_tree_mode<D, FMT, false>(p, tq, tk, tv, stream);
+  if (p.window)
+    return p.pair ? launch_tree_mode<D, FMT, true, true>(p, tq, tk, tv, stream)
+                  : launch_tree_mode<D, FMT, false, true>(p, tq, tk, tv, stream);
+  return p.pair ? launch_tree_mode<D, FMT, true, false>(p, tq, tk, tv, stream)
+                : launch_tree_mode<D, FMT, false, false>(p, tq, tk, tv, stream);
 }
 
 }  // namespace
@@ -949,13 +974,17 @@ size_t fa_tree_attention_workspace_size(int B, int H, int Hkv, int T, int d) {
   return fa::tree_ws_bytes(H, Hkv, T, d);
 }
 
-fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_cache,
-                            const uint8_t* k_scale, const uint8_t* v_scale, const int* page_table,
-                            const int* hist_lens, const int* draft_lens, const uint32_t* tree_mask,
-                            void* o, float* lse, int format, int B, int H, int Hkv, int T, int d,
-                            int num_pages, int page_size, int max_pages, float scale,
-                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  using namespace fa;
+}  // extern "C"
+
+namespace fa {
+namespace {
+// Both entry points; window 0: none.
+fa_status tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                         const uint8_t* k_scale, const uint8_t* v_scale, const int* page_table,
+                         const int* hist_lens, const int* draft_lens, const uint32_t* tree_mask,
+                         void* o, float* lse, int format, int B, int H, int Hkv, int T, int d,
+                         int num_pages, int page_size, int max_pages, float scale, int window,
+                         int sinks, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (B < 1 || H < 1 || T < 1) return FA_ERR_INVALID_ARG;
   if (!(isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (Hkv < 1 || Hkv > H || H % Hkv != 0) return FA_ERR_INVALID_ARG;
@@ -996,6 +1025,8 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.log_page = log2_page(page_size);
   p.max_pages = max_pages;
   p.words = (T + 31) / 32;
+  p.window = window;
+  p.sinks = sinks;
   p.scale = scale;
   // units (TreeParams, find_run) are counted in 32 bits
   if (static_cast<long long>(B) * Hkv * p.groups > ((1LL << 31) - 1) / most_tiles(p))
@@ -1032,6 +1063,40 @@ fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_ca
             : format == kCacheE4m3 ? (launch_tree<128, kCacheE4m3>(p, tq, tk, tv, stream))
                                    : (launch_tree<128, kCacheInt8>(p, tq, tk, tv, stream)));
   return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const uint8_t* k_scale, const uint8_t* v_scale, const int* page_table,
+                            const int* hist_lens, const int* draft_lens, const uint32_t* tree_mask,
+                            void* o, float* lse, int format, int B, int H, int Hkv, int T, int d,
+                            int num_pages, int page_size, int max_pages, float scale,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return fa::tree_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_lens,
+                            draft_lens, tree_mask, o, lse, format, B, H, Hkv, T, d, num_pages,
+                            page_size, max_pages, scale, 0, 0, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_tree_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                                   const uint8_t* k_scale, const uint8_t* v_scale,
+                                   const int* page_table, const int* hist_lens,
+                                   const int* draft_lens, const uint32_t* tree_mask, void* o,
+                                   float* lse, int format, int B, int H, int Hkv, int T, int d,
+                                   int num_pages, int page_size, int max_pages, float scale,
+                                   int window, int sinks, void* workspace, size_t workspace_bytes,
+                                   cudaStream_t stream) {
+  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  // a mask's drafts all lie within the window
+  if (sinks > 1024 || (tree_mask && T > window)) return FA_ERR_UNSUPPORTED;
+  // positions stay below 2^30: no window is longer
+  return fa::tree_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_lens,
+                            draft_lens, tree_mask, o, lse, format, B, H, Hkv, T, d, num_pages,
+                            page_size, max_pages, scale, window < (1 << 30) ? window : 1 << 30,
+                            sinks, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -33,30 +33,65 @@ struct TreeParams {
   int groups, slot_rows;   // row groups per key/value head; rows of a part
   int pair;                // 256-row groups
   int num_pages, log_page, max_pages, words;
+  int window, sinks;       // kernels with a window: at least 1, at least 0
   float scale;
   int* err;
   uint64_t wait_ns;
 };
 
 // Lengths of a sequence, clamped to what the page table can hold.
+//
+// WIN: a draft with c drafts before it on its path sees the positions below
+// `sinks` and those from hist + c - window + 1 on (of the drafts those that
+// its mask row or the chain's order has).  So positions fall into three
+// classes: those that every draft sees (below `sinks`, or in [edge, hist)),
+// those that none sees (in [sinks, lo), and past the end), and those that are
+// a matter of the draft.  Tiles of which no draft sees anything are left out:
+// the t-th of a sequence's tiles is the t-th of the table before `sunk`, the
+// (t + skip)-th from there on.
+template <bool WIN>
 struct SeqLen {
   int hist, nd, tiles;
+  int sinks, lo, edge, sunk, skip;
   FA_DEV int len() const { return hist + nd; }
+  FA_DEV int key_tile(int t) const { return WIN && t >= sunk ? t + skip : t; }
+  FA_DEV bool nobody(int pos) const { return pos >= len() || (WIN && pos >= sinks && pos < lo); }
+  FA_DEV bool everybody(int pos) const {
+    return pos < hist && (!WIN || pos < sinks || pos >= edge);
+  }
+  // whether n positions from pos on are not all everybody's, and are all nobody's
+  FA_DEV bool mixed(int pos, int n) const {
+    return pos + n > hist || (WIN && pos < edge && pos + n > sinks);
+  }
+  FA_DEV bool nothing(int pos, int n) const {
+    return pos >= len() || (WIN && pos >= sinks && pos + n <= lo);
+  }
 };
-FA_DEV SeqLen seq_len(const TreeParams& p, int b) {
-  SeqLen s;
+template <bool WIN>
+FA_DEV SeqLen<WIN> seq_len(const TreeParams& p, int b) {
+  SeqLen<WIN> s;
   const int cap = p.max_pages << p.log_page;
   s.hist = min(max(p.hist[b], 0), cap);
   s.nd = min(p.drafts ? min(max(p.drafts[b], 0), p.T) : p.T, cap - s.hist);
+  int tiles = (s.len() + kTile - 1) / kTile;
+  if (WIN) {
+    s.sinks = p.sinks;
+    s.lo = max(s.hist - p.window + 1, 0);
+    s.edge = max(s.hist - p.window + max(s.nd, 1), 0);
+    s.sunk = min((min(p.sinks, s.len()) + kTile - 1) / kTile, s.lo / kTile);
+    s.skip = s.lo / kTile - s.sunk;
+    tiles -= min(s.skip, tiles);
+  }
   // one unit even without a key: somebody has to write the rows
-  s.tiles = max(1, (s.len() + kTile - 1) / kTile);
+  s.tiles = max(1, tiles);
   return s;
 }
 
 // Units of sequence b: its tiles for each key/value head and row group.  All
 // sequences together have less than 2^31 (checked on the host).
+template <bool WIN>
 FA_DEV uint32_t seq_units(const TreeParams& p, int b) {
-  return b < p.B ? static_cast<uint32_t>(seq_len(p, b).tiles) * (p.Hkv * p.groups) : 0u;
+  return b < p.B ? static_cast<uint32_t>(seq_len<WIN>(p, b).tiles) * (p.Hkv * p.groups) : 0u;
 }
 
 // A CTA's run of units.
@@ -75,11 +110,12 @@ FA_DEV uint32_t run_begin(uint32_t total, uint32_t c, uint32_t n) {
 
 // Run of CTA c: with n = the grid's CTAs, or the units if there are fewer (no
 // run between two others is empty).  Whole warp.
+template <bool WIN>
 FA_DEV Run find_run(const TreeParams& p, int c, int grid, int lane) {
-  const uint32_t mine = seq_units(p, lane);  // the first 32 sequences
+  const uint32_t mine = seq_units<WIN>(p, lane);  // the first 32 sequences
   uint32_t total = __reduce_add_sync(0xffffffffu, mine);
   for (int b0 = 32; b0 < p.B; b0 += 32)
-    total += __reduce_add_sync(0xffffffffu, seq_units(p, b0 + lane));
+    total += __reduce_add_sync(0xffffffffu, seq_units<WIN>(p, b0 + lane));
   const int n = total < static_cast<uint32_t>(grid) ? static_cast<int>(total) : grid;
   Run r = {0, 0, 0, 0, 0, total, n};
   if (c >= n) return r;
@@ -87,7 +123,7 @@ FA_DEV Run find_run(const TreeParams& p, int c, int grid, int lane) {
   r.left = run_begin(total, c + 1, n) - r.first;
   uint32_t base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const uint32_t u = b0 == 0 ? mine : seq_units(p, b0 + lane);
+    const uint32_t u = b0 == 0 ? mine : seq_units<WIN>(p, b0 + lane);
     uint32_t incl = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -110,8 +146,9 @@ FA_DEV Run find_run(const TreeParams& p, int c, int grid, int lane) {
 }
 
 // The parts of problems in a run, in order; every role of the CTA walks it.
+template <bool WIN>
 struct PartIter {
-  SeqLen s;
+  SeqLen<WIN> s;
   int b, hr, t0, t1;  // tiles [t0, t1) of problem (b, hr)
   int next_t;
   uint32_t left;
@@ -120,7 +157,7 @@ struct PartIter {
     hr = r.hr;
     next_t = r.t;
     left = r.left;
-    s = seq_len(p, b);
+    s = seq_len<WIN>(p, b);
   }
   FA_DEV bool next(const TreeParams& p) {
     if (left == 0) return false;
@@ -129,7 +166,7 @@ struct PartIter {
       if (++hr == p.Hkv * p.groups) {
         hr = 0;
         ++b;
-        s = seq_len(p, b);
+        s = seq_len<WIN>(p, b);
       }
     }
     t0 = next_t;
@@ -143,7 +180,8 @@ struct PartIter {
 // The problem that this CTA begins and does not end, for the second kernel;
 // `it` after the last part of the run (one thread; idle CTAs too, with no
 // part).
-FA_DEV void note_join(const TreeParams& p, const Run& r, const PartIter& it, int c) {
+template <bool WIN>
+FA_DEV void note_join(const TreeParams& p, const Run& r, const PartIter<WIN>& it, int c) {
   int2 j = make_int2(0, 0);
   if (r.left > 0 && it.t0 == 0 && it.t1 < it.s.tiles) {
     // unit u belongs to CTA floor(((u + 1) n - 1) / total)
@@ -155,8 +193,9 @@ FA_DEV void note_join(const TreeParams& p, const Run& r, const PartIter& it, int
 }
 
 // The tiles of a run, in order.
+template <bool WIN>
 struct TileIter {
-  PartIter it;
+  PartIter<WIN> it;
   int t = 0, part = -1;
   bool first = false, last = false;
   FA_DEV bool next(const TreeParams& p) {
@@ -173,9 +212,28 @@ struct TileIter {
   }
 };
 
-// Which of the 32 keys from position `pos` on draft t of a sequence sees.
-FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const SeqLen& s, int t,
-                          int pos) {
+// The first position of draft t's window: behind the drafts that it sees
+// beside itself.
+FA_DEV int window_begin(const TreeParams& p, const uint32_t* mask_row, const SeqLen<true>& s,
+                        int t) {
+  int c = t;
+  if (mask_row) {
+    c = 0;
+    for (int i = 0; i < p.words; ++i) {
+      uint32_t w = mask_row[i] & low_bits(s.nd - 32 * i);
+      if (i == t >> 5) w &= ~(1u << (t & 31));
+      c += __popc(w);
+    }
+  }
+  return s.hist + c - p.window + 1;
+}
+
+// Which of the 32 keys from position `pos` on draft t of a sequence sees; its
+// window begins at `begin` (WIN).  (A mask goes with windows no shorter than
+// the drafts: `begin` is then at most hist, and cuts no draft off.)
+template <bool WIN>
+FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const SeqLen<WIN>& s,
+                          int t, int pos, int begin) {
   const int d0 = pos - s.hist;  // draft index of bit 0
   uint32_t w;
   if (!mask_row) {
@@ -187,7 +245,8 @@ FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const S
   } else {
     w = d0 > -32 ? mask_row[0] << -d0 : 0u;
   }
-  return (w & low_bits(s.nd - d0)) | low_bits(-d0);
+  w = (w & low_bits(s.nd - d0)) | low_bits(-d0);
+  return WIN ? w & (~low_bits(begin - pos) | low_bits(s.sinks - pos)) : w;
 }
 
 FA_DEV uint32_t ld_shared_u8(uint32_t addr) {
@@ -221,15 +280,21 @@ FA_DEV uint32_t finite2(uint32_t w) {
   return w;
 }
 
-// Adds the NaN and infinite values among the drafts of positions [lo, hi)
-// that draft t sees to its written row of O (they were zeroed in the tiles):
-// `o` (bf16) or `part` (fp32).  Rare.
-template <int D, int FMT>
-static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, int hkv, SeqLen s, int t,
-                                            int lo, int hi, uint16_t* o, float* part) {
+// Adds the NaN and infinite values among the positions of tiles [t0, t1) that
+// not every draft sees and draft t does to its written row of O (they were
+// zeroed in the tiles): `o` (bf16) or `part` (fp32).  Rare.
+template <int D, int FMT, bool WIN>
+static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, int hkv,
+                                                   SeqLen<WIN> s, int t, int t0, int t1,
+                                                   uint16_t* o, float* part) {
   const uint32_t* mr = p.mask ? p.mask + (static_cast<size_t>(b) * p.T + t) * p.words : nullptr;
-  for (int pos = lo; pos < hi; ++pos) {
-    if (!(seen_bits(p, mr, s, t, pos) & 1u)) continue;
+  int begin = 0;
+  if constexpr (WIN) begin = window_begin(p, mr, s, t);
+  const int first = WIN ? t0 * kTile : max(s.hist, t0 * kTile);
+  for (int at = first; at < (WIN ? t1 * kTile : min(s.len(), t1 * kTile)); ++at) {
+    const int pos = s.key_tile(at / kTile) * kTile + at % kTile;
+    if (WIN && (s.everybody(pos) || s.nobody(pos))) continue;
+    if (!(seen_bits<WIN>(p, mr, s, t, pos, begin) & 1u)) continue;
     int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (pos >> p.log_page)];
     page = min(max(page, 0), p.num_pages - 1);
     const long long row = ((static_cast<long long>(page) * p.Hkv + hkv) << p.log_page) +
@@ -282,6 +347,7 @@ inline bool tree_few_rows(int rows, int format) { return rows <= (format == kCac
 constexpr int few_ctas(int rows, int format, int d) {
   return rows <= 8 && (format != kCacheBf16 || d == 64) ? 2 : 1;
 }
+// (with p.window: the kernels with a window)
 cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream);
 

@@ -140,7 +140,7 @@ FA_DEV float lanes_sum(float v) {
   return v;
 }
 
-template <int D, int FMT, int RT>
+template <int D, int FMT, int RT, bool WIN>
 __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, RT>::CTAS)
     fa_tree_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const TreeParams p) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
   auto empty = [&](int stage) { return sb + L::BAR + 16 * stage + 8; };
 
   if (warp == 0) {
-    const Run r = find_run(p, blockIdx.x, gridDim.x, lane);
+    const Run r = find_run<WIN>(p, blockIdx.x, gridDim.x, lane);
     if (lane == 0) *run_slot = r;
   } else if (warp == 1 && lane == 0) {
     for (int i = 0; i < L::R; ++i) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
   __syncthreads();
   const Run run = *run_slot;
   if (run.left == 0) {
-    if (threadIdx.x == 0) note_join(p, run, PartIter(), blockIdx.x);
+    if (threadIdx.x == 0) note_join(p, run, PartIter<WIN>(), blockIdx.x);
     return;
   }
   const WaitCtl wc{abort_flag, p.err, p.wait_ns};
@@ -191,18 +191,22 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
     const CUtensorMap* map = isv ? &tv : &tk;
     const uint8_t* sc = isv ? p.vs : p.ks;
     const int psize = 1 << p.log_page;
-    TileIter ti;
+    TileIter<WIN> ti;
     ti.it.init(p, run);
     uint32_t n = 0;
     bool ok = true;
     bool have = ti.next(p);
-    // pages of the next tile that hold a token, one per lane
+    // pages of the next tile that hold a token (that a draft sees), one per lane
     int np = 0, id = 0;
+    bool want = false;
     auto look_up = [&]() {
-      const int kb = ti.t * kTile, nval = min(max(ti.it.s.len() - kb, 0), kTile);
+      const int kb = ti.it.s.key_tile(ti.t) * kTile;
+      const int nval = min(max(ti.it.s.len() - kb, 0), kTile);
       np = (nval + psize - 1) >> p.log_page;
+      want = lane < np && !(WIN && ti.it.s.nothing(kb + lane * psize, psize));
+      if (WIN) np = __popc(__ballot_sync(0xffffffffu, want));
       id = 0;
-      if (lane < np)
+      if (want)
         id = p.page_table[static_cast<size_t>(ti.it.b) * p.max_pages + (kb >> p.log_page) + lane];
     };
     if (have) look_up();
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
       if (lane == 0)
         mbar_arrive_expect_tx(full(stage), np * psize * (D * L::EB + (Q8 ? 1 : 0)));
       __syncwarp();
-      if (lane < np) {
+      if (want) {
         const int z = min(max(id, 0), p.num_pages - 1) * p.Hkv + ti.it.hr;
         const uint32_t dst = sb + L::RING + stage * L::STAGE + (isv ? L::KBYTES : 0) +
                              lane * psize * (Q8 ? D : 128);
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
   const float sl2 = p.scale * kLog2e;
   const int k_own = (g & 1) ? (g >> 1) ^ 5 : g >> 1;  // key of index g
   const int k0 = c, k1 = c ^ 5;                       // keys of indices 2c, 2c + 1
-  PartIter it;
+  PartIter<WIN> it;
   it.init(p, run);
   uint32_t n = 0;  // tiles of the run
   int part = -1;
@@ -256,6 +260,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
     uint32_t qf[RT][QR];
     float frow[RT][2];  // score factor of rows 8 rt + 2c, + 1 (log2 units)
     int trow[RT][2];    // their drafts, -1 for none
+    int begin[RT][2];   // WIN: where their windows begin
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int row = 8 * rt + g;
@@ -295,6 +300,12 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
         frow[rt][r] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + r));
         const int row2 = 8 * rt + 2 * c + r, t = row2 % p.T;
         trow[rt][r] = row2 < p.rows && t < it.s.nd ? t : -1;
+        begin[rt][r] = 0;
+        if constexpr (WIN)
+          if (trow[rt][r] >= 0)
+            begin[rt][r] = window_begin(
+                p, p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words : nullptr,
+                it.s, t);
       }
     }
     float o[RT][MT][4];  // column tile: (element 0, rows 2c, 2c + 1), (element 1, ...)
@@ -320,11 +331,11 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
      if (!ok) continue;
 #pragma unroll 1
      for (; chunk < 8 * (tile - it.t0 + 1); chunk += L::NC) {
-      const int sub = chunk & 7, pos = tile * kTile + sub * kFewKeys;
-      if (pos >= it.s.len()) continue;  // nothing there
+      const int sub = chunk & 7, pos = it.s.key_tile(tile) * kTile + sub * kFewKeys;
+      if (it.s.nothing(pos, kFewKeys)) continue;
       const uint32_t ka = sb + L::RING + stage * L::STAGE + sub * kFewKeys * (Q8 ? D : 128);
       const uint32_t va = ka + L::KBYTES;
-      const bool tail = pos + kFewKeys > it.s.hist;
+      const bool tail = it.s.mixed(pos, kFewKeys);
       // ---- S^T = K Q^T: s[rt] = (key g, rows 2c, 2c + 1), (key 8 + g, ...)
       float s[RT][4];
 #pragma unroll
@@ -388,10 +399,11 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
             const int t = trow[rt][r];
             const uint32_t vis =
                 t < 0 ? 0u
-                      : seen_bits(p,
-                                  p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words
-                                         : nullptr,
-                                  it.s, t, pos);
+                      : seen_bits<WIN>(
+                            p,
+                            p.mask ? p.mask + (static_cast<size_t>(it.b) * p.T + t) * p.words
+                                   : nullptr,
+                            it.s, t, pos, begin[rt][r]);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               if (!((vis >> (8 * i + k_own)) & 1u)) x[r][i] = y[r][i] = -INFINITY;
@@ -443,7 +455,6 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
               transpose8(Q8 ? pack_f16(e[0][i], e[1][i]) : pack_bf16(e[0][i], e[1][i]));
       }
       // ---- O^T += V^T P^T
-      const int nval = it.s.len() - pos, ndraft = it.s.hist - pos;
       if (!Q8) {
         // rows of the four 8 x 8 pieces: keys 0-7 and 8-15 of two column halves
         const int j = lane & 7, vrow = 8 * (lane >> 4) + ((j & 1) ? (j >> 1) ^ 5 : j >> 1);
@@ -456,12 +467,13 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int ka0 = 8 * (x >> 1) + k0, ka1 = 8 * (x >> 1) + k1;
-              if (ka0 >= nval) a[x] &= 0xFFFF0000u;  // past the last token
-              if (ka1 >= nval) a[x] &= 0x0000FFFFu;
-              // NaN and infinities of drafts: back at the end of the part
+              if (it.s.nobody(pos + ka0)) a[x] &= 0xFFFF0000u;  // past the last token, say
+              if (it.s.nobody(pos + ka1)) a[x] &= 0x0000FFFFu;
+              // NaN and infinities of drafts (of what not every draft sees):
+              // back at the end of the part
               const uint32_t f = finite2(a[x]);
-              const uint32_t history =
-                  (ka0 < ndraft ? 0x0000FFFFu : 0u) | (ka1 < ndraft ? 0xFFFF0000u : 0u);
+              const uint32_t history = (it.s.everybody(pos + ka0) ? 0x0000FFFFu : 0u) |
+                                       (it.s.everybody(pos + ka1) ? 0xFFFF0000u : 0u);
               const uint32_t n = (f & ~history) | (a[x] & history);
               bad |= n != a[x];
               a[x] = n;
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
             const uint2 y = ld_shared_v2(va + row * 64 + (((u >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (u & 1));
             v[x][0] = y.x, v[x][1] = y.y;
           }
-          if (tail && row >= nval)
+          if (tail && it.s.nobody(pos + row))
 #pragma unroll
             for (int i = 0; i < WV; ++i) v[x][i] = 0;
         }
@@ -602,25 +614,32 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
     if (!Q8 && bad_parts[part & 1] == part) {  // after the barrier: the rows are written
       const int row = tid, t = row % p.T;
       if (row < p.rows && t < it.s.nd)
-        add_not_finite<D, FMT>(p, it.b, it.hr, it.s, t, max(it.s.hist, it.t0 * kTile),
-                               min(it.s.len(), it.t1 * kTile),
-                               whole ? static_cast<uint16_t*>(p.o) + (orow0 + row) * D : nullptr,
-                               whole ? nullptr : p.part_o + (prow0 + row) * D);
+        add_not_finite<D, FMT, WIN>(
+            p, it.b, it.hr, it.s, t, it.t0, it.t1,
+            whole ? static_cast<uint16_t*>(p.o) + (orow0 + row) * D : nullptr,
+            whole ? nullptr : p.part_o + (prow0 + row) * D);
     }
   }
   if (tid == 0) note_join(p, run, it, blockIdx.x);
 }
 
-template <int D, int FMT, int RT>
-cudaError_t launch_few_rows(const TreeParams& p, const CUtensorMap& tk,
+template <int D, int FMT, int RT, bool WIN>
+cudaError_t launch_few_win(const TreeParams& p, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream) {
   using L = FewSmem<D, FMT, RT>;
   static std::atomic<unsigned long long> attr_done{0};
   const cudaError_t e = smem_attr_once(
-      attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, RT>), L::ALLOC);
+      attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, RT, WIN>), L::ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fa_tree_few_kernel<D, FMT, RT>, dim3(grid), dim3(L::THREADS), L::ALLOC,
+  return launch_pdl(fa_tree_few_kernel<D, FMT, RT, WIN>, dim3(grid), dim3(L::THREADS), L::ALLOC,
                     stream, tk, tv, p);
+}
+
+template <int D, int FMT, int RT>
+cudaError_t launch_few_rows(const TreeParams& p, const CUtensorMap& tk,
+                            const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  return p.window ? launch_few_win<D, FMT, RT, true>(p, tk, tv, grid, stream)
+                  : launch_few_win<D, FMT, RT, false>(p, tk, tv, grid, stream);
 }
 
 template <int D, int FMT>

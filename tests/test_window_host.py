@@ -103,3 +103,35 @@ def test_gradient_formula_against_differences():
         h = 1e-5
         # central differences of a smooth function: h^2, and rounding over h
         assert abs((f(h) - f(-h)) / (2 * h) - float((grads[i] * u).sum())) < 1e-6
+
+
+def cached(B=2, H=4, Hkv=2, T=3, d=64, fmt=0, num=8, page=16, most=4, scale=0.1, window=50, sinks=4,
+           mask=A, ptrs=(A,) * 10, ws=A, size=1 << 40):
+    """q, the caches, their scales, table, lengths, drafts, o, lse."""
+    return fa.fa_tree_attention_window(*ptrs[:8], mask, *ptrs[8:], fmt, B, H, Hkv, T, d, num, page,
+                                       most, scale, window, sinks, ws, size, 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(window=0), BAD), (dict(window=-5), BAD), (dict(sinks=-1), BAD), (dict(sinks=1025), UNSUP),
+    (dict(T=51), UNSUP), (dict(window=2), UNSUP),  # a tree longer than the window
+    (dict(B=0), BAD), (dict(Hkv=3), BAD), (dict(scale=0.0), BAD), (dict(d=32), UNSUP),
+    (dict(page=8), UNSUP), (dict(T=1025, mask=None), UNSUP), (dict(size=100), WS), (dict(ws=None), BAD),
+    (dict(ws=A + 16), ALIGN), (dict(mask=A + 2), ALIGN),
+    (dict(B=1 << 20, H=256, Hkv=256, T=1, d=64, most=1 << 20, mask=None), UNSUP),
+])
+def test_cached_window_refuses(kw, want):
+    assert cached(**kw) == want
+
+
+def test_cached_window_refuses_pointers():
+    for i in range(10):
+        if i not in (3, 4, 7):  # bf16 has no scales; drafts may be null
+            assert cached(ptrs=tuple(None if j == i else A for j in range(10))) == BAD, i
+        if i not in (3, 4):
+            assert cached(ptrs=tuple(A + 2 if j == i else A for j in range(10))) == ALIGN, i
+
+
+def test_sinks_without_a_window():
+    with pytest.raises(ValueError):
+        fa.tree_attention(None, None, None, None, None, sinks=4)
