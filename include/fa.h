@@ -432,6 +432,59 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const uint8_t*
                         const int* counts, void* k, void* v, int format, int B, int Hkv, int N,
                         int d, int num_pages, int page_size, int max_pages, cudaStream_t stream);
 
+/*
+ * Writes N packed tokens by their slots (fa_cache_plan): token n goes to row
+ * slots[n] mod page_size of page slots[n] / page_size.
+ *   k, v     bf16 [Hkv, N, d]; strides null (contiguous), or a host array of
+ *            4 element strides: head, row of k, then of v (rules as in
+ *            fa_qk_norm_rope), so views of a packed projection will do
+ *   slots    int64 [N], 8-byte aligned
+ * Tokens whose slot is negative or outside the pool are skipped.  Everything
+ * else as fa_cache_append; N = 0 returns FA_OK with nothing launched.
+ */
+fa_status fa_cache_append_slots(const void* k, const void* v, const long long* slots,
+                                void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                int format, int Hkv, int N, int d, int num_pages, int page_size,
+                                const long long* strides, cudaStream_t stream);
+
+/*
+ * Pages, slots and positions of a step, worked out on the device: B requests,
+ * request b with lens[b] tokens in the cache and counts[b] more to come.
+ *   lens, counts  int32 [B]; counts[b] < 0: the request has ended, and all
+ *                 pages of its row go back
+ *   page_table    int32 [B, max_pages], read and written; an entry outside
+ *                 [0, num_pages) is no page (written as -1)
+ *   free_pages    int32 [num_pages], a ring: the line of free pages, the
+ *   free_state    int32 [2] (first place, length): page i of the line is
+ *                 free_pages[(first + i) mod num_pages].  Both read and
+ *                 written; a fresh pool: 0 .. num_pages - 1 and {0, num_pages}
+ *   slots         int64 [max_tokens]: where each new token goes, the requests'
+ *                 tokens one after the other; page * page_size + row, or -1
+ *   positions     int32 [max_tokens]: lens[b] + n (fa_qk_norm_rope's)
+ *   cu_seqlens    int32 [B+1]: where each request's tokens begin in them
+ *                 (fa_forward_varlen's, fa_forward_window's)
+ *   granted       int32 [B]: its tokens that have a place, lens[b] + granted[b]
+ *                 being its next length
+ * In this order: (1) with window >= 1 (fa_tree_attention_window; 0: none) the
+ * pages that no token from lens[b] on can see any more go to the end of the
+ * line: from the last page that ends at or before position lens[b] - window
+ * down to the first that is gone already, the first `sinks` tokens' pages
+ * excepted; by request, then by position.  (2) Pages that the new tokens need
+ * and the row does not have are taken from the front of the line, by request,
+ * then by position.  Where the line ends, or the table, a request's tokens
+ * from there on get slot -1 and are not granted (pages given to it stay).
+ * Tokens from max_tokens on are not listed and not granted; slots behind the
+ * last token are -1, positions 0.  lens is clamped to [0, the table's
+ * positions].  The same input gives the same output, whole numbers all.
+ * A page must be in one row, once: pages that rows share must not reach this
+ * call.  B <= 8192; page_size 16, 32, 64 or 128; max_pages * page_size <=
+ * 2^30.  Buffers must not overlap; max_tokens = 0 needs no slots and positions.
+ */
+fa_status fa_cache_plan(const int* lens, const int* counts, int* page_table, int* free_pages,
+                        int* free_state, long long* slots, int* positions, int* cu_seqlens,
+                        int* granted, int B, int max_tokens, int num_pages, int page_size,
+                        int max_pages, int window, int sinks, cudaStream_t stream);
+
 /* Bytes of workspace fa_tree_attention needs, whatever the lengths of the
  * histories.  Its contents on entry do not matter; calls that may run at the
  * same time need workspaces of their own. */

@@ -44,7 +44,7 @@ EXPORTS = (
     "fa_qk_norm_rope", "fa_qk_norm_rope_workspace_size", "fa_qk_norm_rope_backward",
     "fa_cache_append", "fa_cache_read", "fa_tree_attention_workspace_size", "fa_tree_attention",
     "fa_forward_window", "fa_backward_window_workspace_size", "fa_backward_window",
-    "fa_tree_attention_window",
+    "fa_tree_attention_window", "fa_cache_append_slots", "fa_cache_plan",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -117,6 +117,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "fa_cache_read": ([P] * 9 + [I] * 8 + [P], I),
             "fa_tree_attention_workspace_size": ([I] * 5, Z),
             "fa_tree_attention": ([P] * 11 + [I] * 9 + [F, P, Z, P], I),
+            "fa_cache_append_slots": ([P] * 7 + [I] * 6 + [P, P], I),
+            "fa_cache_plan": ([P] * 9 + [I] * 7 + [P], I),
             "fa_tree_attention_window": ([P] * 11 + [I] * 9 + [F, I, I, P, Z, P], I),
             "fa_forward_window": ([P] * 6 + [I] * 6 + [F, I, I, P], I),
             "fa_backward_window_workspace_size": ([I] * 8, Z),
@@ -336,6 +338,26 @@ def fa_tree_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_le
         _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(page_table), _p(hist_lens),
         _p(draft_lens), _p(tree_mask), _p(o), _p(lse), int(format), B, H, Hkv, T, d, num_pages,
         page_size, max_pages, float(scale), _p(workspace), int(workspace_bytes), _s(stream))
+
+
+def fa_cache_append_slots(k, v, slots, k_cache, v_cache, k_scale, v_scale, format, Hkv, N, d,
+                          num_pages, page_size, strides=None, stream=None) -> int:
+    if strides is not None:
+        if len(strides) != 4:
+            raise ValueError("strides: four numbers (head, row of both tensors)")
+        strides = (ctypes.c_longlong * 4)(*strides)
+    return load().fa_cache_append_slots(_p(k), _p(v), _p(slots), _p(k_cache), _p(v_cache),
+                                        _p(k_scale), _p(v_scale), int(format), Hkv, N, d,
+                                        num_pages, page_size, strides, _s(stream))
+
+
+def fa_cache_plan(lens, counts, page_table, free_pages, free_state, slots, positions, cu_seqlens,
+                  granted, B, max_tokens, num_pages, page_size, max_pages, window, sinks,
+                  stream=None) -> int:
+    return load().fa_cache_plan(_p(lens), _p(counts), _p(page_table), _p(free_pages),
+                                _p(free_state), _p(slots), _p(positions), _p(cu_seqlens),
+                                _p(granted), B, max_tokens, num_pages, page_size, max_pages,
+                                window, sinks, _s(stream))
 
 
 def fa_tree_attention_window(q, k_cache, v_cache, k_scale, v_scale, page_table, hist_lens,
@@ -738,6 +760,61 @@ def cache_append(k, v, k_cache, v_cache, page_table, start, counts=None, k_scale
         _check(fa_cache_append(k, v, page_table, start, counts, k_cache, v_cache, k_scale, v_scale,
                                fmt, B, Hkv, N, d, *pages, k.stride()[:3] + v.stride()[:3], s),
                "fa_cache_append")
+
+
+def cache_append_slots(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None):
+    """Writes the packed tokens k, v (bf16 [Hkv, N, d], any strides) into the
+    paged cache, token n at slots[n] (int64, cache_plan's; negative: nowhere).
+    Caches and scales as in cache_append."""
+    import torch
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k, v: expected [Hkv, N, d]")
+    N = int(k.shape[1])
+    no_table = torch.empty((0, 0), dtype=torch.int32, device=k_cache.device)
+    fmt, pages, Hkv, d = _cache_args(k_cache, v_cache, k_scale, v_scale, no_table, 0)
+    for name, t in (("k", k), ("v", v)):
+        _want(name, t, (Hkv, N, d), (torch.bfloat16,), k_cache, contiguous=False)
+        if N and t.stride(2) != 1:
+            raise ValueError(f"{name}: the d elements of a row must be contiguous")
+    _want("slots", slots, (N,), (torch.int64,), k_cache)
+    with _launch_on(k_cache, stream) as s:
+        _check(fa_cache_append_slots(k, v, slots, k_cache, v_cache, k_scale, v_scale, fmt, Hkv, N,
+                                     d, *pages[:2], k.stride()[:2] + v.stride()[:2], s),
+               "fa_cache_append_slots")
+
+
+def cache_plan(lens, counts, page_table, free_pages, free_state, page_size, max_tokens,
+               window=None, sinks=0, stream=None):
+    """(slots, positions, cu_seqlens, granted) of a step in which request b,
+    with lens[b] tokens in the cache, gets counts[b] more (negative: it has
+    ended).  page_table (int32 [B, max_pages]) and the line of free pages
+    (free_pages int32 [num_pages], free_state int32 [2]: first place, length)
+    are brought up to date; with a window, pages behind it go back.  A fresh
+    pool: every entry of the table -1, ``free_pages = torch.arange(num_pages)``,
+    ``free_state = [0, num_pages]``.  max_tokens: at least the sum of counts;
+    slots int64 [max_tokens], -1 behind the last token."""
+    import torch
+    i32 = (torch.int32,)
+    if page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("expected page_table [B, max_pages] and free_pages [num_pages]")
+    if sinks and window is None:
+        raise ValueError("sinks apply to a window")
+    if window is not None and window < 1:
+        raise ValueError("window: at least 1")
+    B, max_pages = page_table.shape
+    _want("page_table", page_table, page_table.shape, i32, page_table)
+    _want("free_pages", free_pages, free_pages.shape, i32, page_table)
+    _want("free_state", free_state, (2,), i32, page_table)
+    _want("lens", lens, (B,), i32, page_table)
+    _want("counts", counts, (B,), i32, page_table)
+    with _launch_on(page_table, stream) as s:
+        new = lambda n, t: torch.empty(n, dtype=t, device=page_table.device)
+        slots, positions = new(max_tokens, torch.int64), new(max_tokens, torch.int32)
+        cu, granted = new(B + 1, torch.int32), new(B, torch.int32)
+        _check(fa_cache_plan(lens, counts, page_table, free_pages, free_state, slots, positions,
+                             cu, granted, B, max_tokens, free_pages.numel(), page_size, max_pages,
+                             window or 0, sinks, s), "fa_cache_plan")
+    return slots, positions, cu, granted
 
 
 def cache_read(k_cache, v_cache, page_table, start, N, counts=None, k_scale=None, v_scale=None,

@@ -33,6 +33,7 @@ struct CacheParams {
   void *kc, *vc;             // caches
   uint8_t *ks, *vs;          // scale bytes [num_pages, Hkv, page]
   const int *page_table, *start, *counts;
+  const long long* slots;    // of each token, in place of the three
   void *k, *v;               // bf16 rows: read (append) or written (read)
   Strides sk, sv;
   int B, Hkv, N, num_pages, log_page, max_pages;
@@ -50,9 +51,16 @@ FA_DEV long long cache_row(const CacheParams& p, int b, int h, uint32_t n, int s
          (pos & ((1 << p.log_page) - 1));
 }
 
+// The same by the token's slot (page * page_size + row).
+FA_DEV long long slot_row(const CacheParams& p, int h, uint32_t n, uint32_t count) {
+  const long long slot = n < count ? p.slots[n] : -1;
+  if (slot < 0 || (slot >> p.log_page) >= p.num_pages) return -1;
+  return (((slot >> p.log_page) * p.Hkv + h) << p.log_page) + (slot & ((1 << p.log_page) - 1));
+}
+
 // One block: blockDim / 32 * RPW * U consecutive tokens of one (sequence,
 // k or v, head).
-template <int D, int FMT, bool WRITE, int U>
+template <int D, int FMT, bool WRITE, int U, bool SLOTS>
 __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
   grid_dep_wait();  // the previous kernel's writes are visible from here on
   grid_dep_launch();
@@ -63,9 +71,9 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
   const int b = bkh / (2 * p.Hkv), kh = bkh - b * 2 * p.Hkv;
   const bool isk = kh < p.Hkv;
   const int h = isk ? kh : kh - p.Hkv;
-  const int start = p.start[b], l = lane % LPR;
+  const int start = SLOTS ? 0 : p.start[b], l = lane % LPR;
   // (unsigned: N may be close to 2^31, and the last block reaches past it)
-  const uint32_t count = p.counts ? max(min(p.counts[b], p.N), 0) : p.N;
+  const uint32_t count = !SLOTS && p.counts ? max(min(p.counts[b], p.N), 0) : p.N;
   const uint32_t n0 = static_cast<uint32_t>(chunk) * per + warp * RPW * U + lane / LPR;
   const Strides s = isk ? p.sk : p.sv;
   uint16_t* x0 = static_cast<uint16_t*>(isk ? p.k : p.v) + b * s.b + h * s.h + 8 * l;
@@ -76,7 +84,8 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
 
   long long row[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) row[u] = cache_row(p, b, h, n0 + u * RPW, start, count);
+  for (int u = 0; u < U; ++u) row[u] = SLOTS ? slot_row(p, h, n0 + u * RPW, count)
+                                              : cache_row(p, b, h, n0 + u * RPW, start, count);
   if (WRITE) {
     uint4 x[U];
 #pragma unroll
@@ -149,7 +158,7 @@ __global__ void __launch_bounds__(256) fa_cache_kernel(const CacheParams p) {
   }
 }
 
-template <int D, int FMT, bool WRITE>
+template <int D, int FMT, bool WRITE, bool SLOTS>
 cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   constexpr int RPW = 32 / (D / 8);
   // Up to 8 RPW tokens (a decode step, a tree): one block per (sequence, k or
@@ -162,21 +171,21 @@ cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N - 1) / per + 1);
   if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(warps * 32);
-  return wide ? launch_pdl(fa_cache_kernel<D, FMT, WRITE, 8>, grid, block, 0, stream, p)
-              : launch_pdl(fa_cache_kernel<D, FMT, WRITE, 1>, grid, block, 0, stream, p);
+  return wide ? launch_pdl(fa_cache_kernel<D, FMT, WRITE, 8, SLOTS>, grid, block, 0, stream, p)
+              : launch_pdl(fa_cache_kernel<D, FMT, WRITE, 1, SLOTS>, grid, block, 0, stream, p);
 }
 
-template <bool WRITE>
+template <bool WRITE, bool SLOTS = false>
 fa_status dispatch(const CacheParams& p, int format, int d, cudaStream_t stream) {
   cudaError_t e;
   if (d == 64)
-    e = format == kCacheBf16   ? launch_cache<64, kCacheBf16, WRITE>(p, stream)
-        : format == kCacheE4m3 ? launch_cache<64, kCacheE4m3, WRITE>(p, stream)
-                               : launch_cache<64, kCacheInt8, WRITE>(p, stream);
+    e = format == kCacheBf16   ? launch_cache<64, kCacheBf16, WRITE, SLOTS>(p, stream)
+        : format == kCacheE4m3 ? launch_cache<64, kCacheE4m3, WRITE, SLOTS>(p, stream)
+                               : launch_cache<64, kCacheInt8, WRITE, SLOTS>(p, stream);
   else
-    e = format == kCacheBf16   ? launch_cache<128, kCacheBf16, WRITE>(p, stream)
-        : format == kCacheE4m3 ? launch_cache<128, kCacheE4m3, WRITE>(p, stream)
-                               : launch_cache<128, kCacheInt8, WRITE>(p, stream);
+    e = format == kCacheBf16   ? launch_cache<128, kCacheBf16, WRITE, SLOTS>(p, stream)
+        : format == kCacheE4m3 ? launch_cache<128, kCacheE4m3, WRITE, SLOTS>(p, stream)
+                               : launch_cache<128, kCacheInt8, WRITE, SLOTS>(p, stream);
   FA_CUDA(e);
   return FA_OK;
 }
@@ -248,6 +257,36 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const uint8_t*
   p.k = k;
   p.v = v;
   return dispatch<false>(p, format, d, stream);
+}
+
+fa_status fa_cache_append_slots(const void* k, const void* v, const long long* slots,
+                                void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                int format, int Hkv, int N, int d, int num_pages, int page_size,
+                                const long long* strides, cudaStream_t stream) {
+  using namespace fa;
+  if (N < 0) return FA_ERR_INVALID_ARG;
+  CacheParams p = {};
+  // (no table, start or counts here: the checks of what there is)
+  FA_TRY(cache_params(k_cache, v_cache, k_scale, v_scale, static_cast<const int*>(k_cache),
+                      static_cast<const int*>(k_cache), nullptr, format, 1, Hkv, N > 0 ? N : 1, d,
+                      num_pages, page_size, 1, &p));
+  if (N == 0) return FA_OK;  // no token: nothing to write
+  FA_TRY(check_ptr16(k));
+  FA_TRY(check_ptr16(v));
+  if (!slots) return FA_ERR_INVALID_ARG;
+  if (!aligned(slots, 8)) return FA_ERR_MISALIGNED;
+  long long s[2][3];
+  for (int i = 0; strides && i < 2; ++i) {
+    s[i][0] = 0;
+    s[i][1] = strides[2 * i];
+    s[i][2] = strides[2 * i + 1];
+  }
+  FA_TRY(read_strides(strides ? s[0] : nullptr, 1, Hkv, N, d, &p.sk));
+  FA_TRY(read_strides(strides ? s[1] : nullptr, 1, Hkv, N, d, &p.sv));
+  p.k = const_cast<void*>(k);
+  p.v = const_cast<void*>(v);
+  p.slots = slots;
+  return dispatch<true, true>(p, format, d, stream);
 }
 
 }  // extern "C"

@@ -135,3 +135,59 @@ def test_cached_window_refuses_pointers():
 def test_sinks_without_a_window():
     with pytest.raises(ValueError):
         fa.tree_attention(None, None, None, None, None, sinks=4)
+
+
+def plan(B=2, tokens=5, num=8, page=16, most=4, window=0, sinks=0, ptrs=(A,) * 9):
+    return fa.fa_cache_plan(*ptrs, B, tokens, num, page, most, window, sinks, 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=0), BAD), (dict(B=8193), UNSUP), (dict(tokens=-1), BAD), (dict(num=0), BAD),
+    (dict(page=8), UNSUP), (dict(page=48), UNSUP), (dict(most=0), BAD),
+    (dict(most=(1 << 26) + 1), UNSUP), (dict(window=-1), BAD), (dict(sinks=-1), BAD),
+])
+def test_plan_refuses_sizes(kw, want):
+    assert plan(**kw) == want
+
+
+def test_plan_refuses_pointers():
+    for i in range(9):
+        assert plan(ptrs=tuple(None if j == i else A for j in range(9))) == BAD, i
+        off = A + 4 if i == 5 else A + 2  # slots are 64-bit
+        assert plan(ptrs=tuple(off if j == i else A for j in range(9))) == ALIGN, i
+
+
+def slots(fmt=1, Hkv=2, N=4, d=64, num=8, page=16, strides=None, ptrs=(A,) * 7):
+    return fa.fa_cache_append_slots(*ptrs, fmt, Hkv, N, d, num, page, strides, 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(N=-1), BAD), (dict(Hkv=0), BAD), (dict(num=0), BAD), (dict(fmt=-1), BAD), (dict(fmt=3), BAD),
+    (dict(d=32), UNSUP), (dict(page=8), UNSUP), (dict(num=1 << 30), UNSUP),
+    (dict(Hkv=1 << 10, N=1 << 22), UNSUP), (dict(strides=(256, 60, 256, 64)), ALIGN),
+    (dict(strides=(256, 64, -8, 64)), BAD), (dict(strides=(1 << 62, 64, 256, 64)), BAD),
+])
+def test_slots_refuse_sizes(kw, want):
+    assert slots(**kw) == want
+
+
+def test_slots_refuse_pointers():
+    for i in range(7):
+        assert slots(ptrs=tuple(None if j == i else A for j in range(7))) == BAD, i
+        off = A + 4 if i == 2 else A + 2
+        assert slots(ptrs=tuple(off if j == i else A for j in range(7))) == ALIGN, i
+    with pytest.raises(ValueError):
+        slots(strides=(256, 64, 256))
+    assert slots(N=0, ptrs=(None, None, None) + (A,) * 4) == fa.FA_OK
+
+
+def test_plan_and_slots_python_refusals():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    args = (i32(2), i32(2), i32(2, 4), i32(8), i32(2), 16, 4)
+    for kw in (dict(), dict(sinks=3), dict(window=0)):  # (the first: tensors on the CPU)
+        with pytest.raises(ValueError):
+            fa.cache_plan(*args, **kw)
+    k = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    c = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        fa.cache_append_slots(k, k, c, c, torch.zeros(4, dtype=torch.int64))
