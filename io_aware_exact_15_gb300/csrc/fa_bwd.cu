@@ -47,6 +47,7 @@
 #include "fa_ptx.cuh"
 #include "fa_philox.cuh"
 #include "fa_sched.cuh"
+#include "fa_window.cuh"
 
 namespace fa {
 namespace {
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (p.causal && qrow - kcol0 + 1 < lim) lim = qrow - kcol0 + 1;
         uint32_t pw[32];  // pw[i]: keys 2i, 2i+1 of this thread's 64 columns
         // a row with no live statistics gets the bias -inf: all its P are 0
-        const float nb = live ? -lse2 : -INFINITY;
+        const float nb = live ? (WIN ? 15.f : 0.f) - lse2 : -INFINITY;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nlse2x2 = f2_pack(nb, nb);
         // scale * S * log2 e - lse * log2 e for two keys in one fp32 x2 FMA
         auto arg2 = [&](int i) {
@@ -812,18 +813,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 __uint_as_float(sv[i >> 4][(2 * i + 1) & 31])),
                         sl2x2, nlse2x2);
         };
-        if (WIN && need_mask) {
-          const int lo = qrow - p.window + 1 - kcol0, first = p.sinks - kcol0;
-          const uint32_t vis[2] = {reach_bits(lim, lo, first),
-                                   reach_bits(lim - 32, lo - 32, first - 32)};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float a, b;
-            f2_unpack(arg2(i), a, b);
-            a = (vis[i >> 4] >> ((2 * i) & 31)) & 1u ? ex2(a) : 0.f;
-            b = (vis[i >> 4] >> ((2 * i + 1) & 31)) & 1u ? ex2(b) : 0.f;
-            pw[i] = pack_bf16(a, b);
+        if constexpr (WIN) {
+          // Weights are 2^15 P (at most 2^15): rounded to bf16 for the dV
+          // product (2^-8 of each; dV is scaled back at the end), and for dS
+          // kept as fp16, whose rounding is 2^-11 of weights down to 2^-29 of
+          // the row's sum (of the largest sums' 2^-40 below).  dS is then
+          // their fp32 product with 2^-15 (dP - D), rounded once.  (P, dP - D
+          // and their product rounded to bf16, as the other kinds have it:
+          // twice the error of the gradients' own rounding instead of 1.4.)
+          uint32_t vis[2] = {~0u, ~0u};
+          if (need_mask) {
+            const int lo = qrow - p.window + 1 - kcol0, first = p.sinks - kcol0;
+            vis[0] = reach_bits(lim, lo, first);
+            vis[1] = reach_bits(lim - 32, lo - 32, first - 32);
           }
+          p_rows_free();
+          auto weights = [&](auto masked) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int i = 4 * u + j;
+                float a, b;
+                f2_unpack(arg2(i), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                if (masked.value) {
+                  if (!((vis[i >> 4] >> ((2 * i) & 31)) & 1u)) a = 0.f;
+                  if (!((vis[i >> 4] >> ((2 * i + 1) & 31)) & 1u)) b = 0.f;
+                }
+                pw[i] = pack_f16(a, b);
+                w[j] = pack_bf16(a, b);
+              }
+              st_shared_v4(pbuf + sw128_offset(r, u), w[0], w[1], w[2], w[3]);
+            }
+          };
+          if (need_mask)
+            weights(std::true_type{});
+          else
+            weights(std::false_type{});
         } else if (need_mask) {  // (warp-uniform) the tile crosses N or the diagonal
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -843,7 +872,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         // keep bits of this thread's 64 keys (bit k of kb[c]: key 32 c + k)
         uint32_t kb[2] = {0u, 0u};
-        p_rows_free();
+        if (!WIN) p_rows_free();
         if (DROP) {
           // the dV product takes the dropped weights z * P; dS needs P and z
 #pragma unroll
@@ -863,7 +892,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                             (keep_nibble(mk[2]) << 8) | (keep_nibble(mk[3]) << 12))
                            << (16 * (g4 & 1));
           }
-        } else {
+        } else if (!WIN) {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             st_shared_v4(pbuf + sw128_offset(r, u), pw[4 * u], pw[4 * u + 1], pw[4 * u + 2],
@@ -881,6 +910,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint64_t dltx2 = f2_pack(dlt_c, dlt_c);
+        const float low = 1.f / kPLift, ndl = -dlt_c * low;  // (WIN)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t dp[32];
@@ -902,6 +932,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               // P o (dP - D) for the two keys: dP - D in fp32 x2, rounded to
               // bf16 (the dS written is bf16 anyway), times the packed bf16 P
               float x0, x1;
+              if (WIN) {
+                unpack_f16(pp, x0, x1);
+                f2_unpack(f2_mul(f2_pack(x0, x1), f2_fma(f2_pack(d0, d1), f2_pack(low, low),
+                                                         f2_pack(ndl, ndl))),
+                          x0, x1);
+                w[j] = pack_bf16(x0, x1);
+                continue;
+              }
               f2_unpack(f2_sub(f2_pack(d0, d1), dltx2), x0, x1);
               w[j] = mul_bf16x2(pp, pack_bf16(x0, x1));
             }
@@ -963,7 +1001,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (ok) {  // warp-uniform: every lane takes part in the TMEM reads
         const bool dv_side = half == 0;
         const uint32_t tcol = dv_side ? L::T_DV : L::T_DK;
-        const float mul = dv_side ? (DROP ? p.drop.scale : 1.f) : p.scale;
+        const float mul = !dv_side ? p.scale
+                          : WIN    ? 1.f / kPLift
+                                   : (DROP ? p.drop.scale : 1.f);
         const int krow0 = kbase + 32 * q4;  // key of this warp's first row
         const int nrows = min(32, N - krow0);
         uint8_t* dst = static_cast<uint8_t*>(dv_side ? p.dv : p.dk) +

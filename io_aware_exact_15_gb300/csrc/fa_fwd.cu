@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
       const float mu = (m == -INFINITY) ? 0.f : m;
       const uint64_t sl2x2 = f2_pack(sl2, sl2), nmux2 = f2_pack(-mu, -mu);
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;  // row-sum partials
+      uint64_t lw[2] = {0ull, 0ull};  // WIN: fp32 pairs
       PhiloxOut rw;
       // P (bf16, two per 32-bit column) overwrites the first BC / 2 columns
       // of this tile's S, whose scores are already in registers (group g's
@@ -457,15 +458,21 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
                       e[j], e[j + 1]);
             e[j] = ex2(e[j]);
             e[j + 1] = ex2(e[j + 1]);
+            if (WIN) lw[(j >> 1) & 1] = f2_add(lw[(j >> 1) & 1], f2_pack(e[j], e[j + 1]));
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) sr[q][4 * c4 + j] = pack_bf16(e[2 * j], e[2 * j + 1]);
           // l sums the same bf16-rounded weights the PV MMA consumes, so a
-          // dominant key's rounding cancels in O / l
-          acc_bf16x2(ls0, ls1, sr[q][4 * c4]);
-          acc_bf16x2(ls2, ls3, sr[q][4 * c4 + 1]);
-          acc_bf16x2(ls0, ls1, sr[q][4 * c4 + 2]);
-          acc_bf16x2(ls2, ls3, sr[q][4 * c4 + 3]);
+          // dominant key's rounding cancels in O / l.  WIN: it sums the fp32
+          // weights, which keeps lse exact to fp32 (few keys' roundings do not
+          // average out) and takes one addition per pair instead of four
+          // operations.
+          if (!WIN) {
+            acc_bf16x2(ls0, ls1, sr[q][4 * c4]);
+            acc_bf16x2(ls2, ls3, sr[q][4 * c4 + 1]);
+            acc_bf16x2(ls0, ls1, sr[q][4 * c4 + 2]);
+            acc_bf16x2(ls2, ls3, sr[q][4 * c4 + 3]);
+          }
           if (DROP) {
             // dropped weights leave the PV product (l keeps them); one
             // generator call covers keys 32 q + 16 (c4 / 2) .. + 15
@@ -496,6 +503,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
         tmem_st_wait();
       }
       tmem_st_wait();
+      if (WIN) f2_unpack(f2_add(lw[0], lw[1]), ls0, ls1);
       l += (ls0 + ls1) + (ls2 + ls3);
       tc_fence_before();
       mbar_arrive(bar(L::B_PF + s));
@@ -674,7 +682,13 @@ cudaError_t launch_forward(const FwdParams& p, const CUtensorMap& tq, const CUte
   const int nT = (p.N + kTile - 1) / kTile;
   const long long pairs = static_cast<long long>((nT + 1) / 2) * p.B * p.H;
   const int sms = sm_count();
-  const bool compact = p.lists.row_ptr != nullptr || (sms > 0 && pairs <= 4LL * sms);
+  // So do windows up to 16 key tiles at d = 128 and 32 at d = 64: such a walk
+  // is over soon, and a CTA alone on its SM shows its start and end.  16 heads
+  // (4 of K and V) of 16384 rows, 4 sinks, two-tile | compact, us: d = 128,
+  // window 256 105 | 90, 1024 167 | 154, 2048 243 | 232, 4096 365 | 369;
+  // d = 64, 1024 150 | 128, 4096 328 | 310.
+  const bool compact = p.lists.row_ptr != nullptr || (sms > 0 && pairs <= 4LL * sms) ||
+                       (kind == kWindow && p.window <= (p.d == 64 ? 32 : 16) * kTile);
   if (p.d == 64)
     return compact ? launch_forward_kind<64, true>(kind, p, tq, tk, tv, stream)
                    : launch_forward_kind<64, false>(kind, p, tq, tk, tv, stream);

@@ -140,7 +140,7 @@ struct BwdParams {
   // kind kWindow (as FwdParams).  The first sink_tiles key tiles hold keys
   // that every later query sees: their walk over the query tiles is cut into
   // sink_parts units of part_tiles query tiles (of each head of the group),
-  // which leave fp32 dV, dK ([2][128][d] per slot) in `part` when a sequence
+  // which leave fp32 2^15 dV, dK ([2][128][d] per slot) in `part` when a sequence
   // has more than one of them.  bad: [B * Hkv][key tiles][dV, dK][4], a bit
   // per row of a tile that came out with a NaN or an infinity.
   int window = 0, sinks = 0;

@@ -345,6 +345,12 @@ FA_DEV uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// the two halves of a packed fp16x2 word as fp32 (exact)
+FA_DEV void unpack_f16(uint32_t w, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w));
+}
 // elementwise product of two packed bf16x2 words, rounded once to bf16
 FA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;

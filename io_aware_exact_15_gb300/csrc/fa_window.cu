@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
     if (__any_sync(0xffffffffu, odd != 0.f))
       window_row_dkv<D>(w, side == 0, q0, slice, G, k0, j, s.n);
     else
-      acc.store(side == 0 ? p.dv : p.dk, k0 + j, lane, side == 0 ? 1.f : p.scale);
+      acc.store(side == 0 ? p.dv : p.dk, k0 + j, lane, side == 0 ? 1.f / kPLift : p.scale);
     return;
   }
   if (static_cast<int>(blockIdx.x) < nsum + nbad) {

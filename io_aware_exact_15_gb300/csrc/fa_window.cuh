@@ -19,6 +19,10 @@
 
 namespace fa {
 
+// The window backward's weights are 2^15 P (fa_bwd.cu), and so is what they are
+// summed to before the outputs.
+constexpr float kPLift = 32768.f;
+
 // A lane's elements of a row: E = D / 32 from E * lane on.
 template <int D>
 struct RowPiece {

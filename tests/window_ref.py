@@ -2,9 +2,10 @@
 tests share.  Written from the formulas in include/fa.h; nothing of the
 library is used here.
 
-A rounding to bf16 moves a value by at most 2^-8 of it (half a step).  The
-kernels round P, dP - D, their product dS, and the outputs to bf16; sums are
-fp32.  `off` bounds what fp32 does to a weight: an exponent's argument is a
+A rounding to bf16 moves a value by at most 2^-8 of it (half a step), one to
+fp16 by 2^-11, or by 2^-25 below 2^-14.  The kernels round P to bf16 for its
+products with V and dO, 2^15 P to fp16 for dS, dS and the outputs to bf16; sums
+are fp32.  `off` bounds what fp32 does to a weight: an exponent's argument is a
 sum of d products, scaled and shifted, whose error is below 2^-20 of the sizes
 of its terms, and P moves by that factor.
 """
@@ -51,11 +52,10 @@ def forward(q, k, v, window, sinks, scale):
         p = torch.exp(s - lse[h][:, None])
         off = 2.0 ** -20 * (1 + torch.nan_to_num(size).amax(-1))
         o[h] = _product(p, v[h // G])
-        # each weight rounded, in the product and in the sum it is divided by
-        tol_o[h] = (2 * HALF_BF16 + 2 * off[:, None]) * (p @ torch.nan_to_num(v[h // G]).abs()) \
+        # each weight rounded in the product, not in the sum it is divided by
+        tol_o[h] = (HALF_BF16 + 2 * off[:, None]) * (p @ torch.nan_to_num(v[h // G]).abs()) \
             + HALF_BF16 * o[h].abs() + 1e-30
-        # the sum's weights are rounded (2^-8 of it at most), lse is its logarithm
-        tol_l[h] = HALF_BF16 + off + 2.0 ** -20 * lse[h].abs()
+        tol_l[h] = off + 2.0 ** -20 * lse[h].abs()
     return o, lse, tol_o, tol_l
 
 
@@ -75,11 +75,14 @@ def backward(q, k, v, o, lse, g, window, sinks, scale):
         # (scores without a NaN's own: a weight's error is counted by row)
         off = 2.0 ** -20 * (1 + torch.nan_to_num(size) + torch.nan_to_num(lse[h]).abs()[:, None])
         ds = torch.where(see, p * (g[h] @ vh.T - dlt), torch.zeros((), dtype=torch.float64))
-        # dS: P, dP - D and their product rounded; dP and D are fp32 sums
+        # dS: P and its product with dP - D rounded; dP and D are fp32 sums
         fine = torch.nan_to_num
         inner = 2.0 ** -20 * (fine(g[h]).abs() @ fine(vh).abs().T
                               + (fine(g[h]) * fine(o[h])).abs().sum(-1, keepdim=True))
-        err = fine(ds).abs() * (3.02 * HALF_BF16 + 2 * off) + fine(p) * inner
+        err = fine(ds).abs() * (1.02 * HALF_BF16 + 2.0 ** -11 + 2 * off) + fine(p) * inner
+        # (weights below 2^-29: fp16's smallest steps)
+        err += torch.where(see, 2.0 ** -40 * fine(g[h] @ vh.T - dlt).abs(),
+                           torch.zeros((), dtype=torch.float64))
         dq[h] = scale * _product(ds, kh)
         tq[h] = scale * (err @ fine(kh).abs()) + HALF_BF16 * dq[h].abs() + 1e-30
         gk, gv = scale * _product(ds.T, q[h]), _product(p.T, g[h])
