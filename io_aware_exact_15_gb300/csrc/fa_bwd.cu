@@ -52,8 +52,11 @@
 namespace fa {
 namespace {
 
-template <int D>
+// KVB: units whose K and V have a place.  Two let the next unit's first
+// products start behind this one's last: d = 64 windows, whose units are short.
+template <int D, int KVB_ = 1>
 struct BwdSmem {
+  static constexpr int KVB = KVB_;
   static constexpr int CH = D / 64;
   static constexpr int CHUNK = kTile * 128;
   static constexpr int TILE = CH * CHUNK;
@@ -62,7 +65,7 @@ struct BwdSmem {
   static constexpr int PT = 2 * CHUNK;  // 128 x 128 bf16
   static constexpr int K = 0;
   static constexpr int V = K + TILE;
-  static constexpr int QR = V + TILE;
+  static constexpr int QR = 2 * KVB * TILE;
   static constexpr int DOR = QR + NQ * TILE;
   static constexpr int P = DOR + NDO * TILE;
   static constexpr int DS = P + PT;
@@ -78,7 +81,9 @@ struct BwdSmem {
                        B_FIN = B_DQE + 1, B_SPL = B_FIN + 1, B_EPI = B_SPL + 1;
   // ring of unit indices handed out by the producer (block-sparse kernel)
   static constexpr int NU = 4;
-  static constexpr int B_UF = B_EPI + 1, B_UE = B_UF + NU, NBAR = B_UE + NU;
+  static constexpr int B_UF = B_EPI + 1, B_UE = B_UF + NU;
+  // KVB = 2: the second place's arrival, both places' release
+  static constexpr int B_KV2 = B_UE + NU, B_KVE = B_KV2 + 1, NBAR = B_KVE + KVB;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int RING = MISC + 16;  // NU ints
   static constexpr int ALLOC = RING + 4 * NU + 1024;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tdq, const BwdParams p) {
-  using L = BwdSmem<D>;
+  using L = BwdSmem<D, (D == 64 && KIND == kWindow) ? 2 : 1>;
   // with dQ reduce-adds, no early grid_dep_launch: with it here and in the
   // dQ conversion, 8 x 16 x 2048 rows of 128 took 744 us instead of 709
   if (!DQ) grid_dep_launch();
@@ -274,6 +279,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (k >= L::NU && !wait_bar(bar(L::B_UE + slot), ph ^ 1, wcu)) return false;
       int uu = k == 0 ? static_cast<int>(blockIdx.x)
                       : static_cast<int>(gridDim.x) + atomicAdd(p.unit_counter, 1);
+      if (WIN) {  // packed sequences: not the units behind a shorter one's end
+        BwdUnit w;
+        while (uu < nunits && !unit_at(uu, w))
+          uu = static_cast<int>(gridDim.x) + atomicAdd(p.unit_counter, 1);
+      }
       if (uu >= nunits) uu = -1;
       ring[slot] = uu;
       mbar_arrive(bar(L::B_UF + slot));
@@ -331,6 +341,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::B_KV), 1);
+    if (L::KVB == 2) {
+      mbar_init(bar(L::B_KV2), 1);
+      mbar_init(bar(L::B_KVE), 1);
+      mbar_init(bar(L::B_KVE + 1), 1);
+    }
     for (int s = 0; s < L::NQ; ++s) {
       mbar_init(bar(L::B_QF + s), 1);
       mbar_init(bar(L::B_QE + s), 1);
@@ -383,15 +398,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       BwdUnit un;
       // K_j, V_j of the current unit once every product of the previous unit
       // is done (that unit's final commit also follows its own K/V arrival)
+      // (KVB = 2: once those of the unit before the previous one are)
       auto load_kv = [&]() -> bool {
-        if (nkv > 0 && !wait_bar(bar(L::B_FIN), (nkv - 1) & 1, wc)) return false;
-        mbar_arrive_expect_tx(bar(L::B_KV), 2 * L::TILE);
+        const uint32_t slot = nkv % L::KVB, at = slot * 2 * L::TILE;
+        const uint32_t full = bar(slot ? L::B_KV2 : L::B_KV);
+        if (L::KVB == 2) {
+          if (nkv > 1 && !wait_bar(bar(L::B_KVE + slot), (nkv / 2 - 1) & 1, wc)) return false;
+        } else if (nkv > 0 && !wait_bar(bar(L::B_FIN), (nkv - 1) & 1, wc)) {
+          return false;
+        }
+        mbar_arrive_expect_tx(full, 2 * L::TILE);
 #pragma unroll
         for (int c = 0; c < L::CH; ++c) {
-          tma_load_3d(sb + L::K + c * L::CHUNK, &tk, bar(L::B_KV), 64 * c,
-                      un.row0 + un.kt * kTile, un.zkv);
-          tma_load_3d(sb + L::V + c * L::CHUNK, &tv, bar(L::B_KV), 64 * c,
-                      un.row0 + un.kt * kTile, un.zkv);
+          tma_load_3d(sb + L::K + at + c * L::CHUNK, &tk, full, 64 * c, un.row0 + un.kt * kTile,
+                      un.zkv);
+          tma_load_3d(sb + L::V + at + c * L::CHUNK, &tv, full, 64 * c, un.row0 + un.kt * kTile,
+                      un.zkv);
         }
         ++nkv;
         return true;
@@ -400,7 +422,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!unit_at(u, un)) continue;
         Sched sch;
         start(un, uh, sch);
-        bool kv = false;  // the unit's first Q / dO copies go out before its K/V
+        // the unit's first Q / dO copies go out before its K/V, which wait for
+        // the previous unit's end (KVB = 2: they need not, and go first)
+        bool kv = false;
+        if (L::KVB == 2) {
+          if (!(ok = load_kv())) break;
+          kv = true;
+        }
         int qt, g;
         while (ok && sch.next(qt, g, p.lists)) {
           const int qpos = nq % L::NQ, dpos = nd % L::NDO;
@@ -433,7 +461,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok && !kv) ok = load_kv();
       }
       // let copies still in flight land before the CTA can exit
-      if (nkv > 0) drain_bar(bar(L::B_KV), (nkv - 1) & 1, p.wait_ns);
+      for (uint32_t j = nkv > L::KVB ? nkv - L::KVB : 0; j < nkv; ++j)
+        drain_bar(bar(j % L::KVB ? L::B_KV2 : L::B_KV), (j / L::KVB) & 1, p.wait_ns);
       if (!ok) {
         const uint32_t fq = nq > static_cast<uint32_t>(L::NQ) ? nq - L::NQ : 0;
         for (uint32_t j = fq; j < nq; ++j)
@@ -482,9 +511,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (elect_one()) mma_bf16_ss(dst, da, db, idTT, (acc || kk > 0) ? 1u : 0u);
       };
       // dQ[128 q x D] = dS[128 q x 128 k] K[128 k x D]
+      uint32_t sk = sb + L::K, sv = sb + L::V;  // the unit's K and V
       auto dq_step = [&](uint32_t dst, int kk) {
         const uint32_t aoff = (kk >> 2) * L::CHUNK + (kk & 3) * 32;
-        const uint64_t da = kmaj(sb + L::DS + aoff), db = mnmaj(sb + L::K + kk * 2048);
+        const uint64_t da = kmaj(sb + L::DS + aoff), db = mnmaj(sk + kk * 2048);
         if (elect_one()) mma_bf16_ss(dst, da, db, idDQ, kk > 0);
       };
       auto issue_qk = [&](uint32_t dst, uint32_t a, uint32_t b) {
@@ -509,14 +539,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         Sched sch;
         start(un, uh, sch);
         int qt, qt_n, g_unused;
-        ok = uwait(bar(L::B_KV), ku & 1);
+        const uint32_t slot = ku % L::KVB;
+        if (L::KVB == 2) {
+          sk = sb + L::K + slot * 2 * L::TILE;
+          sv = sb + L::V + slot * 2 * L::TILE;
+        }
+        ok = uwait(bar(slot ? L::B_KV2 : L::B_KV), (ku / L::KVB) & 1);
         bool have = ok && sch.next(qt, g_unused, p.lists);
         uint32_t nu = 0;  // steps of this unit
         if (ok && have) {
           ok = uwait(bar(L::B_QF + n % L::NQ), (n / L::NQ) & 1);
           if (ok) {
             tc_fence_after();
-            issue_qk(tS, sb + L::QR + (n % L::NQ) * L::TILE, sb + L::K);
+            issue_qk(tS, sb + L::QR + (n % L::NQ) * L::TILE, sk);
             ecommit(bar(L::B_SF));
             // d = 128: the previous unit's last dQ shares the dP columns
             if (DQ && D != 64 && n > 0) ok = uwait(bar(L::B_DQE), (n - 1) & 1);
@@ -524,7 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (ok) ok = uwait(bar(L::B_DOF + n % L::NDO), (n / L::NDO) & 1);
           if (ok) {
             tc_fence_after();
-            issue_qk(tDP, sb + L::DOR + (n % L::NDO) * L::TILE, sb + L::V);
+            issue_qk(tDP, sb + L::DOR + (n % L::NDO) * L::TILE, sv);
             ecommit(bar(L::B_DPF));
           }
         }
@@ -546,7 +581,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (have_n) {
             if (!(ok = uwait(bar(L::B_QF + n1 % L::NQ), (n1 / L::NQ) & 1))) break;
             tc_fence_after();
-            issue_qk(tS, qn, sb + L::K);
+            issue_qk(tS, qn, sk);
             ecommit(bar(L::B_SF));
           }
           // dK += dS^T Q_i and dQ_i = dS K once dS is in shared memory.
@@ -589,7 +624,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             if (!(ok = uwait(bar(L::B_DOF + n1 % L::NDO), (n1 / L::NDO) & 1))) break;
             tc_fence_after();
-            issue_qk(tDP, sb + L::DOR + (n1 % L::NDO) * L::TILE, sb + L::V);
+            issue_qk(tDP, sb + L::DOR + (n1 % L::NDO) * L::TILE, sv);
             ecommit(bar(L::B_DPF));
           }
           qt = qt_n;
@@ -605,6 +640,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // still to wait for that one: it waits until they have.
         if (nu == 0 && ku > 0 && !uwait(bar(L::B_EPI), (ku - 1) & 1)) ok = false;
         ecommit(bar(L::B_FIN));
+        if (L::KVB == 2) ecommit(bar(L::B_KVE + slot));
         ++ku;
       }
       if (ku > 0) drain_bar(bar(L::B_FIN), (ku - 1) & 1, p.wait_ns);
@@ -647,7 +683,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // P store waits for that read, about a step later.
     // (not with dropout: there the P phase is longer and the deferred half
     // measured slower, 1.81 -> 1.96 ms at B4 H16 N4096)
-    constexpr bool SPLIT = (D == 128) && DQ && !DROP;
+    constexpr bool SPLIT = (D == 128) && DQ && !DROP && !WIN;
     uint32_t dq1[32];
     int t1 = 0, g1 = 0;
     bool dq1_live = false;
@@ -1152,7 +1188,7 @@ template <int D, int KIND, bool DQ = true, bool SPARSE = false, bool DYN = SPARS
 cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, const CUtensorMap& tdo, const CUtensorMap& tdq,
                          cudaStream_t stream) {
-  using L = BwdSmem<D>;
+  using L = BwdSmem<D, (D == 64 && KIND == kWindow) ? 2 : 1>;
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(
       attr_done, reinterpret_cast<const void*>(fa_bwd_kernel<D, KIND, DQ, SPARSE, DYN>),
@@ -1177,8 +1213,11 @@ cudaError_t launch_backward_main(const BwdParams& p, const CUtensorMap& tq, cons
                                  const CUtensorMap& tv, const CUtensorMap& tdo,
                                  const CUtensorMap& tdq, cudaStream_t stream) {
   if (p.window) {
-    if (p.d == 64) return launch_bwd_d<64, kWindow>(p, tq, tk, tv, tdo, tdq, stream);
-    if (p.d == 128) return launch_bwd_d<128, kWindow>(p, tq, tk, tv, tdo, tdq, stream);
+    // units handed out at run time: packed sequences leave many of them empty
+    if (p.d == 64)
+      return launch_bwd_d<64, kWindow, true, false, true>(p, tq, tk, tv, tdo, tdq, stream);
+    if (p.d == 128)
+      return launch_bwd_d<128, kWindow, true, false, true>(p, tq, tk, tv, tdo, tdq, stream);
     return cudaErrorInvalidValue;
   }
   const int kind = p.drop.t ? kGeneralDropout

@@ -226,6 +226,7 @@ SinkSplit sink_split(int N, int window, int sinks) {
 struct WindowWorkspace {
   float *delta, *dq_acc, *part;
   uint32_t* bad;
+  int* unit_counter;  // [1]
   size_t bytes;
 };
 // rows: of all query slices
@@ -245,6 +246,7 @@ WindowWorkspace window_ws(void* ws, size_t rows, int B, int Hkv, int N, int d,
   w.dq_acc = reinterpret_cast<float*>(take(rows * d * sizeof(float)));
   w.part = reinterpret_cast<float*>(take(part));
   w.bad = reinterpret_cast<uint32_t*>(take(bkv * nT * 8 * sizeof(uint32_t)));
+  w.unit_counter = reinterpret_cast<int*>(take(sizeof(int)));
   w.bytes = at;
   return w;
 }
@@ -366,7 +368,8 @@ fa_status fa_backward_window(const void* q, const void* k, const void* v, const 
       !make_tile_map(&tv, v, zkv, rows, d) || !make_tile_map(&tdo, dO, zq, rows, d) ||
       !make_acc_map(&tdq, ws.dq_acc, zq, rows, d))
     return FA_ERR_CUDA;
-  FA_CUDA(launch_bwd_preprocess(o, dO, ws.delta, ws.dq_acc, nullptr, 0, qrows, d, stream));
+  FA_CUDA(launch_bwd_preprocess(o, dO, ws.delta, ws.dq_acc, ws.unit_counter, 1, qrows, d,
+                                stream));
   WindowFinish w;
   BwdParams& p = w.b;
   p.lse = lse;
@@ -390,6 +393,7 @@ fa_status fa_backward_window(const void* q, const void* k, const void* v, const 
   p.sink_parts = split.parts;
   p.part_tiles = split.part_tiles;
   p.bad = ws.bad;
+  p.unit_counter = ws.unit_counter;
   p.err = err;
   p.wait_ns = wait_limit_ns();
   FA_CUDA(launch_backward_main(p, tq, tk, tv, tdo, tdq, stream));
