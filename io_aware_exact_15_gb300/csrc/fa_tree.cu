@@ -92,6 +92,7 @@ FA_DEV uint32_t ring_place(uint32_t g, uint32_t total, bool isv) {
 template <int D, int FMT, bool PAIR>
 struct TreeSmem {
   static constexpr bool Q8 = FMT != kCacheBf16;
+  static constexpr int GROUP = PAIR ? 2 * kTile : kTile;  // query rows of a problem
   static constexpr int CH = D / 64;             // 128-byte column chunks per row
   static constexpr int CHUNK = kTile * 128;     // [128 rows x 128 B] = 16 KB
   static constexpr int TILE = CH * CHUNK;       // one 128 x D bf16 tile
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         if (!ok) break;
         ++parts;
         if (lane == 0) {
-          const int r0 = (ti.it.hr - hkv * p.groups) * 2 * kTile;
+          const int r0 = (ti.it.hr - hkv * p.groups) * L::GROUP;
           const bool two = PAIR && r0 + kTile < p.rows;
           mbar_arrive_expect_tx(bar(L::B_QF + qb), (two ? 2 : 1) * L::TILE);
           for (int i = 0; i < (two ? 2 : 1); ++i)
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     while (ok && it.next(p)) {
       ++part;
       const int hkv = it.hr / p.groups;
-      const int row0 = PAIR ? (it.hr - hkv * p.groups) * 2 * kTile + s * kTile : 0;
+      const int row0 = (it.hr - hkv * p.groups) * L::GROUP + (PAIR ? s * kTile : 0);
       const bool mine_all = row0 < p.rows;             // pair: this warpgroup has rows
       const bool busy = row0 + q4 * 32 < p.rows;       // this warp has rows
       const int row = row0 + r, t = row % p.T;
@@ -930,9 +931,44 @@ int tree_grid(const TreeParams& p, int per_sm) {
   return most < grid ? static_cast<int>(most) : grid;
 }
 
+// Windows make problems of about the same length, known to the host, so CTAs
+// can take whole ones: no parts to store, no second kernel, and no CTA reads
+// the lengths of others' sequences.  That leaves SMs idle when there are fewer
+// problems than SMs, or a last round of them.  It is done where the estimates
+// say so: us per tile, and what cutting costs beside it (4 where each CTA has
+// one tile at most, else 10, 24 with 256-row groups, whose parts are 128 KB).
+// With more than 128 rows, whole problems are 128-row groups if the SMs have
+// one each.  cut | whole, us, 4 key/value heads of 128 but for drafts:
+//   1 token x 16 sequences, bf16, window 128 27.3 | 17.0, 1024 33.4 | 27.3
+//   1 token x 1, bf16, window 128 19.1 | 15.0, 512 19.1 | 21.1
+//   1 token x 64, e4m3, window 4096 70.3 | 66.2
+//   23 drafts, 12 heads of 64, x 8, window 1024 31.4 | 23.2, x 16 45.7 | 39.6
+//   92 rows, bf16, x 32, window 1024 49.8 | 35.5; e4m3 55.9 | 37.5
+//   256 rows, bf16, x 16, window 1024 51.8 | 33.4, x 4, 4096 45.7 | 51.8
+//   256 rows, int8, x 16, window 1024 53.9 | 37.5, 4096 82.6 | 86.7
+void split_window(TreeParams* p, int format, int d) {
+  const bool few = tree_few_rows(p->rows, format);
+  const int sms = sm_count() * (few ? few_ctas(p->rows, format, d) : 1);
+  if (sms <= 0) return;
+  const double us = few                    ? 0.9
+                    : format != kCacheBf16 ? (d == 64 ? 1.1 : 2.0)
+                                           : (d == 64 ? 0.7 : 1.2);
+  const double mt = static_cast<double>(most_tiles(*p));
+  const double bh = static_cast<double>(p->B) * p->Hkv;
+  const double units = bh * p->groups * mt;  // if cut
+  const double per_cta = units / sms > 1 ? units / sms : 1;
+  const double cut = per_cta * us * (p->pair ? 1.45 : 1.0) +
+                     (units <= sms ? 4 : p->pair ? 24 : 10);
+  const int groups = (p->rows + kTile - 1) / kTile;
+  if (ceil(bh * groups / sms) * mt * us > cut || (p->pair && bh * groups > sms)) return;
+  p->whole = 1;
+  p->pair = 0;
+  p->groups = groups;
+}
+
 cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t stream) {
   // tables of one tile: every problem is one unit, nothing to join
-  if (most_tiles(p) == 1) return cudaSuccess;
+  if (p.whole || most_tiles(p) == 1) return cudaSuccess;
   const dim3 blocks((p.slot_rows + 7) / 8, grid);
   return d == 64 ? launch_pdl(fa_tree_join_kernel<64>, blocks, dim3(256), 0, stream, p)
                  : launch_pdl(fa_tree_join_kernel<128>, blocks, dim3(256), 0, stream, p);
@@ -1028,6 +1064,7 @@ fa_status tree_attention(const void* q, const void* k_cache, const void* v_cache
   p.window = window;
   p.sinks = sinks;
   p.scale = scale;
+  if (window) split_window(&p, format, d);
   // units (TreeParams, find_run) are counted in 32 bits
   if (static_cast<long long>(B) * Hkv * p.groups > ((1LL << 31) - 1) / most_tiles(p))
     return FA_ERR_UNSUPPORTED;

@@ -32,6 +32,7 @@ struct TreeParams {
   int B, Hkv, T, rows;     // rows = H / Hkv * T
   int groups, slot_rows;   // row groups per key/value head; rows of a part
   int pair;                // 256-row groups
+  int whole;               // (windows) CTAs take whole problems: nothing to join
   int num_pages, log_page, max_pages, words;
   int window, sinks;       // kernels with a window: at least 1, at least 0
   float scale;
@@ -112,6 +113,19 @@ FA_DEV uint32_t run_begin(uint32_t total, uint32_t c, uint32_t n) {
 // run between two others is empty).  Whole warp.
 template <bool WIN>
 FA_DEV Run find_run(const TreeParams& p, int c, int grid, int lane) {
+  if (WIN && p.whole) {  // an equal number of problems each
+    const uint32_t per_b = p.Hkv * p.groups, problems = p.B * per_b;
+    const uint32_t n = min(problems, static_cast<uint32_t>(grid));
+    Run r = {0, 0, 0, 0, 0, 0, static_cast<int>(n)};
+    if (c >= static_cast<int>(n)) return r;
+    const uint32_t p0 = run_begin(problems, c, n), p1 = run_begin(problems, c + 1, n);
+    r.b = p0 / per_b;
+    r.hr = p0 - r.b * per_b;
+    for (uint32_t i = p0; i < p1; i += 32)
+      r.left += __reduce_add_sync(
+          0xffffffffu, i + lane < p1 ? seq_len<WIN>(p, (i + lane) / per_b).tiles : 0);
+    return r;
+  }
   const uint32_t mine = seq_units<WIN>(p, lane);  // the first 32 sequences
   uint32_t total = __reduce_add_sync(0xffffffffu, mine);
   for (int b0 = 32; b0 < p.B; b0 += 32)

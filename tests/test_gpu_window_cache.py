@@ -172,13 +172,14 @@ def test_same_as_whole_sequence(fmt):
 
 
 def test_window_beyond_everything_is_tree_attention():
-    """The same tiles in the same order: the same bits."""
+    """The same sums, cut in other places: both within the same tolerances."""
     dev = device()
     for T, mask in ((1, None), (9, "tree"), (70, "tree"), (140, None)):
         p = Problem(R.BF16, 2, 4, 2, T, 128, 32, [500, 77], None, mask, 9, dev)
         a, b = p.run(), p.run(window=1 << 30, sinks=4)
         status_ok()
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        p.check(*a)
+        p.check(*b)
 
 
 def test_streams_and_a_graph():
