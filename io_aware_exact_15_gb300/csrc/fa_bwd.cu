@@ -131,8 +131,8 @@ FA_DEV bool bwd_unit(int u, const BwdParams& p, int Hkv, int G, int ntmax, bool 
   int part = 0;
   if (WIN) {
     // the first tiles' parts, then the other tiles, all heads of one together
-    const int v = u / (p.B * Hkv), sunk = p.sink_tiles * p.sink_parts;
-    bkv = u - v * (p.B * Hkv);
+    const int v0 = u / (p.B * Hkv), v = v0 / p.group_parts, sunk = p.sink_tiles * p.sink_parts;
+    bkv = u - v0 * (p.B * Hkv);
     w.kt = v < sunk ? v / p.sink_parts : p.sink_tiles + v - sunk;
     part = v < sunk ? v - w.kt * p.sink_parts : 0;
   } else if (SPARSE) {
@@ -176,15 +176,17 @@ FA_DEV bool bwd_unit(int u, const BwdParams& p, int Hkv, int G, int ntmax, bool 
   }
   w.nT = (w.N + kTile - 1) / kTile;
   if (WIN) {
+    const int v0 = u / (p.B * Hkv);
     w.bkv = bkv;
-    w.slot = -1;
+    w.bq0 += v0 % p.group_parts * (G / p.group_parts);
+    w.slot = p.group_parts > 1 ? bkv * p.slot_units + v0 : -1;
     w.q0 = w.kt;
     w.q1 = window_end(w.kt, w.nT, p.window);
     if (w.kt < p.sink_tiles) {
       w.q0 = w.kt + part * p.part_tiles;
       w.q1 = min(w.nT, w.q0 + p.part_tiles);
       if (w.kt + p.part_tiles < w.nT)
-        w.slot = (bkv * p.sink_tiles + w.kt) * p.sink_parts + part;
+        w.slot = bkv * p.slot_units + v0;
       return w.q0 < w.nT;
     }
   }
@@ -230,7 +232,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int G = GQA ? p.H / p.Hkv : 1;
   constexpr bool WIN = KIND == kWindow;
   const int nunits =
-      p.B * Hkv * (WIN ? ntmax + p.sink_tiles * (p.sink_parts - 1) : ntmax);
+      p.B * Hkv *
+      (WIN ? (ntmax + p.sink_tiles * (p.sink_parts - 1)) * p.group_parts : ntmax);
   constexpr bool DROP = KIND == kGeneralDropout;
   const bool varlen = KIND >= kGeneral && p.cu_seqlens != nullptr;
   const size_t slice_rows = varlen ? static_cast<size_t>(p.total) : static_cast<size_t>(p.N);
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       typename std::conditional<GQA, BwdGroupSchedule, BwdSingleSchedule>::type>::type;
   auto start = [&](const BwdUnit& w, int uh, BwdPartSchedule<Sched0>& ps) {
     if constexpr (WIN)
-      ps.s.init(w.q0, w.q1, G);
+      ps.s.init(w.q0, w.q1, G / p.group_parts);
     else
       ps.s.init(w.kt, w.nT, p.causal != 0, p.lists, w.bq0 % p.H, G);
     ps.left = INT_MAX;
@@ -1196,8 +1199,10 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtens
   if (e != cudaSuccess) return e;
   const int nT = (p.N + kTile - 1) / kTile;
   const long long units =
-      static_cast<long long>(KIND == kWindow ? nT + p.sink_tiles * (p.sink_parts - 1) : nT) * p.B *
-      (p.Hkv > 0 ? p.Hkv : p.H);
+      static_cast<long long>(KIND == kWindow
+                                 ? (nT + p.sink_tiles * (p.sink_parts - 1)) * p.group_parts
+                                 : nT) *
+      p.B * (p.Hkv > 0 ? p.Hkv : p.H);
   // persistent: one CTA per SM (the CTA holds the SM's TMEM and most of its
   // shared memory), each walking units blockIdx.x, blockIdx.x + grid, ...
   const int sms = sm_count();

@@ -56,15 +56,21 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
     // ------------------------------------------------ sums of parts
     const int t = blockIdx.x * 8 + warp;  // ((bkv, tile), dV or dK, row)
     const int r = t & (kTile - 1), side = (t >> 7) & 1, unit = t >> 8;
-    if (unit >= p.B * p.Hkv * p.sink_tiles) return;
-    const int bkv = unit / p.sink_tiles, kt = unit - bkv * p.sink_tiles;
+    const int tiles = p.group_parts > 1 ? ntmax : p.sink_tiles;
+    if (unit >= p.B * p.Hkv * tiles) return;
+    const int bkv = unit / tiles, kt = unit - bkv * tiles;
     const Seq s = sequence(p, bkv / p.Hkv);
     const int nT = (s.n + kTile - 1) / kTile, j = kt * kTile + r;
-    if (j >= s.n || kt + p.part_tiles >= nT) return;  // no such row, or written whole
-    const int parts = (nT - kt + p.part_tiles - 1) / p.part_tiles;
-    const float* src = p.part +
-                       ((static_cast<size_t>(unit) * p.sink_parts * 2 + side) * kTile + r) * D +
-                       lane * RowPiece<D>::E;
+    if (j >= s.n || (p.group_parts == 1 && kt + p.part_tiles >= nT)) return;  // no row, or written whole
+    const bool sunk = kt < p.sink_tiles;
+    const int parts =
+        (sunk ? (nT - kt + p.part_tiles - 1) / p.part_tiles : 1) * p.group_parts;
+    const int first = (sunk ? kt * p.sink_parts : p.sink_tiles * (p.sink_parts - 1) + kt) *
+                      p.group_parts;
+    const float* src =
+        p.part +
+        (((static_cast<size_t>(bkv) * p.slot_units + first) * 2 + side) * kTile + r) * D +
+        lane * RowPiece<D>::E;
     RowPiece<D> acc;
     acc.zero();
     float odd = 0.f;
@@ -97,7 +103,8 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
       s = sequence(p, bkv / p.Hkv);
       const int nT = (s.n + kTile - 1) / kTile;
       // tiles that were written whole
-      if (kt < nT && !(kt < p.sink_tiles && kt + p.part_tiles < nT)) word = p.bad[t];
+      if (p.group_parts == 1 && kt < nT && !(kt < p.sink_tiles && kt + p.part_tiles < nT))
+        word = p.bad[t];
     }
     for (uint32_t some = __ballot_sync(0xffffffffu, word != 0); some; some &= some - 1) {
       const int from = __ffs(some) - 1;
@@ -189,7 +196,9 @@ cudaError_t launch_finish(const WindowFinish& w, cudaStream_t stream) {
   const long long bkv = static_cast<long long>(p.B) * p.Hkv, nT = (p.N + kTile - 1) / kTile;
   const long long rows = p.cu_seqlens ? static_cast<long long>(p.H) * p.total
                                       : static_cast<long long>(p.B) * p.H * p.N;
-  const long long nsum = p.sink_parts > 1 ? bkv * p.sink_tiles * (2 * kTile / 8) : 0;
+  const long long nsum = p.group_parts > 1  ? bkv * nT * (2 * kTile / 8)
+                         : p.sink_parts > 1 ? bkv * p.sink_tiles * (2 * kTile / 8)
+                                            : 0;
   const long long nbad = (8 * bkv * nT + 255) / 256;
   const long long want = (rows * (D / 8) + 256 * kUnroll - 1) / (256 * kUnroll);
   const long long most = 8LL * sm_count();
@@ -207,19 +216,31 @@ cudaError_t launch_window_finish(const WindowFinish& w, cudaStream_t stream) {
 
 namespace {
 
-// How the first key tiles' walks are cut: parts as long as the other tiles'
+// How walks are cut.  The first key tiles': parts as long as the other tiles'
 // walks, of 8 query tiles at least (a part ends with 128 KB of fp32 sums at
-// d = 128, about what three tiles' products cost).
-struct SinkSplit {
-  int tiles, parts, part_tiles;
+// d = 128, about what three tiles' products cost), or 2 where there are fewer
+// key tiles than SMs.  Then the heads of a group go apart too, as far as
+// there are SMs: 1024 rows of 16 heads (4 of K and V), window 256, 114 -> 45 us.
+struct WalkSplit {
+  int tiles, parts, part_tiles, group_parts;
+  long long slot_units(int nT) const {
+    return group_parts > 1 ? (nT + static_cast<long long>(tiles) * (parts - 1)) * group_parts
+           : parts > 1     ? static_cast<long long>(tiles) * parts
+                           : 0;
+  }
 };
-SinkSplit sink_split(int N, int window, int sinks) {
+WalkSplit walk_split(int B, int H, int Hkv, int N, int window, int sinks) {
+  constexpr int kSms = 152;  // (not the device's: workspaces are sized without one)
   const int nT = (N + kTile - 1) / kTile;
-  SinkSplit s;
+  const long long units = static_cast<long long>(B) * Hkv * nT;
+  WalkSplit s;
   s.tiles = ((sinks < N ? sinks : N) + kTile - 1) / kTile;
-  const int walk = (window - 2 + kTile) / kTile + 1;
-  s.part_tiles = walk > 8 ? walk : 8;
+  const int walk = (window - 2 + kTile) / kTile + 1, least = units <= kSms ? 2 : 8;
+  s.part_tiles = walk > least ? walk : least;
   s.parts = s.tiles ? (nT + s.part_tiles - 1) / s.part_tiles : 1;
+  s.group_parts = 1;
+  for (int g = 2; g <= H / Hkv && units * g <= kSms; ++g)
+    if (H / Hkv % g == 0) s.group_parts = g;
   return s;
 }
 
@@ -231,9 +252,9 @@ struct WindowWorkspace {
 };
 // rows: of all query slices
 WindowWorkspace window_ws(void* ws, size_t rows, int B, int Hkv, int N, int d,
-                          const SinkSplit& s) {
+                          const WalkSplit& s) {
   const size_t bkv = static_cast<size_t>(B) * Hkv, nT = (N + kTile - 1) / kTile;
-  const size_t part = s.parts > 1 ? bkv * s.tiles * s.parts * 2 * kTile * d * sizeof(float) : 0;
+  const size_t part = bkv * s.slot_units(static_cast<int>(nT)) * 2 * kTile * d * sizeof(float);
   char* base = static_cast<char*>(ws);
   WindowWorkspace w;
   size_t at = 0;
@@ -273,7 +294,7 @@ fa_status check_window(bool packed, int B, int H, int Hkv, int N, int total, int
     if (rows >= (1LL << 31) || rows * N >= (1LL << 31) || rows * N * d >= (1LL << 31))
       return FA_ERR_UNSUPPORTED;
   }
-  const SinkSplit s = sink_split(N, window < N ? window : N, sinks);
+  const WalkSplit s = walk_split(B, H, Hkv, N, window < N ? window : N, sinks);
   const long long bh = static_cast<long long>(B) * H, nT = (N + kTile - 1) / kTile;
   const long long units = nT + static_cast<long long>(s.tiles) * s.parts;
   // units, and a row of the last kernel's 256 each, are counted in 32 bits
@@ -334,7 +355,8 @@ size_t fa_backward_window_workspace_size(int B, int H, int Hkv, int N, int total
   using namespace fa;
   if (check_window(total > 0, B, H, Hkv, N, total, d, 1.f, window, sinks) != FA_OK) return 0;
   const size_t rows = total > 0 ? static_cast<size_t>(H) * total : static_cast<size_t>(B) * H * N;
-  return window_ws(nullptr, rows, B, Hkv, N, d, sink_split(N, window < N ? window : N, sinks))
+  return window_ws(nullptr, rows, B, Hkv, N, d,
+                   walk_split(B, H, Hkv, N, window < N ? window : N, sinks))
       .bytes;
 }
 
@@ -354,7 +376,7 @@ fa_status fa_backward_window(const void* q, const void* k, const void* v, const 
     FA_TRY(check_ptr16(x));
   FA_TRY(check_ptr4(lse));
   if (window > N) window = N;
-  const SinkSplit split = sink_split(N, window, sinks);
+  const WalkSplit split = walk_split(B, H, Hkv, N, window, sinks);
   const int zq = cu_seqlens ? H : B * H, zkv = cu_seqlens ? Hkv : B * Hkv;
   const int rows = cu_seqlens ? total : N;
   const long long qrows = static_cast<long long>(zq) * rows;
@@ -392,6 +414,8 @@ fa_status fa_backward_window(const void* q, const void* k, const void* v, const 
   p.sink_tiles = split.tiles;
   p.sink_parts = split.parts;
   p.part_tiles = split.part_tiles;
+  p.group_parts = split.group_parts;
+  p.slot_units = static_cast<int>(split.slot_units((N + kTile - 1) / kTile));
   p.bad = ws.bad;
   p.unit_counter = ws.unit_counter;
   p.err = err;

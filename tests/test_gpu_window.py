@@ -260,3 +260,17 @@ def test_two_streams_and_a_graph():
             assert torch.equal(t[m], one[m]), m
         assert bool(((t["dq"] - one["dq"]).abs().float()
                      <= 2 * R.HALF_BF16 * one["dq"].abs().float() + 1e-4).all())
+
+
+@pytest.mark.parametrize("case", [
+    # few key tiles: walks cut by the group's heads too
+    (1, 8, 1, 140, 64, 20, 0), (1, 12, 2, 700, 128, 150, 4), (2, 6, 1, 1100, 64, 260, 129),
+    (1, 16, 4, 1025, 128, 1025, 2), (3, 16, 1, 257, 128, 64, 1),
+])
+def test_few_key_tiles(case):
+    B, H, Hkv, N, d, window, sinks = case
+    x = R.Batch([N] * B, H, Hkv, d, False, 17 + N)
+    check(x, run(x, window, sinks, device()), window, sinks)
+    if B == 1:
+        x = R.Batch([N // 3, 0, N - N // 3], H, Hkv, d, True, 19 + N, 3, 9)
+        check(x, run(x, window, sinks, device()), window, sinks)
