@@ -166,8 +166,12 @@ cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   // flight per lane (16 x 4096 tokens, int8, append and read, before the
   // rounding by addition: 59.7 us; 8 warps 62.0, 2 warps 60.7, four rows per
   // lane 65.7).
-  const bool wide = p.N > 8 * RPW;
-  const int warps = wide ? 4 : (p.N + RPW - 1) / RPW, per = warps * RPW * (wide ? 8 : 1);
+  // By slots: one row per lane up to 16384 warps of them (N tokens of 4 + 4
+  // heads of 128, e4m3, one | eight rows: 64 tokens 6.8 | 8.9 us, 1024 8.9 |
+  // 10.9, 4096 10.9 | 10.9, 8192 15.0 | 13.0, 32768 37.5 | 29.3).
+  const bool wide = SLOTS ? 2LL * p.Hkv * p.N > 16384 * RPW : p.N > 8 * RPW;
+  const int need = (p.N + RPW - 1) / RPW;
+  const int warps = wide ? 4 : need < 8 ? need : 8, per = warps * RPW * (wide ? 8 : 1);
   const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N - 1) / per + 1);
   if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(warps * 32);

@@ -218,7 +218,8 @@ def test_streams_and_a_graph():
 # ------------------------------------------------------------------ writes by slot
 @pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.INT8])
 @pytest.mark.parametrize("N,Hkv,d,page", [(1, 1, 64, 16), (5, 4, 128, 64), (8, 2, 64, 32), (33, 3, 128, 16),
-                                          (300, 2, 64, 128), (1001, 1, 128, 32)])
+                                          (300, 2, 64, 128), (1001, 1, 128, 32),
+                                          (9001, 4, 64, 64), (5003, 4, 128, 16)])
 def test_slots(N, Hkv, d, page, fmt):
     """As if each token had been appended by table and position; skipped tokens
     and all other rows left as they were."""
