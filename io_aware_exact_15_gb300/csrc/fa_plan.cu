@@ -304,39 +304,54 @@ __global__ void __launch_bounds__(32 * kPlanWarps, 1) fa_plan_kernel(const PlanP
   }
 }
 
-// Slots and positions of long lists, over the whole GPU: kTokens consecutive
-// tokens per thread, whose request is found by bisection once.
+// The last of cu[lo .. hi - 1] (ascending) that is <= t, with cu[lo] <= t: 32
+// places looked at together.  Whole warp.
+FA_DEV int last_begin(const int* cu, int lo, int hi, int t, int lane) {
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, at < hi && cu[at] <= t);
+    const int last = 31 - __clz(le);  // lane 0 always is
+    hi = min(hi, lo + (last + 1) * step);
+    lo += last * step;
+  }
+  return lo;
+}
+
+// Slots and positions of long lists, over the whole GPU: a warp takes 32
+// kTokens consecutive ones, finds the requests of its first and last token,
+// and each lane those of its own between them (in a prompt they are the same).
 constexpr int kTokens = 4;
 __global__ void __launch_bounds__(256) fa_plan_tokens_kernel(const PlanParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long t0 = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * kTokens;
-  if (t0 >= p.max_tokens) return;
-  const int listed = p.cu[p.B];
-  int b = 0, hi = p.B;  // the last request that begins at or before t0
-  while (hi - b > 1) {
-    const int mid = (b + hi) >> 1;
-    (p.cu[mid] <= t0 ? b : hi) = mid;
+  const int lane = threadIdx.x & 31;
+  const long long t0 =
+      (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x - lane) * kTokens;
+  const int listed = p.cu[p.B], cap = p.max_pages << p.log_page;
+  int b0 = 0, b1 = 0;
+  if (t0 < listed) {
+    const int t1 = static_cast<int>(min(t0 + 32 * kTokens, static_cast<long long>(listed))) - 1;
+    b0 = last_begin(p.cu, 0, p.B, static_cast<int>(t0), lane);
+    b1 = p.cu[b0 + 1] > t1 ? b0 : last_begin(p.cu, b0, p.B, t1, lane);
   }
-  int begin = p.cu[b], end = p.cu[b + 1];
-  int len = min(max(p.lens[b], 0), p.max_pages << p.log_page), granted = p.granted[b];
 #pragma unroll
   for (int k = 0; k < kTokens; ++k) {
-    const int t = static_cast<int>(t0) + k;
-    if (t0 + k >= p.max_tokens) return;
+    const long long at = t0 + 32 * k + lane;
+    if (at >= p.max_tokens) return;
+    const int t = static_cast<int>(at);
     if (t >= listed) {
       p.slots[t] = -1;
       p.positions[t] = 0;
       continue;
     }
-    if (t >= end) {
-      do end = p.cu[++b + 1];
-      while (t >= end);
-      begin = p.cu[b];
-      len = min(max(p.lens[b], 0), p.max_pages << p.log_page);
-      granted = p.granted[b];
+    int b = b0, hi = b1 + 1;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      (p.cu[mid] <= t ? b : hi) = mid;
     }
-    write_token(p, p.table + static_cast<size_t>(b) * p.max_pages, begin, t - begin, len, granted);
+    const int begin = p.cu[b];
+    write_token(p, p.table + static_cast<size_t>(b) * p.max_pages, begin, t - begin,
+                min(max(p.lens[b], 0), cap), p.granted[b]);
   }
 }
 

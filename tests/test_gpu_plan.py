@@ -334,3 +334,14 @@ def test_a_windowed_server(fmt):
         # 8 bits: f16 weights add at most 2^-31 of the largest value per key
         more = 0 if fmt == R.BF16 else n[b] * 2.0 ** -31 * float(v.abs().max())
         assert bool(((got - ro).abs() <= to + more).all())
+
+
+def test_long_lists_of_single_tokens():
+    """Many requests to a warp's stretch of the list, runs of empty ones."""
+    rng = np.random.default_rng(8)
+    counts = (rng.random(8192) < 0.9).astype(np.int64) * rng.integers(1, 4, 8192)
+    counts[1000:1700] = 0
+    lens = rng.integers(0, 40, 8192)
+    pool = Pool(8192, 4, 33000, 0, device())
+    pool.step(np.zeros(8192), lens, 16, int(lens.sum()), 0, 0)
+    pool.step(lens, counts, 16, int(counts.sum()), 0, 0)
