@@ -48,6 +48,7 @@ EXPORTS = (
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
+_SIX, _FOUR = ctypes.c_longlong * 6, ctypes.c_longlong * 4  # host arrays of strides
 _lock = threading.Lock()
 _lib = None
 
@@ -134,11 +135,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
 
 # ------------------------------------------------------------------ marshalling
 def _p(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    """The address of a tensor; None and integers are ones already."""
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return x
-    return x.data_ptr()
 
 
 def _s(stream):
@@ -289,7 +290,7 @@ def _six(strides):
         return None
     if len(strides) != 6:
         raise ValueError("strides: six numbers (batch, head, row of both tensors)")
-    return (ctypes.c_longlong * 6)(*strides)
+    return _SIX(*strides)
 
 
 def fa_qk_norm_rope(q, k, wq, wk, cos, sin, positions, q_out, k_out, B, H, Hkv, N, d, rot,
@@ -345,7 +346,7 @@ def fa_cache_append_slots(k, v, slots, k_cache, v_cache, k_scale, v_scale, forma
     if strides is not None:
         if len(strides) != 4:
             raise ValueError("strides: four numbers (head, row of both tensors)")
-        strides = (ctypes.c_longlong * 4)(*strides)
+        strides = _FOUR(*strides)
     return load().fa_cache_append_slots(_p(k), _p(v), _p(slots), _p(k_cache), _p(v_cache),
                                         _p(k_scale), _p(v_scale), int(format), Hkv, N, d,
                                         num_pages, page_size, strides, _s(stream))
