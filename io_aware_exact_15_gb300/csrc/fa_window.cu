@@ -83,10 +83,9 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
     for (int e = 0; e < RowPiece<D>::E; ++e) odd = fmaf(acc.x[e], 0.f, odd);
     size_t q0, k0;
     origin(bkv, s, q0, k0);
+    acc.store(side == 0 ? p.dv : p.dk, k0 + j, lane, side == 0 ? 1.f / kPLift : p.scale);
     if (__any_sync(0xffffffffu, odd != 0.f))
       window_row_dkv<D>(w, side == 0, q0, slice, G, k0, j, s.n);
-    else
-      acc.store(side == 0 ? p.dv : p.dk, k0 + j, lane, side == 0 ? 1.f / kPLift : p.scale);
     return;
   }
   if (static_cast<int>(blockIdx.x) < nsum + nbad) {

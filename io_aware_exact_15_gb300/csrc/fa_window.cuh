@@ -7,9 +7,10 @@
 // of the next sequence of a packed batch and what stands behind the last one
 // among them.  Checking tiles on their way in would cost every tile; a row
 // that caught something shows it in its result.  So results are looked at as
-// they are written, and a row with a NaN or an infinity in it is formed again
-// here from the keys (or queries) that belong to it and nothing else.  Rows to
-// which such a number belongs end as soon as every column is NaN.
+// they are written, and the columns of a row that hold a NaN or an infinity are
+// formed again here from the keys (or queries) that belong to it and nothing
+// else.  Where such a number does belong to the row, that ends as soon as all of
+// these columns have one again, since no sum brings them back.
 #pragma once
 
 #include <stdint.h>
@@ -52,20 +53,51 @@ struct RowPiece {
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = fmaf(f, y.x[i], x[i]);
   }
-  // the same sum in every lane
-  FA_DEV float dot(const RowPiece& y) const {
+  FA_DEV float dot(const RowPiece& y) const {  // this lane's share
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) s = fmaf(x[i], y.x[i], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
   }
-  FA_DEV bool all_nan() const {
-    bool n = true;
+};
+
+// Rows taken at a time: their loads and sums over the lanes overlap.
+constexpr int kRowBatch = 4;
+FA_DEV void sum_lanes(float (&s)[kRowBatch]) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) n = n && x[i] != x[i];
-    return __all_sync(0xffffffffu, n);
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+}
+FA_DEV bool not_finite(float x) { return !(fabsf(x) <= 3.402823466e38f); }
+
+// The columns of row `row` that are to be formed again, the others as they are.
+template <int D>
+struct Mend {
+  static constexpr int E = RowPiece<D>::E;
+  RowPiece<D> old, acc;
+  FA_DEV void begin(const void* rows, size_t row, int lane) {
+    // (written by this warp, or by an earlier kernel)
+    const volatile uint32_t* w = reinterpret_cast<const volatile uint32_t*>(
+        static_cast<const uint16_t*>(rows) + row * D + lane * E);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const uint32_t y = w[i];
+      old.x[2 * i] = bf16_lo(y);
+      old.x[2 * i + 1] = bf16_hi(y);
+    }
+    acc.zero();
+  }
+  FA_DEV bool done() const {  // none of them can become finite any more
+    bool d = true;
+#pragma unroll
+    for (int i = 0; i < E; ++i) d = d && (!not_finite(old.x[i]) || not_finite(acc.x[i]));
+    return __all_sync(0xffffffffu, d);
+  }
+  FA_DEV void end(void* rows, size_t row, int lane, float f) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc.x[i] = not_finite(old.x[i]) ? acc.x[i] * f : old.x[i];
+    acc.store(rows, row, lane, 1.f);
   }
 };
 
@@ -76,19 +108,30 @@ static __device__ __noinline__ void window_row_o(const void* q, const void* k, c
                                                  void* o, size_t q0, size_t k0, int i, int window,
                                                  int sinks, float sl2, float lse2) {
   const int lane = threadIdx.x & 31;
-  RowPiece<D> qi, kj, vj, acc;
+  RowPiece<D> qi;
+  Mend<D> m;
   qi.load(q, q0 + i, lane);
-  acc.zero();
-  const int lo = max(i - window + 1, 0), first = min(sinks, lo);
+  m.begin(o, q0 + i, lane);
+  const int lo = max(i - window + 1, 0), first = min(sinks, lo), total = first + i + 1 - lo;
 #pragma unroll 1
-  for (int n = 0; n < first + i + 1 - lo; ++n) {
-    const int j = n < first ? n : lo + n - first;
-    kj.load(k, k0 + j, lane);
-    vj.load(v, k0 + j, lane);
-    acc.add(ex2(fmaf(qi.dot(kj), sl2, -lse2)), vj);
-    if (acc.all_nan()) break;
+  for (int n = 0; n < total && !m.done(); n += kRowBatch) {
+    RowPiece<D> kj[kRowBatch], vj[kRowBatch];
+    float s[kRowBatch];
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+      const int x = min(n + u, total - 1);
+      const size_t j = k0 + (x < first ? x : lo + x - first);
+      kj[u].load(k, j, lane);
+      vj[u].load(v, j, lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) s[u] = qi.dot(kj[u]);
+    sum_lanes(s);
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u)
+      if (n + u < total) m.acc.add(ex2(fmaf(s[u], sl2, -lse2)), vj[u]);
   }
-  acc.store(o, q0 + i, lane, 1.f);
+  m.end(o, q0 + i, lane, 1.f);
 }
 
 // dq of query i: rows q0 + i of q, dO and dq.
@@ -97,20 +140,35 @@ static __device__ __noinline__ void window_row_dq(const WindowFinish& w, size_t 
                                                   int i, float lse2, float delta) {
   const int lane = threadIdx.x & 31;
   const float sl2 = w.b.scale * 1.4426950408889634f;
-  RowPiece<D> qi, gi, kj, vj, acc;
+  RowPiece<D> qi, gi;
+  Mend<D> m;
   qi.load(w.q, q0 + i, lane);
   gi.load(w.dO, q0 + i, lane);
-  acc.zero();
-  const int lo = max(i - w.b.window + 1, 0), first = min(w.b.sinks, lo);
+  m.begin(w.dq, q0 + i, lane);
+  const int lo = max(i - w.b.window + 1, 0), first = min(w.b.sinks, lo), total = first + i + 1 - lo;
 #pragma unroll 1
-  for (int n = 0; n < first + i + 1 - lo; ++n) {
-    const int j = n < first ? n : lo + n - first;
-    kj.load(w.k, k0 + j, lane);
-    vj.load(w.v, k0 + j, lane);
-    acc.add(ex2(fmaf(qi.dot(kj), sl2, -lse2)) * (gi.dot(vj) - delta), kj);
-    if (acc.all_nan()) break;
+  for (int n = 0; n < total && !m.done(); n += kRowBatch) {
+    RowPiece<D> kj[kRowBatch], vj[kRowBatch];
+    float s[kRowBatch], t[kRowBatch];
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+      const int x = min(n + u, total - 1);
+      const size_t j = k0 + (x < first ? x : lo + x - first);
+      kj[u].load(w.k, j, lane);
+      vj[u].load(w.v, j, lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+      s[u] = qi.dot(kj[u]);
+      t[u] = gi.dot(vj[u]);
+    }
+    sum_lanes(s);
+    sum_lanes(t);
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u)
+      if (n + u < total) m.acc.add(ex2(fmaf(s[u], sl2, -lse2)) * (t[u] - delta), kj[u]);
   }
-  acc.store(w.dq, q0 + i, lane, w.b.scale);
+  m.end(w.dq, q0 + i, lane, w.b.scale);
 }
 
 // dv (or dk) of key j of a sequence of N rows, over G query heads whose slices
@@ -120,26 +178,46 @@ static __device__ __noinline__ void window_row_dkv(const WindowFinish& w, bool d
                                                    size_t slice, int G, size_t k0, int j, int N) {
   const int lane = threadIdx.x & 31;
   const float sl2 = w.b.scale * 1.4426950408889634f;
-  RowPiece<D> kj, vj, qi, gi, acc;
+  void* out = dv ? w.b.dv : w.b.dk;
+  RowPiece<D> kj, vj;
+  Mend<D> m;
   kj.load(w.k, k0 + j, lane);
   vj.load(w.v, k0 + j, lane);
-  acc.zero();
+  m.begin(out, k0 + j, lane);
   const int end = j < w.b.sinks || N - j < w.b.window ? N : j + w.b.window;
 #pragma unroll 1
   for (int g = 0; g < G; ++g, q0 += slice) {
 #pragma unroll 1
-    for (int i = j; i < end; ++i) {
-      qi.load(w.q, q0 + i, lane);
-      gi.load(w.dO, q0 + i, lane);
-      const float pij = ex2(fmaf(qi.dot(kj), sl2, -w.b.lse[q0 + i] * 1.4426950408889634f));
-      if (dv)
-        acc.add(pij, gi);
-      else
-        acc.add(pij * (gi.dot(vj) - w.b.delta[q0 + i]), qi);
-      if (acc.all_nan()) break;
+    for (int i = j; i < end && !m.done(); i += kRowBatch) {
+      RowPiece<D> qi[kRowBatch], gi[kRowBatch];
+      float s[kRowBatch], t[kRowBatch], l[kRowBatch], dl[kRowBatch];
+#pragma unroll
+      for (int u = 0; u < kRowBatch; ++u) {
+        const size_t row = q0 + min(i + u, end - 1);
+        qi[u].load(w.q, row, lane);
+        gi[u].load(w.dO, row, lane);
+        l[u] = w.b.lse[row];
+        dl[u] = w.b.delta[row];
+      }
+#pragma unroll
+      for (int u = 0; u < kRowBatch; ++u) {
+        s[u] = kj.dot(qi[u]);
+        t[u] = vj.dot(gi[u]);
+      }
+      sum_lanes(s);
+      if (!dv) sum_lanes(t);
+#pragma unroll
+      for (int u = 0; u < kRowBatch; ++u) {
+        if (i + u >= end) continue;
+        const float pij = ex2(fmaf(s[u], sl2, -l[u] * 1.4426950408889634f));
+        if (dv)
+          m.acc.add(pij, gi[u]);
+        else
+          m.acc.add(pij * (t[u] - dl[u]), qi[u]);
+      }
     }
   }
-  acc.store(dv ? w.b.dv : w.b.dk, k0 + j, lane, dv ? 1.f : w.b.scale);
+  m.end(out, k0 + j, lane, dv ? 1.f : w.b.scale);
 }
 
 }  // namespace fa

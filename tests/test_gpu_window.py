@@ -274,3 +274,20 @@ def test_few_key_tiles(case):
     if B == 1:
         x = R.Batch([N // 3, 0, N - N // 3], H, Hkv, d, True, 19 + N, 3, 9)
         check(x, run(x, window, sinks, device()), window, sinks)
+
+
+def test_an_infinity_that_everyone_sees():
+    """In a first token's value: one column of every later row, formed again
+    only until it is met; the other columns as without it."""
+    dev = device()
+    x = R.Batch([2500], 4, 2, 64, False, 41)
+    clean = run(x, 300, 4, dev)
+    x.v[0, :, 2, 7] = float("inf")
+    o, lse, dq, dk, dv = run(x, 300, 4, dev)
+    assert bool(torch.isinf(o[0, :, 2:, 7]).all()) and torch.equal(lse, clean[1])
+    keep = [c for c in range(64) if c != 7]
+    assert torch.equal(o[..., keep], clean[0][..., keep])
+    # rows 0 and 1 do not see it: formed again, both within the formula's tolerance
+    _, _, tol, _ = R.forward(*(x.seq(t, 0)[:, :2] for t in (x.q, x.k, x.v)), 300, 4, 0.125)
+    assert bool(((o[0, :, :2] - clean[0][0, :, :2]).cpu().double().abs() <= 2 * tol).all())
+    assert bool(torch.isfinite(dv).all()) and not bool(torch.isfinite(dq[0, :, 2:]).any())
