@@ -35,8 +35,8 @@ FA_DEV Seq sequence(const BwdParams& p, int b) {
 
 // The backward's last kernel: dq = bf16(scale * accumulator); the parts of the
 // first key tiles added up in their order; rows with a NaN or an infinity
-// formed again.  Blocks [0, nsum): a warp per row of a first key tile's dV or
-// dK; [nsum, nsum + nbad): a warp per 32 words of `bad`; the rest: dq.
+// formed again.  Blocks [0, nsum): a warp per 4 (d = 64) or 2 rows of a first
+// key tile's dV or dK; [nsum, nsum + nbad): a warp per 32 words of `bad`; the rest: dq.
 template <int D>
 __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinish w, int nsum,
                                                                int nbad) {
@@ -54,38 +54,49 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
   };
   if (static_cast<int>(blockIdx.x) < nsum) {
     // ------------------------------------------------ sums of parts
-    const int t = blockIdx.x * 8 + warp;  // ((bkv, tile), dV or dK, row)
-    const int r = t & (kTile - 1), side = (t >> 7) & 1, unit = t >> 8;
+    constexpr int LPR = D / 8, RPW = 32 / LPR;    // lanes per row, 8 columns each
+    const int t = (blockIdx.x * 8 + warp) * RPW;  // ((bkv, tile), dV or dK, first row)
+    const int r = (t & (kTile - 1)) + lane / LPR, side = (t >> 7) & 1, unit = t >> 8;
     const int tiles = p.group_parts > 1 ? ntmax : p.sink_tiles;
     if (unit >= p.B * p.Hkv * tiles) return;
     const int bkv = unit / tiles, kt = unit - bkv * tiles;
     const Seq s = sequence(p, bkv / p.Hkv);
     const int nT = (s.n + kTile - 1) / kTile, j = kt * kTile + r;
-    if (j >= s.n || (p.group_parts == 1 && kt + p.part_tiles >= nT)) return;  // no row, or written whole
+    // no such rows, or written whole
+    if (j - lane / LPR >= s.n || (p.group_parts == 1 && kt + p.part_tiles >= nT)) return;
     const bool sunk = kt < p.sink_tiles;
     const int parts =
         (sunk ? (nT - kt + p.part_tiles - 1) / p.part_tiles : 1) * p.group_parts;
-    const int first = (sunk ? kt * p.sink_parts : p.sink_tiles * (p.sink_parts - 1) + kt) *
-                      p.group_parts;
+    const int slot = (sunk ? kt * p.sink_parts : p.sink_tiles * (p.sink_parts - 1) + kt) *
+                     p.group_parts;
     const float* src =
-        p.part +
-        (((static_cast<size_t>(bkv) * p.slot_units + first) * 2 + side) * kTile + r) * D +
-        lane * RowPiece<D>::E;
-    RowPiece<D> acc;
-    acc.zero();
-    float odd = 0.f;
+        p.part + (((static_cast<size_t>(bkv) * p.slot_units + slot) * 2 + side) * kTile + r) * D +
+        8 * (lane % LPR);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i)
-#pragma unroll
-      for (int e = 0; e < RowPiece<D>::E; ++e)
-        acc.x[e] += src[static_cast<size_t>(i) * 2 * kTile * D + e];
-#pragma unroll
-    for (int e = 0; e < RowPiece<D>::E; ++e) odd = fmaf(acc.x[e], 0.f, odd);
+    for (int i = 0; i < parts; ++i) {
+      const float4* x = reinterpret_cast<const float4*>(src + static_cast<size_t>(i) * 2 * kTile * D);
+      const float4 y = x[0], z = x[1];
+      a = make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w);
+      b = make_float4(b.x + z.x, b.y + z.y, b.z + z.z, b.w + z.w);
+    }
+    float odd = fmaf(a.x, 0.f, fmaf(a.y, 0.f, fmaf(a.z, 0.f, a.w * 0.f)));
+    odd = fmaf(b.x, 0.f, fmaf(b.y, 0.f, fmaf(b.z, 0.f, fmaf(b.w, 0.f, odd))));
     size_t q0, k0;
     origin(bkv, s, q0, k0);
-    acc.store(side == 0 ? p.dv : p.dk, k0 + j, lane, side == 0 ? 1.f / kPLift : p.scale);
-    if (__any_sync(0xffffffffu, odd != 0.f))
-      window_row_dkv<D>(w, side == 0, q0, slice, G, k0, j, s.n);
+    const float f = side == 0 ? 1.f / kPLift : p.scale;
+    if (j < s.n)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(side == 0 ? p.dv : p.dk) + (k0 + j) * D +
+                                8 * (lane % LPR)) =
+          make_uint4(pack_bf16(a.x * f, a.y * f), pack_bf16(a.z * f, a.w * f),
+                     pack_bf16(b.x * f, b.y * f), pack_bf16(b.z * f, b.w * f));
+    uint32_t again = __ballot_sync(0xffffffffu, j < s.n && odd != 0.f);
+    while (again) {  // (rare) the lanes of one row at a time
+      const int first = (__ffs(again) - 1) / LPR * LPR;
+      again &= ~(((1u << LPR) - 1u) << first);
+      __syncwarp();  // the row was written by its lanes
+      window_row_dkv<D>(w, side == 0, q0, slice, G, k0, __shfl_sync(0xffffffffu, j, first), s.n);
+    }
     return;
   }
   if (static_cast<int>(blockIdx.x) < nsum + nbad) {
@@ -195,9 +206,10 @@ cudaError_t launch_finish(const WindowFinish& w, cudaStream_t stream) {
   const long long bkv = static_cast<long long>(p.B) * p.Hkv, nT = (p.N + kTile - 1) / kTile;
   const long long rows = p.cu_seqlens ? static_cast<long long>(p.H) * p.total
                                       : static_cast<long long>(p.B) * p.H * p.N;
-  const long long nsum = p.group_parts > 1  ? bkv * nT * (2 * kTile / 8)
-                         : p.sink_parts > 1 ? bkv * p.sink_tiles * (2 * kTile / 8)
-                                            : 0;
+  const long long nsum = (p.group_parts > 1  ? bkv * nT
+                          : p.sink_parts > 1 ? bkv * p.sink_tiles
+                                             : 0) *
+                         (2 * kTile * (D / 8) / 256);
   const long long nbad = (8 * bkv * nT + 255) / 256;
   const long long want = (rows * (D / 8) + 256 * kUnroll - 1) / (256 * kUnroll);
   const long long most = 8LL * sm_count();
