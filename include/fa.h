@@ -216,8 +216,11 @@ fa_status fa_backward_varlen(const void* q, const void* k, const void* v, const 
  * The backward enqueues three kernels; dq is summed with fp32 atomics, dk and
  * dv in a fixed order.  Workspace: fa_backward_window_workspace_size bytes for
  * the same sizes (0 for sizes that the calls refuse): D and the fp32 dQ
- * accumulator as in fa_backward, a bit per key row, and, where sequences are
- * longer than 8 tiles and the window, fp32 sums of the sinks' tiles.
+ * accumulator as in fa_backward, a bit per key row, and fp32 sums of the key
+ * tiles whose walk over the queries is cut: the sinks' where sequences are
+ * long, all of them where the batch has few tiles and heads in groups.  Its
+ * contents on entry do not matter; calls that may run at the same time need
+ * workspaces of their own.
  */
 fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o, float* lse,
                             const int* cu_seqlens, int B, int H, int Hkv, int N, int total, int d,
@@ -439,8 +442,8 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const uint8_t*
  *            4 element strides: head, row of k, then of v (rules as in
  *            fa_qk_norm_rope), so views of a packed projection will do
  *   slots    int64 [N], 8-byte aligned
- * Tokens whose slot is negative or outside the pool are skipped.  Everything
- * else as fa_cache_append; N = 0 returns FA_OK with nothing launched.
+ * Tokens whose slot is negative or outside the pool are skipped; no slot may
+ * come twice in a call.  Everything else as fa_cache_append; N = 0 returns FA_OK with nothing launched.
  */
 fa_status fa_cache_append_slots(const void* k, const void* v, const long long* slots,
                                 void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
@@ -477,8 +480,8 @@ fa_status fa_cache_append_slots(const void* k, const void* v, const long long* s
  * last token are -1, positions 0.  lens is clamped to [0, the table's
  * positions].  The same input gives the same output, whole numbers all.
  * A page must be in one row, once: pages that rows share must not reach this
- * call.  B <= 8192; page_size 16, 32, 64 or 128; max_pages * page_size <=
- * 2^30.  Buffers must not overlap; max_tokens = 0 needs no slots and positions.
+ * call.  B <= 8192; page_size 16, 32, 64 or 128; max_pages * page_size and
+ * max_tokens <= 2^30.  Buffers must not overlap; max_tokens = 0 needs no slots and positions.
  */
 fa_status fa_cache_plan(const int* lens, const int* counts, int* page_table, int* free_pages,
                         int* free_state, long long* slots, int* positions, int* cu_seqlens,

@@ -445,6 +445,11 @@ def _varlen_shape(q, k, cu_seqlens, max_seqlen):
     return B, H, int(k.shape[0]), T, d, int(max_seqlen)
 
 
+def _int32(x):
+    """x as a C int that is refused or means the same where x does not fit."""
+    return max(-1, min(x, 2**31 - 1))
+
+
 def _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen):
     """(B, H, Hkv, N, total, d) of a call with a window, its tensors checked."""
     import torch
@@ -482,11 +487,12 @@ def attention_forward(q, k, v, scale=None, causal=False, block_mask=None, worksp
     import torch
     if window is not None:
         sizes = _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen)
+        reach = _int32(window), _int32(sinks)
         scale = (1.0 / sizes[-1] ** 0.5) if scale is None else scale
         with _launch_on(q, stream) as s:
             o = torch.empty_like(q)
             lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-            _check(fa_forward_window(q, k, v, o, lse, cu_seqlens, *sizes, scale, window, sinks, s),
+            _check(fa_forward_window(q, k, v, o, lse, cu_seqlens, *sizes, scale, *reach, s),
                    "fa_forward_window")
         return o, lse
     if sinks:
@@ -537,6 +543,7 @@ def attention_backward(q, k, v, o, dO, lse, scale=None, causal=False, block_mask
     import torch
     if window is not None:
         sizes = _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen)
+        reach = _int32(window), _int32(sinks)
         _want("o", o, q.shape, (torch.bfloat16,), q)
         _want("dO", dO, q.shape, (torch.bfloat16,), q)
         _want("lse", lse, q.shape[:-1], (torch.float32,), q)
@@ -544,10 +551,10 @@ def attention_backward(q, k, v, o, dO, lse, scale=None, causal=False, block_mask
         with _launch_on(q, stream) as s:
             dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
             if workspace is None:
-                workspace = torch.empty(fa_backward_window_workspace_size(*sizes, window, sinks),
+                workspace = torch.empty(fa_backward_window_workspace_size(*sizes, *reach),
                                         dtype=torch.uint8, device=q.device)
             _check(fa_backward_window(q, k, v, o, dO, lse, dq, dk, dv, cu_seqlens, *sizes, scale,
-                                      window, sinks, workspace, _bytes(workspace, q), s),
+                                      *reach, workspace, _bytes(workspace, q), s),
                    "fa_backward_window")
         return dq, dk, dv
     if sinks:
@@ -802,6 +809,8 @@ def cache_plan(lens, counts, page_table, free_pages, free_state, page_size, max_
         raise ValueError("sinks apply to a window")
     if window is not None and window < 1:
         raise ValueError("window: at least 1")
+    if not 0 <= max_tokens <= 2**30:
+        raise ValueError("max_tokens: 0 .. 2^30")
     B, max_pages = page_table.shape
     _want("page_table", page_table, page_table.shape, i32, page_table)
     _want("free_pages", free_pages, free_pages.shape, i32, page_table)
@@ -814,7 +823,7 @@ def cache_plan(lens, counts, page_table, free_pages, free_state, page_size, max_
         cu, granted = new(B + 1, torch.int32), new(B, torch.int32)
         _check(fa_cache_plan(lens, counts, page_table, free_pages, free_state, slots, positions,
                              cu, granted, B, max_tokens, free_pages.numel(), page_size, max_pages,
-                             window or 0, sinks, s), "fa_cache_plan")
+                             _int32(window or 0), _int32(sinks), s), "fa_cache_plan")
     return slots, positions, cu, granted
 
 
@@ -873,6 +882,6 @@ def tree_attention(q, k_cache, v_cache, page_table, hist_lens, draft_lens=None, 
             _check(fa_tree_attention(*args, workspace, _bytes(workspace, q), s),
                    "fa_tree_attention")
         else:
-            _check(fa_tree_attention_window(*args, window, sinks, workspace,
+            _check(fa_tree_attention_window(*args, _int32(window), _int32(sinks), workspace,
                                             _bytes(workspace, q), s), "fa_tree_attention_window")
     return o, lse

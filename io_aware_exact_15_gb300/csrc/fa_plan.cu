@@ -397,6 +397,7 @@ fa_status fa_cache_plan(const int* lens, const int* counts, int* page_table, int
   if (window < 0 || sinks < 0) return FA_ERR_INVALID_ARG;
   if (log2_page(page_size) < 0 || B > kMaxRequests) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(max_pages) * page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  if (max_tokens > (1 << 30)) return FA_ERR_UNSUPPORTED;  // (positions fit in 31 bits)
   for (const void* x : {static_cast<const void*>(lens), static_cast<const void*>(counts),
                         static_cast<const void*>(page_table), static_cast<const void*>(free_pages),
                         static_cast<const void*>(free_state),

@@ -89,6 +89,15 @@ def test_python_refusals():
         fa.attention_forward(q, q, q, causal=True, sinks=4)
 
 
+def test_numbers_past_32_bits():
+    """A C int would take 2^32 + 1 for 1, another window."""
+    assert fa._int32(2**32 + 1) == fa._int32(2**31) == fa._int32(2**31 - 1) == 2**31 - 1
+    assert fa._int32(-2**32 + 1) == fa._int32(-1) == -1 and fa._int32(0) == 0
+    # the longest window there is, and more first tokens than there may be
+    assert fa.fa_backward_window_workspace_size(2, 4, 2, 300, 0, 64, fa._int32(2**40), 4) > 0
+    assert forward(sinks=fa._int32(2**32 + 1)) == UNSUP and forward(window=fa._int32(-2**40)) == BAD
+
+
 def test_gradient_formula_against_differences():
     x = R.Batch([40], 4, 2, 64, False, 2)
     q, k, v, g = (x.seq(t, 0) for t in (x.q, x.k, x.v, x.g))
@@ -145,6 +154,7 @@ def plan(B=2, tokens=5, num=8, page=16, most=4, window=0, sinks=0, ptrs=(A,) * 9
     (dict(B=0), BAD), (dict(B=8193), UNSUP), (dict(tokens=-1), BAD), (dict(num=0), BAD),
     (dict(page=8), UNSUP), (dict(page=48), UNSUP), (dict(most=0), BAD),
     (dict(most=(1 << 26) + 1), UNSUP), (dict(window=-1), BAD), (dict(sinks=-1), BAD),
+    (dict(tokens=(1 << 30) + 1), UNSUP),
 ])
 def test_plan_refuses_sizes(kw, want):
     assert plan(**kw) == want
@@ -187,6 +197,9 @@ def test_plan_and_slots_python_refusals():
     for kw in (dict(), dict(sinks=3), dict(window=0)):  # (the first: tensors on the CPU)
         with pytest.raises(ValueError):
             fa.cache_plan(*args, **kw)
+    for tokens in (-1, 2**30 + 1, 2**32 + 4):
+        with pytest.raises(ValueError, match="max_tokens"):
+            fa.cache_plan(*args[:6], tokens)
     k = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     c = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
