@@ -10,9 +10,11 @@ Raw calls (``fa_forward``, ``fa_backward`` ...) take tensors or integer
 device pointers, the sizes, and a stream (``None`` = PyTorch's current
 stream); they return the ``fa_status`` code.  ``attention_forward`` and
 ``attention_backward`` allocate outputs and raise ``FaError`` on failure;
-so do ``qk_norm_rope`` (and its backward), ``cache_append``,
-``cache_read`` and ``tree_attention``, which also check types, shapes and
-devices (``ValueError``) and run on their tensors' device.
+so do ``qk_norm_rope`` (and its backward), ``cache_plan``,
+``cache_append``, ``cache_append_slots``, ``cache_read`` and
+``tree_attention``, and the attention calls with a ``window``, which also
+check types, shapes and devices (``ValueError``) and run on their tensors'
+device.
 """
 from __future__ import annotations
 

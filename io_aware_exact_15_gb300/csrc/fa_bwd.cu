@@ -36,7 +36,16 @@
 // longer reach back to it; the tiles of the first keys that stay visible are
 // walked to the end of the sequence, in parts of about a window's length (one
 // such walk would outlast everything else), whose fp32 dV, dK the last kernel
-// adds up (fa_window.cu).
+// adds up (fa_window.cu).  Units are handed out at run time: of 6 sequences
+// packed raggedly a third of the units lies behind some sequence's end.
+// Measured with the kernels around it: 6 sequences of up to 4096 rows, 12
+// heads of 64, window 512, 16 first keys: 193 us; 2 x 16 heads (4 of K and V)
+// of 8192 rows of 128, window 1024, 4 first keys: 533 us, 607 TFLOP/s of
+// visible pairs.  Tensor pipe 24 and 36 %, issue 32 and 22 %: a step is the
+// chain S, P, dP, dS, dQ of one 128 x 128 tile with its barriers.  At d = 64
+// P's exponentials and the dQ adds are longer than the products.  Tried and
+// no faster: 16 warps on half the columns each, keys on the lanes with P^T
+// and dS^T from tensor memory, P and dS by warps of their own, dP first.
 // TMEM: S [0,128) dP [128,256) dV [256,256+d) dK [256+d,256+2d);
 //       dQ at [384,448) for d = 64 and over the dP columns for d = 128.
 #include <math.h>

@@ -19,6 +19,8 @@
 // conversions to integers: 4.3), the rest latency: lengths, then the page,
 // then rows, one wave of blocks after the other.  Persistent warps that ask
 // for the next rows before they finish these took 60 instead of 47 us.
+// By slots (fa_cache_append_slots): 32 prompts packed, up to 4096 tokens of 4
+// heads of 128, bf16: 53.4 us, 6.4 TB/s (the bytes at a plain copy's rate: 50.5).
 #include <stdint.h>
 
 #include "../../include/fa.h"

@@ -27,11 +27,19 @@
 // issue order, so P_s is read before the next scores overwrite it.  The K/V
 // ring is 5 (d = 128) or 8 (d = 64) tiles.
 //
-// Compact form (grids of at most four waves of two-tile CTAs, and every
-// grid with a block mask): one query
-// tile per CTA, warps 0-5 only, 256 TMEM columns (S [0,128), O [128,128+d)),
+// Compact form (grids of at most four waves of two-tile CTAs, every grid
+// with a block mask, and windows whose walks are short): one query tile per CTA, warps 0-5 only, 256 TMEM columns (S [0,128), O [128,128+d)),
 // a 2 (d = 128) or 4 (d = 64) tile ring, so that two CTAs share an SM.  The
 // block-size sweep also builds key tiles of 64 and 256 keys (template BC).
+//
+// Sliding windows (kind kWindow): the walk leaves out the tiles between the
+// first keys and the windows; rows whose O caught a NaN or an infinity
+// are formed again (fa_window.cuh).  Measured, 4 first keys: 16 heads (4 of K
+// and V) of 16384 rows of 128, window 1024: 151 us, 884 TFLOP/s counting the
+// visible pairs, 1.1 PFLOP/s counting the visited tiles whole; the tensor pipe
+// is 46 % busy, the rest the start and end of walks of 10 tiles and the
+// softmax between their products.  2 x 12 heads of 1000 rows of 64, window
+// 256: 9.4 us (the bytes: 1.8), a launch and a walk of 4 tiles.
 #include <math.h>
 
 #include "fa_internal.h"

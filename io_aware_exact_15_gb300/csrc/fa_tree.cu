@@ -40,6 +40,14 @@
 // 16 x 64 drafts over up to 8192 keys, int8, 256 rows: 79.1 us (15.2, by the
 // products); both wait for widened tiles: issue slots 52 and 42 % busy.
 //
+// With a window (WIN, fa_tree_attention_window) units are the tiles that some
+// draft sees something of; a problem has few of them (window / 128 and two or
+// three), so its ends weigh more, and whole problems go to the CTAs where
+// there are enough of them (split_window).  8 x 23 drafts of 12 heads of 64,
+// window 2048, 64 first positions, bf16: 24.9 us (the bytes: 7.8); 16 x 64
+// drafts of 16 + 4 heads of 128, window 1024, int8: 32.4 us (3.9): the
+// launch, the search for the run, and one problem's chain of tiles.
+//
 // Keys that nobody may see are never left to chance: scores are replaced by
 // -inf, values of rows past the last token are zeroed in shared memory, and
 // so are NaN and infinite values of drafts, which the rows that do see them

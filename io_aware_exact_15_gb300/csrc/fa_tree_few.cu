@@ -45,6 +45,8 @@
 // keys: 40.8 us, 4.2 TB/s (the bytes at a plain copy's rate: 25.8); 256
 // sequences of 500 keys 47.7 (20.0).  Issue slots are 44 % busy, the
 // ALU 46 %; the rest is the chain of a chunk and the ends of problems.
+// With a window of 4096: 64 sequences x 1 token of up to 32768 e4m3 keys 55.1 us, 4.9
+// TB/s (40.0); 1 sequence x 1 token, window 512, bf16: 12.7 us, two launches.
 #include <math.h>
 #include <stdint.h>
 

@@ -8,6 +8,13 @@
 // the sequence's end crosses.  Their work is about window / 128 + 1 tiles of
 // 128 keys per 128 rows and the first tokens' tiles, so they are bound by the
 // tensor cores and the exponentials as the causal kernels are.
+//
+// The backward is three kernels: D = <dO, O> and a cleared dQ accumulator;
+// the tiles; and what is here.  All but the second are bound by memory: of
+// 533 us for 2 x 16 heads (4 of K and V) of 8192 rows of 128, window 1024, 4
+// first keys, the first takes 40 and the last 35 (4.2 TB/s: fp32 accumulator
+// in, bf16 out), of 193 us for 6 packed sequences of up to 4096 rows, 12 heads
+// of 64, window 512, 16 first keys, 17 and 21.
 #include <math.h>
 #include <stdint.h>
 
