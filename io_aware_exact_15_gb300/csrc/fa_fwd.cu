@@ -28,7 +28,8 @@
 // ring is 5 (d = 128) or 8 (d = 64) tiles.
 //
 // Compact form (grids of at most four waves of two-tile CTAs, every grid
-// with a block mask, and windows whose walks are short): one query tile per CTA, warps 0-5 only, 256 TMEM columns (S [0,128), O [128,128+d)),
+// with a block mask, and windows whose walks are short): one query tile per
+// CTA, warps 0-5 only, 256 TMEM columns (S [0,128), O [128,128+d)),
 // a 2 (d = 128) or 4 (d = 64) tile ring, so that two CTAs share an SM.  The
 // block-size sweep also builds key tiles of 64 and 256 keys (template BC).
 //
@@ -115,6 +116,9 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
   auto bar = [&](int i) { return sb + L::BAR + 8 * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
+  // WIN: the sequence's first row in Q, O, lse and in K, V, kept in shared
+  // memory: in registers they would push others out of the softmax loop
+  const uint32_t origin = sb + L::MISC + 8;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // one query tile per CTA: the compact instantiations
@@ -122,8 +126,18 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
   const int ntmax = (p.N + kTile - 1) / kTile;
   const int npairs = single ? ntmax : (ntmax + 1) / 2;
   const int BH = p.B * p.H;
+  constexpr bool WIN = KIND == kWindow || KIND == kWindowPacked;
+  const bool varlen = WIN ? KIND == kWindowPacked : KIND >= kGeneral && p.cu_seqlens != nullptr;
   int bh, pair;
-  fwd_cta_coords(blockIdx.x, BH, npairs, p.causal != 0, bh, pair);
+  if (WIN && varlen) {
+    const PackedTile t = packed_tile(p.cu_seqlens, p.B, p.total, static_cast<int>(blockIdx.x) / p.H,
+                                     L::NQT * kTile, p.N);
+    if (t.unit < 0) return;  // no query tile here (CTA-uniform)
+    bh = t.b * p.H + static_cast<int>(blockIdx.x) % p.H;
+    pair = t.unit;
+  } else {
+    fwd_cta_coords(blockIdx.x, BH, npairs, p.causal != 0, bh, pair);
+  }
   const int head = bh % p.H;
   // Sequence geometry: length N, first row row0 of the sequence in its
   // slice, the TMA slices zq (Q, O) and zkv (K, V).  Grouped K/V has H / Hkv
@@ -132,7 +146,6 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
   constexpr bool DROP = KIND == kGeneralDropout;
   int N = p.N, row0 = 0, zq = bh, zkv = bh;
   if (KIND == kGrouped || KIND >= kGeneral) zkv = bh / (p.H / p.Hkv);
-  const bool varlen = KIND >= kGeneral && p.cu_seqlens != nullptr;
   if (varlen) {
     // variable-length batch: slices are heads, sequences are row ranges
     // (indices clamped to [0, total], so bad offsets cannot write outside)
@@ -148,7 +161,6 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
   const size_t slice_rows = varlen ? static_cast<size_t>(p.total) : static_cast<size_t>(p.N);
   const int nT = (N + kTile - 1) / kTile;
 
-  constexpr bool WIN = KIND == kWindow;
   FwdScheduleT<BC, WIN> sch;
   sch.init(pair, nT, p.causal != 0, p.lists, head, single, (N + BC - 1) / BC);
   if (WIN) sch.reach(p.window, p.sinks, N);
@@ -178,6 +190,10 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
     }
     mbar_init(bar(L::B_OF), 1);
     *abort_flag = 0;
+    if (WIN) {
+      st_shared_u32(origin, static_cast<uint32_t>(zq * slice_rows + row0));
+      st_shared_u32(origin + 4, static_cast<uint32_t>(zkv * slice_rows + row0));
+    }
     fence_mbar_init();
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
@@ -365,9 +381,15 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
     float m = -INFINITY, l = 0.f;
     int cnt = 0;
     bool ok = true;
-    int kt, mem;
-    while (ok && sch.next(kt, mem)) {
-      if (!(mem & (1 << s))) continue;
+    int kt = -1, mem;
+    // WIN: the schedule of this query tile alone, from what it has to keep anyway
+    auto window_next = [&] {
+      ++kt;
+      if (kt * kTile >= p.sinks) kt = max(kt, max(qt * kTile - p.window + 1, 0) / kTile);
+      return active && kt <= qt;
+    };
+    while (ok && (WIN ? window_next() : sch.next(kt, mem))) {
+      if (!WIN && !(mem & (1 << s))) continue;
       ok = __all_sync(0xffffffffu, wait_bar(bar(L::B_SF + s), cnt & 1, wc));
       if (!ok) break;
       tc_fence_after();
@@ -523,9 +545,9 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
     if (ok && active) {
       const int qrow0 = qt * kTile + q4 * 32;  // this warp's first query row
       const int nrows = min(32, N - qrow0);
-      uint8_t* obase = static_cast<uint8_t*>(p.o) +
-                       (static_cast<size_t>(zq) * slice_rows + row0 + qrow0) *
-                           static_cast<size_t>(D) * 2;
+      const size_t first =
+          WIN ? ld_shared_u32(origin) : static_cast<size_t>(zq) * slice_rows + row0;
+      uint8_t* obase = static_cast<uint8_t*>(p.o) + (first + qrow0) * static_cast<size_t>(D) * 2;
       const bool store = qrow < N;
       const bool has = cnt > 0 && l > 0.f;
       // inverted dropout scales the kept weights by 1 / (1 - p')
@@ -574,7 +596,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
         }
       }
       if (store)
-        p.lse[static_cast<size_t>(zq) * slice_rows + row0 + qrow] =
+        p.lse[first + qrow] =
             has ? (m + lg2(l)) * kLn2 : -INFINITY;
       if (WIN) {
         // (a NaN logsumexp: the row sees a key whose score is one)
@@ -583,9 +605,8 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
         for (; again; again &= again - 1) {  // the rows were written by all lanes
           const int j = __ffs(again) - 1;
           __syncwarp();
-          window_row_o<D>(p.q, p.k, p.v, p.o, static_cast<size_t>(zq) * slice_rows + row0,
-                          static_cast<size_t>(zkv) * slice_rows + row0, qrow0 + j, p.window,
-                          p.sinks, sl2, __shfl_sync(0xffffffffu, lse2, j));
+          window_row_o<D>(p.q, p.k, p.v, p.o, first, ld_shared_u32(origin + 4), qrow0 + j,
+                          p.window, p.sinks, sl2, __shfl_sync(0xffffffffu, lse2, j));
         }
       }
     }
@@ -608,7 +629,9 @@ cudaError_t launch_fwd_d(const FwdParams& p, const CUtensorMap& tq, const CUtens
   if (e != cudaSuccess) return e;
   const int nT = (p.N + kTile - 1) / kTile;
   const int npairs = L::NQT == 1 ? nT : (nT + 1) / 2;
-  const long long ctas = static_cast<long long>(npairs) * p.B * p.H;
+  const long long ctas = KIND == kWindowPacked
+                             ? packed_units(p.B, p.total, L::NQT * kTile) * p.H
+                             : static_cast<long long>(npairs) * p.B * p.H;
   return launch_pdl(fa_fwd_kernel<D, KIND, NS_, BC, CMP>, dim3(static_cast<unsigned>(ctas)),
                     dim3(L::THREADS), L::ALLOC, stream, tq, tk, tv, p);
 }
@@ -666,6 +689,8 @@ cudaError_t launch_forward_kind(int kind, const FwdParams& p, const CUtensorMap&
   if (kind == kGeneralDropout)
     return launch_fwd_d<D, kGeneralDropout, 0, kTile, CMP>(p, tq, tk, tv, stream);
   if (kind == kWindow) return launch_fwd_d<D, kWindow, 0, kTile, CMP>(p, tq, tk, tv, stream);
+  if (kind == kWindowPacked)
+    return launch_fwd_d<D, kWindowPacked, 0, kTile, CMP>(p, tq, tk, tv, stream);
   if (kind == kGeneral) return launch_fwd_d<D, kGeneral, 0, kTile, CMP>(p, tq, tk, tv, stream);
   if (kind == kGrouped) return launch_fwd_d<D, kGrouped, 0, kTile, CMP>(p, tq, tk, tv, stream);
   return launch_fwd_d<D, kPlain, 0, kTile, CMP>(p, tq, tk, tv, stream);
@@ -673,7 +698,7 @@ cudaError_t launch_forward_kind(int kind, const FwdParams& p, const CUtensorMap&
 
 cudaError_t launch_forward(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, cudaStream_t stream) {
-  const int kind = p.window ? kWindow
+  const int kind = p.window ? (p.cu_seqlens ? kWindowPacked : kWindow)
                    : p.drop.t ? kGeneralDropout
                    : p.cu_seqlens ? kGeneral
                    : (p.Hkv > 0 && p.Hkv != p.H) ? kGrouped : kPlain;
@@ -688,7 +713,9 @@ cudaError_t launch_forward(const FwdParams& p, const CUtensorMap& tq, const CUte
   // scattered masks most of those steps hold one tile only (one MMA chain
   // per SM instead of two).
   const int nT = (p.N + kTile - 1) / kTile;
-  const long long pairs = static_cast<long long>((nT + 1) / 2) * p.B * p.H;
+  const long long pairs =
+      kind == kWindowPacked ? packed_units(p.B, p.total, 2 * kTile) * p.H
+                                      : static_cast<long long>((nT + 1) / 2) * p.B * p.H;
   const int sms = sm_count();
   // So do windows up to 16 key tiles at d = 128 and 32 at d = 64: such a walk
   // is over soon, and a CTA alone on its SM shows its start and end.  16 heads
@@ -696,7 +723,7 @@ cudaError_t launch_forward(const FwdParams& p, const CUtensorMap& tq, const CUte
   // window 256 105 | 90, 1024 167 | 154, 2048 243 | 232, 4096 365 | 369;
   // d = 64, 1024 150 | 128, 4096 328 | 310.
   const bool compact = p.lists.row_ptr != nullptr || (sms > 0 && pairs <= 4LL * sms) ||
-                       (kind == kWindow && p.window <= (p.d == 64 ? 32 : 16) * kTile);
+                       (p.window > 0 && p.window <= (p.d == 64 ? 32 : 16) * kTile);
   if (p.d == 64)
     return compact ? launch_forward_kind<64, true>(kind, p, tq, tk, tv, stream)
                    : launch_forward_kind<64, false>(kind, p, tq, tk, tv, stream);

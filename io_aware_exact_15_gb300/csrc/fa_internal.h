@@ -160,7 +160,8 @@ enum KernelKind : int {
   kGrouped = 1,
   kGeneral = 2,
   kGeneralDropout = 3,
-  kWindow = 4
+  kWindow = 4,
+  kWindowPacked = 5  // (forward: its packed batches apart, for their registers' sake)
 };
 
 // 3-D bf16 view {d, N, B*H} of a [B, H, N, d] tensor, box_rows x 64-column

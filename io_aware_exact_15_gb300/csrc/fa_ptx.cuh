@@ -366,6 +366,14 @@ FA_DEV uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // the two halves of a packed bf16x2 word as fp32 (exact)
 FA_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 FA_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+FA_DEV void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+FA_DEV uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 FA_DEV uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"

@@ -212,6 +212,37 @@ struct BwdWindowSchedule {
   }
 };
 
+// Units of `rows` query rows of the windowed forward's packed sequences: those
+// of sequence b are numbered from cu[b] / rows + b on, which leaves room for
+// ceil(n_b / rows) of them and grows with b, so that a unit is found without
+// the lengths of the sequences before it, and the grid has at most one CTA per
+// sequence (and head) too many.  One for every tile of the longest length
+// would cost some 1.3 us of a place each: 16 heads (4 of K and V) of 128,
+// window 1024, one sequence of 13784 rows with seven short ones 292 -> 173 us,
+// 16 of up to 4045 rows 326 -> 289.
+inline long long packed_units(int B, int total, int rows) {
+  return static_cast<long long>(total / rows) + B;
+}
+struct PackedTile {
+  int b, unit;  // sequence; its unit (the longest walks first), or -1: none
+};
+// Whole warp; offsets that break the rules give some unit or none.
+FA_DEV PackedTile packed_tile(const int* cu, int B, int total, int v, int rows, int N) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;  // the last b that begins at or before v
+  while (hi - lo > 1) {  // 32 places looked at together
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const uint32_t le = __ballot_sync(
+        0xffffffffu, at < hi && min(max(cu[at], 0), total) / rows + at <= v);
+    const int last = le ? 31 - __clz(le) : 0;
+    hi = min(hi, lo + (last + 1) * step);
+    lo += last * step;
+  }
+  const int a = min(max(cu[lo], 0), total), e = min(max(cu[lo + 1], a), total);
+  const int units = (min(e - a, N) + rows - 1) / rows, t = v - (a / rows + lo);
+  return PackedTile{lo, t >= 0 && t < units ? units - 1 - t : -1};
+}
+
 // Query tiles behind the last one that sees a key of tile kt (window >= 1).
 FA_DEV int window_end(int kt, int nT, int window) {
   return min(nT, (kt * kTile + kTile - 1 + window - 1) / kTile + 1);

@@ -107,6 +107,22 @@ def test_two_tile_form():
             check(y, [t[b:b + 1] for t in out], 140, 4)
 
 
+@pytest.mark.parametrize("count,longest,lead,window", [(33, 300, 0, 40), (1100, 3, 7, 2),
+                                                       (160, 700, 130, 100000)])
+def test_many_packed_sequences(count, longest, lead, window):
+    """More sequences than a warp looks at together, empty ones among them; the
+    last case in both of the forward's forms."""
+    gen = torch.Generator().manual_seed(count)
+    lens = torch.randint(0, longest + 1, (count,), generator=gen).tolist()
+    for H, Hkv, d in ((1, 1, 64), (6, 2, 128)) if count == 160 else ((2, 1, 64),):
+        x = R.Batch(lens, H, Hkv, d, True, 3, lead, 5)
+        out = run(x, window, 2, device())
+        some = range(count) if count != 160 else (0, 1, 31, 32, 33, 100, 158, 159)
+        y = R.Batch(lens, H, Hkv, d, True, 3, lead, 5)
+        y.lens = [n if b in some else 0 for b, n in enumerate(lens)]
+        check(y, out, window, 2)
+
+
 def test_rows_of_no_sequence_are_left():
     """Rows in front of the first sequence and behind the last."""
     dev = device()
