@@ -210,9 +210,10 @@ fa_status fa_backward_varlen(const void* q, const void* k, const void* v, const 
  * Grouped heads as in fa_forward_gqa.  A row's results depend on the rows that
  * it sees (dk, dv: that see it) alone: a NaN or an infinity anywhere else does
  * not reach it.  window >= 1, 0 <= sinks <= 1024 (more: FA_ERR_UNSUPPORTED);
- * B * H times the 128-row tiles (with those of the sinks, counted once per
- * 8 tiles or window) below 2^23.  Other rules as fa_forward / fa_backward;
- * outputs must not overlap inputs or each other.
+ * B * H times the 128-row tiles of N (with those of the sinks, counted once
+ * per 8 tiles or window) below 2^23, packed with total / 128 + B in place of
+ * B times the tiles where that is less than a third.  Other rules as
+ * fa_forward / fa_backward; outputs must not overlap inputs or each other.
  * The backward enqueues three kernels; dq is summed with fp32 atomics, dk and
  * dv in a fixed order.  Workspace: fa_backward_window_workspace_size bytes for
  * the same sizes (0 for sizes that the calls refuse): D and the fp32 dQ

@@ -195,11 +195,44 @@ FA_DEV bool bwd_unit(int u, const BwdParams& p, int Hkv, int G, int ntmax, bool 
       w.q0 = w.kt + part * p.part_tiles;
       w.q1 = min(w.nT, w.q0 + p.part_tiles);
       if (w.kt + p.part_tiles < w.nT)
-        w.slot = bkv * p.slot_units + v0;
+        w.slot = p.packed ? (w.zkv * p.sink_tiles + w.kt) * p.slot_units +
+                                2 * (w.row0 / (p.part_tiles * kTile)) + part
+                          : bkv * p.slot_units + v0;
       return w.q0 < w.nT;
     }
   }
   return w.kt * kTile < w.N;
+}
+
+// Units of a packed batch as they are handed out: the first tiles' parts, then
+// all tiles, by where their sequences begin (fa_internal.h).
+FA_DEV int packed_handouts(const BwdParams& p, int& parts) {
+  parts = p.total / (p.part_tiles * kTile) + p.B;
+  return p.Hkv * (p.sink_tiles * parts + p.total / kTile + p.B);
+}
+// The unit with this number, or -1.
+FA_DEV int packed_unit(const BwdParams& p, int c) {
+  int parts;
+  packed_handouts(p, parts);
+  const int L = p.part_tiles * kTile, sunk = p.sink_tiles * p.sink_parts;
+  int v = c / p.Hkv, b, v0;
+  const int head = c - v * p.Hkv;
+  auto begin = [&](int rows) { return min(max(p.cu_seqlens[b], 0), p.total) / rows + b; };
+  if (v < p.sink_tiles * parts) {
+    const int kt = v / parts;
+    v -= kt * parts;
+    b = packed_find(p.cu_seqlens, p.B, p.total, v, L, 1);
+    v -= begin(L);
+    if (v < 0 || v >= p.sink_parts) return -1;
+    v0 = kt * p.sink_parts + v;
+  } else {
+    v -= p.sink_tiles * parts;
+    b = packed_find(p.cu_seqlens, p.B, p.total, v, kTile, 1);
+    v -= begin(kTile);
+    if (v < p.sink_tiles || v >= (p.N + kTile - 1) / kTile) return -1;
+    v0 = sunk + v - p.sink_tiles;
+  }
+  return v0 * (p.B * p.Hkv) + b * p.Hkv + head;
 }
 
 // Persistent: each CTA takes one unit of every round of gridDim.x units.  Per
@@ -292,9 +325,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int uu = k == 0 ? static_cast<int>(blockIdx.x)
                       : static_cast<int>(gridDim.x) + atomicAdd(p.unit_counter, 1);
       if (WIN) {  // packed sequences: not the units behind a shorter one's end
+        int parts;
+        const int n = p.packed ? packed_handouts(p, parts) : nunits;
         BwdUnit w;
-        while (uu < nunits && !unit_at(uu, w))
-          uu = static_cast<int>(gridDim.x) + atomicAdd(p.unit_counter, 1);
+        for (int c = uu;; c = static_cast<int>(gridDim.x) + atomicAdd(p.unit_counter, 1)) {
+          uu = c >= n ? nunits : p.packed ? packed_unit(p, c) : c;
+          if (uu >= nunits || (uu >= 0 && unit_at(uu, w))) break;
+        }
       }
       if (uu >= nunits) uu = -1;
       ring[slot] = uu;
@@ -1157,10 +1194,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           __syncwarp();
         }
         if (WIN && ok && order < 0) {
+          const size_t bad_tile =
+              p.packed ? static_cast<size_t>(un.zkv) * (p.total / kTile + p.B) +
+                             un.row0 / kTile + un.bkv / Hkv + un.kt
+                       : static_cast<size_t>(un.bkv) * ntmax + un.kt;
           const uint32_t rows = __ballot_sync(0xffffffffu, odd != 0.f && lane < nrows);
           if (lane == 0)
-            p.bad[((static_cast<size_t>(un.bkv) * ntmax + un.kt) * 2 + (dv_side ? 0 : 1)) * 4 + q4] =
-                rows;
+            p.bad[(bad_tile * 2 + (dv_side ? 0 : 1)) * 4 + q4] = rows;
         }
         if (!WIN && ok && order == 0) {  // phase 1: every row parked, then the flag
           mbar_arrive(bar(L::B_SPL));
@@ -1208,10 +1248,13 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtens
   if (e != cudaSuccess) return e;
   const int nT = (p.N + kTile - 1) / kTile;
   const long long units =
-      static_cast<long long>(KIND == kWindow
-                                 ? (nT + p.sink_tiles * (p.sink_parts - 1)) * p.group_parts
-                                 : nT) *
-      p.B * (p.Hkv > 0 ? p.Hkv : p.H);
+      p.packed ? p.Hkv * (p.sink_tiles * packed_units(p.B, p.total, p.part_tiles * kTile) +
+                          packed_units(p.B, p.total, kTile))
+               : static_cast<long long>(KIND == kWindow
+                                            ? (nT + p.sink_tiles * (p.sink_parts - 1)) *
+                                                  p.group_parts
+                                            : nT) *
+                     p.B * (p.Hkv > 0 ? p.Hkv : p.H);
   // persistent: one CTA per SM (the CTA holds the SM's TMEM and most of its
   // shared memory), each walking units blockIdx.x, blockIdx.x + grid, ...
   const int sms = sm_count();

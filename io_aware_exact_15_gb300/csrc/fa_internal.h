@@ -143,10 +143,16 @@ struct BwdParams {
   // which leave fp32 2^15 dV, dK ([2][128][d] per slot) in `part` when a sequence
   // has more than one of them.  With group_parts > 1 every walk is cut by the
   // group's heads as well, and every unit has a slot.  Units are numbered
-  // u = v * B * Hkv + (b * Hkv + head), slot_units of them by head have slots.  bad: [B * Hkv][key tiles][dV, dK][4], a bit
+  // u = v * B * Hkv + (b * Hkv + head), slot_units of them by head have slots.
+  // packed (sequences of one slice, group_parts 1): few of these units may
+  // exist, so they are handed out, and slots and bad are numbered, by where
+  // their sequences begin, as in packed_units: parts by L = 128 part_tiles rows,
+  // slots 2 (cu[b] / L) + part of slot_units for each (head, first tile).
+  // bad: [B * Hkv][key tiles] (packed: [Hkv][packed_units]) [dV, dK][4], a bit
   // per row of a tile that came out with a NaN or an infinity.
   int window = 0, sinks = 0;
   int sink_tiles = 0, sink_parts = 0, part_tiles = 0, group_parts = 1, slot_units = 0;
+  int packed = 0;
   uint32_t* bad = nullptr;
   int* err = nullptr;
   uint64_t wait_ns = 0;

@@ -243,6 +243,17 @@ FA_DEV PackedTile packed_tile(const int* cu, int B, int total, int v, int rows, 
   return PackedTile{lo, t >= 0 && t < units ? units - 1 - t : -1};
 }
 
+// The same search by one thread: the last sequence whose number min(cu, total) /
+// rows + b * step is not above v.
+FA_DEV int packed_find(const int* cu, int B, int total, int v, int rows, int step) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    (min(max(cu[mid], 0), total) / rows + mid * step <= v ? lo : hi) = mid;
+  }
+  return lo;
+}
+
 // Query tiles behind the last one that sees a key of tile kt (window >= 1).
 FA_DEV int window_end(int kt, int nT, int window) {
   return min(nT, (kt * kTile + kTile - 1 + window - 1) / kTile + 1);

@@ -21,6 +21,7 @@
 #include "../../include/fa.h"
 #include "fa_host.h"
 #include "fa_internal.h"
+#include "fa_sched.cuh"
 #include "fa_window.cuh"
 
 namespace fa {
@@ -65,8 +66,19 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
     const int t = (blockIdx.x * 8 + warp) * RPW;  // ((bkv, tile), dV or dK, first row)
     const int r = (t & (kTile - 1)) + lane / LPR, side = (t >> 7) & 1, unit = t >> 8;
     const int tiles = p.group_parts > 1 ? ntmax : p.sink_tiles;
-    if (unit >= p.B * p.Hkv * tiles) return;
-    const int bkv = unit / tiles, kt = unit - bkv * tiles;
+    // packed: a sequence with parts is longer than L = 128 part_tiles rows, so
+    // it has a multiple of L among them, and is looked for at its first
+    const int L = p.part_tiles * kTile, marks = p.packed ? p.total / L + 1 : 1;
+    if (unit >= (p.packed ? p.Hkv * marks : p.B * p.Hkv) * tiles) return;
+    int bkv = unit / tiles;
+    const int kt = unit - bkv * tiles;
+    if (p.packed) {
+      const int head = bkv / marks, mark = (bkv - head * marks) * L;
+      const int b = packed_find(p.cu_seqlens, p.B, p.total, mark, 1, 0);
+      const int a = min(max(p.cu_seqlens[b], 0), p.total);
+      if (a > mark || a <= mark - L) return;
+      bkv = b * p.Hkv + head;
+    }
     const Seq s = sequence(p, bkv / p.Hkv);
     const int nT = (s.n + kTile - 1) / kTile, j = kt * kTile + r;
     // no such rows, or written whole
@@ -74,11 +86,12 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
     const bool sunk = kt < p.sink_tiles;
     const int parts =
         (sunk ? (nT - kt + p.part_tiles - 1) / p.part_tiles : 1) * p.group_parts;
-    const int slot = (sunk ? kt * p.sink_parts : p.sink_tiles * (p.sink_parts - 1) + kt) *
-                     p.group_parts;
-    const float* src =
-        p.part + (((static_cast<size_t>(bkv) * p.slot_units + slot) * 2 + side) * kTile + r) * D +
-        8 * (lane % LPR);
+    const size_t slot =
+        p.packed ? static_cast<size_t>(bkv % p.Hkv * tiles + kt) * p.slot_units + 2 * (s.row0 / L)
+                 : static_cast<size_t>(bkv) * p.slot_units +
+                       (sunk ? kt * p.sink_parts : p.sink_tiles * (p.sink_parts - 1) + kt) *
+                           p.group_parts;
+    const float* src = p.part + ((slot * 2 + side) * kTile + r) * D + 8 * (lane % LPR);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
@@ -108,19 +121,27 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
   }
   if (static_cast<int>(blockIdx.x) < nsum + nbad) {
     // ------------------------------------------------ rows that caught something
-    const long long total = 8LL * p.B * p.Hkv * ntmax;
+    const int per = p.packed ? p.total / kTile + p.B : p.B * ntmax;  // tiles of a head
+    const long long total = 8LL * p.Hkv * per;
     const long long t = (static_cast<long long>(blockIdx.x - nsum) * 8 + warp) * 32 + lane;
     uint32_t word = 0;
     int bkv = 0, kt = 0;
     Seq s = {0, 0};
     if (t < total) {
       const int unit = static_cast<int>(t >> 3);
-      bkv = unit / ntmax;
-      kt = unit - bkv * ntmax;
+      if (p.packed) {
+        const int head = unit / per, v = unit - head * per;
+        const int b = packed_find(p.cu_seqlens, p.B, p.total, v, kTile, 1);
+        bkv = b * p.Hkv + head;
+        kt = v - (min(max(p.cu_seqlens[b], 0), p.total) / kTile + b);
+      } else {
+        bkv = unit / ntmax;
+        kt = unit - bkv * ntmax;
+      }
       s = sequence(p, bkv / p.Hkv);
       const int nT = (s.n + kTile - 1) / kTile;
       // tiles that were written whole
-      if (p.group_parts == 1 && kt < nT && !(kt < p.sink_tiles && kt + p.part_tiles < nT))
+      if (p.group_parts == 1 && kt >= 0 && kt < nT && !(kt < p.sink_tiles && kt + p.part_tiles < nT))
         word = p.bad[t];
     }
     for (uint32_t some = __ballot_sync(0xffffffffu, word != 0); some; some &= some - 1) {
@@ -213,11 +234,14 @@ cudaError_t launch_finish(const WindowFinish& w, cudaStream_t stream) {
   const long long bkv = static_cast<long long>(p.B) * p.Hkv, nT = (p.N + kTile - 1) / kTile;
   const long long rows = p.cu_seqlens ? static_cast<long long>(p.H) * p.total
                                       : static_cast<long long>(p.B) * p.H * p.N;
-  const long long nsum = (p.group_parts > 1  ? bkv * nT
-                          : p.sink_parts > 1 ? bkv * p.sink_tiles
-                                             : 0) *
+  const long long marks = p.total / (p.part_tiles * kTile) + 1;
+  const long long nsum = (p.group_parts > 1    ? bkv * nT
+                          : p.sink_parts == 1  ? 0
+                          : p.packed           ? p.Hkv * marks * p.sink_tiles
+                                               : bkv * p.sink_tiles) *
                          (2 * kTile * (D / 8) / 256);
-  const long long nbad = (8 * bkv * nT + 255) / 256;
+  const long long tiles = p.packed ? p.Hkv * packed_units(p.B, p.total, kTile) : bkv * nT;
+  const long long nbad = (8 * tiles + 255) / 256;
   const long long want = (rows * (D / 8) + 256 * kUnroll - 1) / (256 * kUnroll);
   const long long most = 8LL * sm_count();
   if (most <= 0) return cudaErrorInvalidDevice;
@@ -241,24 +265,43 @@ namespace {
 // there are SMs: 1024 rows of 16 heads (4 of K and V), window 256, 114 -> 45 us.
 struct WalkSplit {
   int tiles, parts, part_tiles, group_parts;
-  long long slot_units(int nT) const {
-    return group_parts > 1 ? (nT + static_cast<long long>(tiles) * (parts - 1)) * group_parts
-           : parts > 1     ? static_cast<long long>(tiles) * parts
-                           : 0;
-  }
+  bool packed;           // units, slots and flags by where the sequences begin
+  int slot_units;        // slots of a head (packed: of its first tiles each)
+  long long slots;       // all of them
+  long long bad_tiles;   // tiles with flags
 };
-WalkSplit walk_split(int B, int H, int Hkv, int N, int window, int sinks) {
+// total: rows of a packed batch, else 0
+WalkSplit walk_split(int B, int H, int Hkv, int N, int total, int d, int window, int sinks) {
   constexpr int kSms = 152;  // (not the device's: workspaces are sized without one)
-  const int nT = (N + kTile - 1) / kTile;
-  const long long units = static_cast<long long>(B) * Hkv * nT;
+  const long long nT = (N + kTile - 1) / kTile, units = static_cast<long long>(B) * Hkv * nT;
+  const long long live = total > 0 ? Hkv * packed_units(B, total, kTile) : units;
   WalkSplit s;
   s.tiles = ((sinks < N ? sinks : N) + kTile - 1) / kTile;
-  const int walk = (window - 2 + kTile) / kTile + 1, least = units <= kSms ? 2 : 8;
+  const int walk = (window - 2 + kTile) / kTile + 1;
+  const int least = (live < units ? live : units) <= kSms ? 2 : 8;
   s.part_tiles = walk > least ? walk : least;
   s.parts = s.tiles ? (nT + s.part_tiles - 1) / s.part_tiles : 1;
   s.group_parts = 1;
   for (int g = 2; g <= H / Hkv && units * g <= kSms; ++g)
     if (H / Hkv % g == 0) s.group_parts = g;
+  // Packed batches: units by where their sequences begin if they would mostly be
+  // of tiles that do not exist, or if the walks of all sequences at once read
+  // more of Q and dO than L2 keeps.  Else tile by tile, all sequences together:
+  // the longest walks come first.  16 heads (4 of K and V), tile by tile | by
+  // begin, us: 64 sequences of up to 2027 rows of 128, window 512, 1437 | 1241;
+  // 16 of up to 4045, window 1024, 989 | 976; 64 of up to 509 rows of 64, window
+  // 256, 135 | 147; one of 14000 among 63 of up to 199 (8 heads, 2) 386 | 313.
+  const long long tiles_q = static_cast<long long>(B) * H * walk, all_q = H * (total / kTile + 1LL);
+  const long long near = (tiles_q < all_q ? tiles_q : all_q) * 4 * kTile * d;
+  s.packed = total > 0 && s.group_parts == 1 && (units > 3 * live || near > (96LL << 20));
+  const long long L = static_cast<long long>(s.part_tiles) * kTile;
+  const long long per = s.group_parts > 1 ? (nT + s.tiles * (s.parts - 1LL)) * s.group_parts
+                        : s.parts == 1    ? 0
+                        : s.packed        ? 2 * (total / L)
+                                          : static_cast<long long>(s.tiles) * s.parts;
+  s.slot_units = static_cast<int>(per);
+  s.slots = per * Hkv * (s.packed ? s.tiles : B);
+  s.bad_tiles = s.packed ? live : units;
   return s;
 }
 
@@ -269,10 +312,7 @@ struct WindowWorkspace {
   size_t bytes;
 };
 // rows: of all query slices
-WindowWorkspace window_ws(void* ws, size_t rows, int B, int Hkv, int N, int d,
-                          const WalkSplit& s) {
-  const size_t bkv = static_cast<size_t>(B) * Hkv, nT = (N + kTile - 1) / kTile;
-  const size_t part = bkv * s.slot_units(static_cast<int>(nT)) * 2 * kTile * d * sizeof(float);
+WindowWorkspace window_ws(void* ws, size_t rows, int d, const WalkSplit& s) {
   char* base = static_cast<char*>(ws);
   WindowWorkspace w;
   size_t at = 0;
@@ -283,8 +323,8 @@ WindowWorkspace window_ws(void* ws, size_t rows, int B, int Hkv, int N, int d,
   };
   w.delta = reinterpret_cast<float*>(take(rows * sizeof(float)));
   w.dq_acc = reinterpret_cast<float*>(take(rows * d * sizeof(float)));
-  w.part = reinterpret_cast<float*>(take(part));
-  w.bad = reinterpret_cast<uint32_t*>(take(bkv * nT * 8 * sizeof(uint32_t)));
+  w.part = reinterpret_cast<float*>(take(s.slots * 2 * kTile * d * sizeof(float)));
+  w.bad = reinterpret_cast<uint32_t*>(take(s.bad_tiles * 8 * sizeof(uint32_t)));
   w.unit_counter = reinterpret_cast<int*>(take(sizeof(int)));
   w.bytes = at;
   return w;
@@ -312,11 +352,16 @@ fa_status check_window(bool packed, int B, int H, int Hkv, int N, int total, int
     if (rows >= (1LL << 31) || rows * N >= (1LL << 31) || rows * N * d >= (1LL << 31))
       return FA_ERR_UNSUPPORTED;
   }
-  const WalkSplit s = walk_split(B, H, Hkv, N, window < N ? window : N, sinks);
   const long long bh = static_cast<long long>(B) * H, nT = (N + kTile - 1) / kTile;
-  const long long units = nT + static_cast<long long>(s.tiles) * s.parts;
+  if (bh >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  const WalkSplit s =
+      walk_split(B, H, Hkv, N, packed ? total : 0, d, window < N ? window : N, sinks);
+  const long long units = bh * (nT + static_cast<long long>(s.tiles) * s.parts);
   // units, and a row of the last kernel's 256 each, are counted in 32 bits
-  if (bh >= (1LL << 31) || bh * units >= (1LL << 23)) return FA_ERR_UNSUPPORTED;
+  const long long some = !s.packed ? units
+                                 : H * (packed_units(B, total, kTile) +
+                                        s.tiles * packed_units(B, total, s.part_tiles * kTile));
+  if (some >= (1LL << 23) || units >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -373,8 +418,8 @@ size_t fa_backward_window_workspace_size(int B, int H, int Hkv, int N, int total
   using namespace fa;
   if (check_window(total > 0, B, H, Hkv, N, total, d, 1.f, window, sinks) != FA_OK) return 0;
   const size_t rows = total > 0 ? static_cast<size_t>(H) * total : static_cast<size_t>(B) * H * N;
-  return window_ws(nullptr, rows, B, Hkv, N, d,
-                   walk_split(B, H, Hkv, N, window < N ? window : N, sinks))
+  return window_ws(nullptr, rows, d,
+                   walk_split(B, H, Hkv, N, total, d, window < N ? window : N, sinks))
       .bytes;
 }
 
@@ -394,11 +439,11 @@ fa_status fa_backward_window(const void* q, const void* k, const void* v, const 
     FA_TRY(check_ptr16(x));
   FA_TRY(check_ptr4(lse));
   if (window > N) window = N;
-  const WalkSplit split = walk_split(B, H, Hkv, N, window, sinks);
+  const WalkSplit split = walk_split(B, H, Hkv, N, total, d, window, sinks);
   const int zq = cu_seqlens ? H : B * H, zkv = cu_seqlens ? Hkv : B * Hkv;
   const int rows = cu_seqlens ? total : N;
   const long long qrows = static_cast<long long>(zq) * rows;
-  const WindowWorkspace ws = window_ws(workspace, qrows, B, Hkv, N, d, split);
+  const WindowWorkspace ws = window_ws(workspace, qrows, d, split);
   FA_TRY(check_ws(workspace, workspace_bytes, ws.bytes));
   fa_status st = FA_OK;
   int* err = status_word(&st);
@@ -433,7 +478,8 @@ fa_status fa_backward_window(const void* q, const void* k, const void* v, const 
   p.sink_parts = split.parts;
   p.part_tiles = split.part_tiles;
   p.group_parts = split.group_parts;
-  p.slot_units = static_cast<int>(split.slot_units((N + kTile - 1) / kTile));
+  p.slot_units = split.slot_units;
+  p.packed = split.packed;
   p.bad = ws.bad;
   p.unit_counter = ws.unit_counter;
   p.err = err;

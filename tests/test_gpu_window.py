@@ -123,6 +123,15 @@ def test_many_packed_sequences(count, longest, lead, window):
         check(y, out, window, 2)
 
 
+@pytest.mark.parametrize("d,sinks,lead", [(64, 3, 0), (128, 200, 77)])
+def test_long_sequences_among_short_ones(d, sinks, lead):
+    """First tiles' walks in parts, at offsets all over the batch: a sequence
+    with parts beside ones without, and two on end."""
+    lens = [5, 0, 1400, 130] + [3] * 90 + [1025, 1300, 0, 1, 2100] + [7, 0, 60] * 9 + [1024, 1100]
+    x = R.Batch(lens, 2, 1, d, True, 21, lead, 300)
+    check(x, run(x, 60, sinks, device()), 60, sinks)
+
+
 def test_rows_of_no_sequence_are_left():
     """Rows in front of the first sequence and behind the last."""
     dev = device()

@@ -70,6 +70,15 @@ def test_window_refuses_workspaces():
     assert backward(B=3, N=4000, total=9000, d=128, cu=A, size=n - 1) == WS
 
 
+def test_a_packed_batch_takes_what_its_rows_take():
+    """1023 short sequences and one of 32768 rows: D and the accumulator (516
+    bytes a row), and not a slot for every part that a sequence might have."""
+    total = 1023 * 20 + 32768
+    n = fa.fa_backward_window_workspace_size(1024, 8, 8, 32768, total, 128, 512, 4)
+    assert 516 * 8 * total <= n < 2 * 516 * 8 * total
+    assert backward(B=1024, H=8, Hkv=8, N=32768, total=total, d=128, window=512, cu=A, size=n - 1) == WS
+
+
 def test_empty_packed_batch():
     """Nothing to do and nothing to point to."""
     assert forward(cu=A, total=0, N=0, ptrs=(None,) * 5) == fa.FA_OK
