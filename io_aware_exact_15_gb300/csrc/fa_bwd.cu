@@ -36,8 +36,8 @@
 // longer reach back to it; the tiles of the first keys that stay visible are
 // walked to the end of the sequence, in parts of about a window's length (one
 // such walk would outlast everything else), whose fp32 dV, dK the last kernel
-// adds up (fa_window.cu).  Units are handed out at run time: of 6 sequences
-// packed raggedly a third of the units lies behind some sequence's end.
+// adds up (fa_window.cu).  Units are handed out at run time, those of packed
+// sequences by where the sequences begin when most would not exist otherwise.
 // Measured with the kernels around it: 6 sequences of up to 4096 rows, 12
 // heads of 64, window 512, 16 first keys: 193 us; 2 x 16 heads (4 of K and V)
 // of 8192 rows of 128, window 1024, 4 first keys: 533 us, 607 TFLOP/s of
