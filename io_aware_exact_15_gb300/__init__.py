@@ -463,7 +463,9 @@ def _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen)
             raise ValueError("cu_seqlens: expected [B + 1]")
         _want("cu_seqlens", cu_seqlens, cu_seqlens.shape, (torch.int32,), q)
         B, H, Hkv, total, d, N = _varlen_shape(q, k, cu_seqlens, max_seqlen)
-        N = max(N, 1) if total else 0  # (every sequence may be empty)
+        if N < 0:
+            raise ValueError("max_seqlen: the longest length, or more")
+        N = min(max(N, 1), total)  # (every sequence may be empty, N more than all rows)
         lead, rows = (), total
     else:
         B, H, N, d = _shape(q)
@@ -485,7 +487,8 @@ def attention_forward(q, k, v, scale=None, causal=False, block_mask=None, worksp
     Philox keep rule of (seed, offset); the backward must get the same.
     window (with causal=True): each query sees the last `window` keys, itself
     included, and the first `sinks` keys of its sequence; the packed sequences
-    may then end before `total` (rows that belong to none are not written)."""
+    may then end before `total` (rows that belong to none are not written), and
+    max_seqlen may be more than the longest length."""
     import torch
     if window is not None:
         sizes = _window_args(q, k, v, causal, block_mask, dropout_p, cu_seqlens, max_seqlen)

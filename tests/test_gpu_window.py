@@ -132,6 +132,22 @@ def test_long_sequences_among_short_ones(d, sinks, lead):
     check(x, run(x, 60, sinks, device()), 60, sinks)
 
 
+def test_numbers_beyond_the_batch():
+    """A longest length and a window that are more than there is, past 32 bits
+    too; a longest length below zero."""
+    dev = device()
+    x = R.Batch([70, 0, 200], 2, 1, 64, True, 31, 0, 9)
+    q, k, v, g, cu = (t.to(dev) for t in (x.q, x.k, x.v, x.g, x.cu))
+    kw = dict(causal=True, sinks=2, cu_seqlens=cu)
+    for N, window in ((4096, 30), (2**40, 2**32 + 1)):
+        o, lse = fa.attention_forward(q, k, v, max_seqlen=N, window=window, **kw)
+        grads = fa.attention_backward(q, k, v, o, g, lse, max_seqlen=N, window=window, **kw)
+        status_ok()
+        check(x, (o, lse) + grads, min(window, 1000), 2)
+    with pytest.raises(ValueError):
+        fa.attention_forward(q, k, v, max_seqlen=-1, window=30, **kw)
+
+
 def test_rows_of_no_sequence_are_left():
     """Rows in front of the first sequence and behind the last."""
     dev = device()
