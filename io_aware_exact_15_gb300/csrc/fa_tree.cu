@@ -933,6 +933,7 @@ long long most_tiles(const TreeParams& p) {
 
 // CTAs: `per_sm` per SM, no more than there can be units (0 on error).
 int tree_grid(const TreeParams& p, int per_sm) {
+  if (p.cluster) return p.B * p.Hkv * p.cluster;
   const int sms = sm_count() * per_sm;
   const long long most = static_cast<long long>(p.B) * p.Hkv * p.groups * most_tiles(p);
   const int grid = sms < most_ctas(p.rows) ? sms : most_ctas(p.rows);
@@ -946,7 +947,16 @@ int tree_grid(const TreeParams& p, int per_sm) {
 // say so: us per tile, and what cutting costs beside it (4 where each CTA has
 // one tile at most, else 10, 24 with 256-row groups, whose parts are 128 KB).
 // With more than 128 rows, whole problems are 128-row groups if the SMs have
-// one each.  cut | whole, us, 4 key/value heads of 128 but for drafts:
+// one each.  A third way, for few rows and fewer problems than SMs: 2, 4 or 8
+// CTAs of a cluster share a problem and join its parts themselves behind a
+// cluster barrier (2 us), where a second kernel takes 4 at least.  (8 CTAs that
+// have an SM each leave SMs of a GPC idle: only for a quarter of the SMs.)
+// cut or whole, the better | shared, us, 1 token, 4 key/value heads:
+//   d = 128, bf16  x 1, window 512 13.2 | 10.4; x 8, 512 19.0 | 12.0, 4096 31.6 |
+//   21.0; x 16, 4096 38.0 | 29.4; e4m3 x 1, 512 10.5 | 8.4; x 16, 1024 14.3 | 11.2
+//   d = 64, bf16  x 1, 512 10.7 | 8.3; x 8, 4096 19.4 | 15.9; e4m3 x 8, 4096
+//   13.9 | 12.5; (4 rows a token: bf16, d = 128, x 8, 512 22.6 | 15.9)
+// cut | whole, us, 4 key/value heads of 128 but for drafts:
 //   1 token x 16 sequences, bf16, window 128 27.3 | 17.0, 1024 33.4 | 27.3
 //   1 token x 1, bf16, window 128 19.1 | 15.0, 512 19.1 | 21.1
 //   1 token x 64, e4m3, window 4096 70.3 | 66.2
@@ -967,6 +977,16 @@ void split_window(TreeParams* p, int format, int d) {
   const double per_cta = units / sms > 1 ? units / sms : 1;
   const double cut = per_cta * us * (p->pair ? 1.45 : 1.0) +
                      (units <= sms ? 4 : p->pair ? 24 : 10);
+  if (few && mt > 1) {
+    int n = 2;
+    const bool two = few_ctas(p->rows, format, d) == 2;
+    while (n < 8 && n < mt && bh * 2 * n <= (n < 4 || two ? sms : sms / 2)) n *= 2;
+    const double shared = ceil(mt / n) * us + 2;
+    if (bh * n <= sms && shared < cut && shared < mt * us) {
+      p->cluster = n;
+      return;
+    }
+  }
   const int groups = (p->rows + kTile - 1) / kTile;
   if (ceil(bh * groups / sms) * mt * us > cut || (p->pair && bh * groups > sms)) return;
   p->whole = 1;
@@ -976,7 +996,7 @@ void split_window(TreeParams* p, int format, int d) {
 
 cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t stream) {
   // tables of one tile: every problem is one unit, nothing to join
-  if (p.whole || most_tiles(p) == 1) return cudaSuccess;
+  if (p.whole || p.cluster || most_tiles(p) == 1) return cudaSuccess;
   const dim3 blocks((p.slot_rows + 7) / 8, grid);
   return d == 64 ? launch_pdl(fa_tree_join_kernel<64>, blocks, dim3(256), 0, stream, p)
                  : launch_pdl(fa_tree_join_kernel<128>, blocks, dim3(256), 0, stream, p);

@@ -33,6 +33,7 @@ struct TreeParams {
   int groups, slot_rows;   // row groups per key/value head; rows of a part
   int pair;                // 256-row groups
   int whole;               // (windows) CTAs take whole problems: nothing to join
+  int cluster;             // (windows, few rows) CTAs of a cluster share a problem and join it
   int num_pages, log_page, max_pages, words;
   int window, sinks;       // kernels with a window: at least 1, at least 0
   float scale;
@@ -126,6 +127,15 @@ FA_DEV Run find_run(const TreeParams& p, int c, int grid, int lane) {
           0xffffffffu, i + lane < p1 ? seq_len<WIN>(p, (i + lane) / per_b).tiles : 0);
     return r;
   }
+  if (WIN && p.cluster) {  // CTA c: its share of the tiles of problem c / cluster
+    const int problem = c / p.cluster, i = c - problem * p.cluster;
+    Run r = {problem / (p.Hkv * p.groups), 0, 0, 0, 0, 0, grid};
+    r.hr = problem - r.b * (p.Hkv * p.groups);
+    const int tiles = seq_len<WIN>(p, r.b).tiles;
+    r.t = tiles * i / p.cluster;
+    r.left = tiles * (i + 1) / p.cluster - r.t;
+    return r;
+  }
   const uint32_t mine = seq_units<WIN>(p, lane);  // the first 32 sequences
   uint32_t total = __reduce_add_sync(0xffffffffu, mine);
   for (int b0 = 32; b0 < p.B; b0 += 32)
@@ -204,6 +214,48 @@ FA_DEV void note_join(const TreeParams& p, const Run& r, const PartIter<WIN>& it
     j = make_int2(it.b * p.Hkv * p.groups + it.hr, c1 - c + 1);
   }
   p.joins[c] = j;
+}
+
+// Row `row` of problem bh from its n <= 8 parts, whose rows in part_ml and
+// part_o `at` says (fa_tree_join_kernel's sum).  Whole warp.  The parts are of
+// other SMs of the cluster: L1 may hold what stood there before.
+template <int D, class At>
+FA_DEV void join_row(const TreeParams& p, int bh, int row, int n, const At& at, int lane) {
+  constexpr int E = D / 32;
+  float v[8][E];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {  // all on their way together
+    const float* y = p.part_o + at(min(k, n - 1)) * D + lane * E;
+    if (E == 4)
+      *reinterpret_cast<float4*>(v[k]) = __ldcg(reinterpret_cast<const float4*>(y));
+    else
+      *reinterpret_cast<float2*>(v[k]) = __ldcg(reinterpret_cast<const float2*>(y));
+  }
+  const float2 x = lane < n ? __ldcg(p.part_ml + at(lane)) : make_float2(-INFINITY, 0.f);
+  float M = x.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  // a part in which the row saw nothing counts nothing, whatever it holds
+  const float a = x.y == 0.f ? 0.f : ex2(x.x - (M == -INFINITY ? 0.f : M));
+  const uint32_t use = __ballot_sync(0xffffffffu, x.y != 0.f);
+  float l = x.y * a, o[E];
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float ak = __shfl_sync(0xffffffffu, a, k);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = (use >> k) & 1u ? fmaf(v[k][e], ak, o[e]) : o[e];
+  }
+  const bool has = !(l == 0.f);
+  const float inv = has ? 1.f / l : 0.f;
+  const size_t gr = static_cast<size_t>(bh) * p.rows + row;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + gr * D + lane * E);
+#pragma unroll
+  for (int i = 0; i < E; i += 2) dst[i / 2] = has ? pack_bf16(o[i] * inv, o[i + 1] * inv) : 0u;
+  if (lane == 0) p.lse[gr] = has ? (M + lg2(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // The tiles of a run, in order.

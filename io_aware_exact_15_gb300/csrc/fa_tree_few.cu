@@ -46,7 +46,8 @@
 // sequences of 500 keys 47.7 (20.0).  Issue slots are 44 % busy, the
 // ALU 46 %; the rest is the chain of a chunk and the ends of problems.
 // With a window of 4096: 64 sequences x 1 token of up to 32768 e4m3 keys 55.1 us, 4.9
-// TB/s (40.0); 1 sequence x 1 token, window 512, bf16: 12.7 us, two launches.
+// TB/s (40.0); 1 sequence x 1 token, window 512, bf16: 10.4 us, one launch of
+// clusters whose CTAs share a problem (split_window in fa_tree.cu).
 #include <math.h>
 #include <stdint.h>
 
@@ -180,8 +181,17 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
   }
   __syncthreads();
   const Run run = *run_slot;
+  // WIN: the CTAs of a cluster each have a part of one problem; once all parts
+  // are written (every thread of the cluster comes here), the first one joins them
+  auto parts_written = [&]() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  };
   if (run.left == 0) {
-    if (threadIdx.x == 0) note_join(p, run, PartIter<WIN>(), blockIdx.x);
+    if (WIN && p.cluster)
+      parts_written();
+    else if (threadIdx.x == 0)
+      note_join(p, run, PartIter<WIN>(), blockIdx.x);
     return;
   }
   const WaitCtl wc{abort_flag, p.err, p.wait_ns};
@@ -242,6 +252,7 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
     // let copies still in flight land before the CTA can exit
     for (uint32_t j = n > L::R ? n - L::R : 0; j < n; ++j)
       drain_bar(full(j % L::R), (j / L::R) & 1, p.wait_ns);
+    if (WIN && p.cluster) parts_written();
     return;
   }
 
@@ -622,6 +633,23 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
             whole ? nullptr : p.part_o + (prow0 + row) * D);
     }
   }
+  if (WIN && p.cluster) {
+    const int tiles = it.s.tiles;
+    parts_written();
+    if (it.t0 > 0 || it.t1 == tiles) return;  // not the first part, or all there is
+    // the k-th part is CTA k's, or with fewer tiles than CTAs that of the k-th one with a tile
+    const int n = min(tiles, p.cluster);
+    const size_t c0 = blockIdx.x - blockIdx.x % p.cluster;
+#pragma unroll 1
+    for (int row = w; row < p.rows; row += L::NC) {
+      auto at = [&](int k) {
+        const int i = n == p.cluster ? k : ((k + 1) * p.cluster + tiles - 1) / tiles - 1;
+        return (2 * (c0 + i) + (k == 0 ? 1 : 0)) * p.slot_rows + row;
+      };
+      join_row<D>(p, it.b * p.Hkv + it.hr, row, n, at, lane);
+    }
+    return;
+  }
   if (tid == 0) note_join(p, run, it, blockIdx.x);
 }
 
@@ -633,6 +661,22 @@ cudaError_t launch_few_win(const TreeParams& p, const CUtensorMap& tk,
   const cudaError_t e = smem_attr_once(
       attr_done, reinterpret_cast<const void*>(fa_tree_few_kernel<D, FMT, RT, WIN>), L::ALLOC);
   if (e != cudaSuccess) return e;
+  if (WIN && p.cluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = L::ALLOC;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fa_tree_few_kernel<D, FMT, RT, WIN>, tk, tv, p);
+  }
   return launch_pdl(fa_tree_few_kernel<D, FMT, RT, WIN>, dim3(grid), dim3(L::THREADS), L::ALLOC,
                     stream, tk, tv, p);
 }

@@ -106,6 +106,12 @@ CASES = [
     (2, 4, 2, 300, 64, 64, [1000, 0], [300, 150], None, 90, 7),  # a prompt in chunks
     (33, 4, 2, 1, 64, 16, [37 * i for i in range(33)], None, None, 200, 20),
     (1, 2, 1, 6, 128, 64, [500], None, None, 4, 1024),           # all of it first tokens
+    # long windows and few problems: several CTAs on each, also on those of a tile or none
+    (1, 4, 1, 1, 128, 64, [2900], None, None, 2500, 4),
+    (5, 4, 2, 1, 64, 32, [1500, 0, 129, 640, 2600], [1, 0, 1, 1, 1], None, 1400, 70),
+    (9, 8, 4, 1, 128, 16, [1000, 3, 999, 0, 300, 128, 127, 1300, 700], None, None, 1024, 0),
+    (18, 4, 4, 1, 64, 64, [97 * i for i in range(18)], None, None, 600, 16),
+    (2, 4, 1, 4, 128, 128, [1900, 60], None, "tree", 1100, 200),
 ]
 
 
