@@ -513,6 +513,15 @@ __global__ void __launch_bounds__(FewSmem<D, FMT, RT>::THREADS, FewSmem<D, FMT, 
           if (tail && it.s.nobody(pos + row))
 #pragma unroll
             for (int i = 0; i < WV; ++i) v[x][i] = 0;
+          // Not every draft sees it: no e4m3 number that is a NaN, which a weight
+          // of zero would not stop.  (A row that is NaN has a scale that says
+          // so, and those that see it get theirs from that.)
+          if (WIN && FMT == kCacheE4m3 && tail && !it.s.everybody(pos + row))
+#pragma unroll
+            for (int i = 0; i < WV; ++i) {
+              const uint32_t n = ((v[x][i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              v[x][i] &= ~((n >> 7) * 0xFFu);
+            }
         }
 #pragma unroll
         for (int i = 0; i < WV; ++i) {

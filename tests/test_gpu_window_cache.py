@@ -112,6 +112,7 @@ CASES = [
     (9, 8, 4, 1, 128, 16, [1000, 3, 999, 0, 300, 128, 127, 1300, 700], None, None, 1024, 0),
     (18, 4, 4, 1, 64, 64, [97 * i for i in range(18)], None, None, 600, 16),
     (2, 4, 1, 4, 128, 128, [1900, 60], None, "tree", 1100, 200),
+    (3, 2, 2, 12, 64, 32, [0, 1111, 800], [12, 1, 7], "any", 500, 3),
 ]
 
 
