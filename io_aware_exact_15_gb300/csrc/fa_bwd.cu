@@ -693,6 +693,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ++ku;
       }
       if (ku > 0) drain_bar(bar(L::B_FIN), (ku - 1) & 1, p.wait_ns);
+      // the releases of the last two units' K and V, which nobody waited for:
+      // they must not arrive in the next CTA's shared memory
+      if (L::KVB == 2)
+        for (uint32_t j = ku > 2 ? ku - 2 : 0; j < ku; ++j)
+          drain_bar(bar(L::B_KVE + j % L::KVB), (j / L::KVB) & 1, p.wait_ns);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------ P, dS, dQ warps
