@@ -549,7 +549,8 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
           WIN ? ld_shared_u32(origin) : static_cast<size_t>(zq) * slice_rows + row0;
       uint8_t* obase = static_cast<uint8_t*>(p.o) + (first + qrow0) * static_cast<size_t>(D) * 2;
       const bool store = qrow < N;
-      const bool has = cnt > 0 && l > 0.f;
+      // (WIN: a NaN sum stays one, in lse and O; l = 0 says that nothing was seen)
+      const bool has = cnt > 0 && (WIN ? !(l == 0.f) : l > 0.f);
       // inverted dropout scales the kept weights by 1 / (1 - p')
       const float inv = has ? (DROP ? p.drop.scale : 1.f) / l : 0.f;
       // Each thread packs 64 columns of its O row (128 bytes) into this
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
         p.lse[first + qrow] =
             has ? (m + lg2(l)) * kLn2 : -INFINITY;
       if (WIN) {
-        // (a NaN logsumexp: the row sees a key whose score is one)
+        // (a NaN logsumexp: the row sees a key whose score is one, or +infinity)
         const float lse2 = m + lg2(l);
         uint32_t again = __ballot_sync(0xffffffffu, store && has && odd != 0.f && lse2 == lse2);
         for (; again; again &= again - 1) {  // the rows were written by all lanes
