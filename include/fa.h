@@ -211,7 +211,7 @@ fa_status fa_backward_varlen(const void* q, const void* k, const void* v, const 
  * it sees (dk, dv: that see it) alone: a NaN or an infinity anywhere else does
  * not reach it.  A row with a score that is NaN or +infinity has NaN in lse and
  * o, and what its gradients add to is NaN; one whose scores are all -infinity
- * has lse -infinity and o 0.  window >= 1, 0 <= sinks <= 1024 (more: FA_ERR_UNSUPPORTED);
+ * has lse -infinity, o 0 and no part in the gradients.  window >= 1, 0 <= sinks <= 1024 (more: FA_ERR_UNSUPPORTED);
  * B * H times the 128-row tiles of N (with those of the sinks, counted once
  * per 8 tiles or window) below 2^23, packed with total / 128 + B in place of
  * B times the tiles where that is less than a third.  Other rules as

@@ -601,8 +601,8 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
             has ? (m + lg2(l)) * kLn2 : -INFINITY;
       if (WIN) {
         // (a NaN logsumexp: the row sees a key whose score is one, or +infinity)
-        const float lse2 = m + lg2(l);
-        uint32_t again = __ballot_sync(0xffffffffu, store && has && odd != 0.f && lse2 == lse2);
+        const float lse2 = has ? m + lg2(l) : -INFINITY;
+        uint32_t again = __ballot_sync(0xffffffffu, store && odd != 0.f && lse2 == lse2);
         for (; again; again &= again - 1) {  // the rows were written by all lanes
           const int j = __ffs(again) - 1;
           __syncwarp();

@@ -10,7 +10,9 @@
 // they are written, and the columns of a row that hold a NaN or an infinity are
 // formed again here from the keys (or queries) that belong to it and nothing
 // else.  Where such a number does belong to the row, that ends as soon as all of
-// these columns have one again, since no sum brings them back.
+// these columns have one again, since no sum brings them back.  A query with
+// the logsumexp -infinity (all its scores are) has no weights: its sums are
+// empty, whatever numbers its keys have.
 #pragma once
 
 #include <stdint.h>
@@ -112,7 +114,8 @@ static __device__ __noinline__ void window_row_o(const void* q, const void* k, c
   Mend<D> m;
   qi.load(q, q0 + i, lane);
   m.begin(o, q0 + i, lane);
-  const int lo = max(i - window + 1, 0), first = min(sinks, lo), total = first + i + 1 - lo;
+  const int lo = max(i - window + 1, 0), first = min(sinks, lo);
+  const int total = lse2 == -INFINITY ? 0 : first + i + 1 - lo;
 #pragma unroll 1
   for (int n = 0; n < total && !m.done(); n += kRowBatch) {
     RowPiece<D> kj[kRowBatch], vj[kRowBatch];
@@ -145,7 +148,8 @@ static __device__ __noinline__ void window_row_dq(const WindowFinish& w, size_t 
   qi.load(w.q, q0 + i, lane);
   gi.load(w.dO, q0 + i, lane);
   m.begin(w.dq, q0 + i, lane);
-  const int lo = max(i - w.b.window + 1, 0), first = min(w.b.sinks, lo), total = first + i + 1 - lo;
+  const int lo = max(i - w.b.window + 1, 0), first = min(w.b.sinks, lo);
+  const int total = lse2 == -INFINITY ? 0 : first + i + 1 - lo;
 #pragma unroll 1
   for (int n = 0; n < total && !m.done(); n += kRowBatch) {
     RowPiece<D> kj[kRowBatch], vj[kRowBatch];
@@ -208,7 +212,7 @@ static __device__ __noinline__ void window_row_dkv(const WindowFinish& w, bool d
       if (!dv) sum_lanes(t);
 #pragma unroll
       for (int u = 0; u < kRowBatch; ++u) {
-        if (i + u >= end) continue;
+        if (i + u >= end || l[u] == -INFINITY) continue;
         const float pij = ex2(fmaf(s[u], sl2, -l[u] * 1.4426950408889634f));
         if (dv)
           m.acc.add(pij, gi[u]);

@@ -95,3 +95,44 @@ def test_an_infinite_score(which, d):
         assert bool(torch.isnan(got_l[up]).all()) and bool(torch.isnan(got_o[up]).all())
         assert bool(torch.isfinite(got_o[~up]).all())
         assert bool(((got_l - want).abs() <= tol + 2.0 ** -20 * want.abs())[~up].all())
+
+
+@pytest.mark.parametrize("case", [
+    # lengths, H, Hkv, d, window, sinks, packed, the row
+    ([420, 260], 2, 1, 64, 60, 3, True, 400),
+    ([420, 260], 4, 2, 128, 500, 0, True, 419),
+    ([300], 4, 1, 128, 300, 0, False, 17),
+    ([300], 4, 1, 64, 1, 0, False, 299),
+    ([1281], 2, 2, 64, 200, 4, False, 1100),
+])
+def test_a_row_whose_scores_are_all_minus_infinity(case):
+    """It sees nothing: o 0, lse -infinity, dq 0, and no share in dk, dv.  The
+    next sequence (all NaN) shares its last tile and shows nowhere."""
+    lens, H, Hkv, d, window, sinks, packed, row = case
+    x = R.Batch(lens, H, Hkv, d, packed, 53)
+    at = (slice(None), row) if packed else (slice(None), slice(None), row)
+    x.k[..., 5] = 1.0
+    x.g[at] = 0.0  # for the formula: a row without a gradient has no share either
+    n = lens[0]
+    q, k, v, g = (x.seq(t, 0) for t in (x.q, x.k, x.v, x.g))
+    ro, rl, to, tl = R.forward(q, k, v, window, sinks, d ** -0.5)
+    x.q[at + (5,)] = -INF
+    x.g[at] = 1.0
+    for t in (x.q, x.k, x.v, x.g):
+        if packed:
+            t[:, n:] = NAN
+    out = run(x, window, sinks, device())
+    o, lse = x.seq(out[0], 0), x.seq(out[1][..., None], 0)[..., 0]
+    assert bool(torch.isneginf(lse[:, row]).all()) and bool((o[:, row] == 0).all())
+    rest = torch.arange(n) != row
+    assert bool(((o - ro).abs() <= to)[:, rest].all())
+    assert bool(((lse - rl).abs() <= tl)[:, rest].all())
+    o[:, row], lse[:, row] = ro[:, row], rl[:, row]
+    ref, tol = R.backward(q, k, v, o, lse, g, window, sinks, d ** -0.5)
+    for name, a, r, t in zip(("dq", "dk", "dv"), out[2:], ref, tol):
+        a = x.seq(a, 0)
+        assert bool(torch.isfinite(a).all()), name
+        if name == "dq":
+            assert bool((a[:, row] == 0).all())
+            a, r, t = a[:, rest], r[:, rest], t[:, rest]
+        assert bool(((a - r).abs() <= t).all()), name
