@@ -43,7 +43,7 @@
 // With a window (WIN, fa_tree_attention_window) units are the tiles that some
 // draft sees something of; a problem has few of them (window / 128 and two or
 // three), so its ends weigh more, and whole problems go to the CTAs where
-// there are enough of them (split_window).  8 x 23 drafts of 12 heads of 64,
+// there are enough of them (split_window, fa_tree_host.h).  8 x 23 drafts of 12 heads of 64,
 // window 2048, 64 first positions, bf16: 24.9 us (the bytes: 7.8); 16 x 64
 // drafts of 16 + 4 heads of 128, window 1024, int8: 32.4 us (3.9): the
 // launch, the search for the run, and one problem's chain of tiles.
@@ -909,8 +909,6 @@ int slot_rows(int rows) {
   return rows < most ? rows : most;
 }
 
-int most_ctas(int rows) { return rows <= 8 ? 2 * kMaxGrid : kMaxGrid; }
-
 constexpr size_t kJoinBytes = 2 * kMaxGrid * sizeof(int2);  // a multiple of 256
 size_t tree_ml_bytes(int rows) {
   return align256(2ull * most_ctas(rows) * slot_rows(rows) * sizeof(float2));
@@ -919,79 +917,6 @@ size_t tree_ws_bytes(int H, int Hkv, int T, int d) {
   const int rows = H / Hkv * T;
   return kJoinBytes + tree_ml_bytes(rows) +
          align256(2ull * most_ctas(rows) * slot_rows(rows) * d * sizeof(float));
-}
-
-// Tiles of the longest sequence that the page table can hold (with a window:
-// the sinks', and those that window + T - 1 positions can touch).
-long long most_tiles(const TreeParams& p) {
-  const long long all = ((static_cast<long long>(p.max_pages) << p.log_page) + kTile - 1) / kTile;
-  if (!p.window) return all;
-  const long long near = (static_cast<long long>(p.window) + p.T + kTile - 3) / kTile + 1 +
-                         (p.sinks + kTile - 1) / kTile;
-  return near < all ? near : all;
-}
-
-// CTAs: `per_sm` per SM, no more than there can be units (0 on error).
-int tree_grid(const TreeParams& p, int per_sm) {
-  if (p.cluster) return p.B * p.Hkv * p.cluster;
-  const int sms = sm_count() * per_sm;
-  const long long most = static_cast<long long>(p.B) * p.Hkv * p.groups * most_tiles(p);
-  const int grid = sms < most_ctas(p.rows) ? sms : most_ctas(p.rows);
-  return most < grid ? static_cast<int>(most) : grid;
-}
-
-// Windows make problems of about the same length, known to the host, so CTAs
-// can take whole ones: no parts to store, no second kernel, and no CTA reads
-// the lengths of others' sequences.  That leaves SMs idle when there are fewer
-// problems than SMs, or a last round of them.  It is done where the estimates
-// say so: us per tile, and what cutting costs beside it (4 where each CTA has
-// one tile at most, else 10, 24 with 256-row groups, whose parts are 128 KB).
-// With more than 128 rows, whole problems are 128-row groups if the SMs have
-// one each.  A third way, for few rows and fewer problems than SMs: 2, 4 or 8
-// CTAs of a cluster share a problem and join its parts themselves behind a
-// cluster barrier (2 us), where a second kernel takes 4 at least.  (8 CTAs that
-// have an SM each leave SMs of a GPC idle: only for a quarter of the SMs.)
-// cut or whole, the better | shared, us, 1 token, 4 key/value heads:
-//   d = 128, bf16  x 1, window 512 13.2 | 10.4; x 8, 512 19.0 | 12.0, 4096 31.6 |
-//   21.0; x 16, 4096 38.0 | 29.4; e4m3 x 1, 512 10.5 | 8.4; x 16, 1024 14.3 | 11.2
-//   d = 64, bf16  x 1, 512 10.7 | 8.3; x 8, 4096 19.4 | 15.9; e4m3 x 8, 4096
-//   13.9 | 12.5; (4 rows a token: bf16, d = 128, x 8, 512 22.6 | 15.9)
-// cut | whole, us, 4 key/value heads of 128 but for drafts:
-//   1 token x 16 sequences, bf16, window 128 27.3 | 17.0, 1024 33.4 | 27.3
-//   1 token x 1, bf16, window 128 19.1 | 15.0, 512 19.1 | 21.1
-//   1 token x 64, e4m3, window 4096 70.3 | 66.2
-//   23 drafts, 12 heads of 64, x 8, window 1024 31.4 | 23.2, x 16 45.7 | 39.6
-//   92 rows, bf16, x 32, window 1024 49.8 | 35.5; e4m3 55.9 | 37.5
-//   256 rows, bf16, x 16, window 1024 51.8 | 33.4, x 4, 4096 45.7 | 51.8
-//   256 rows, int8, x 16, window 1024 53.9 | 37.5, 4096 82.6 | 86.7
-void split_window(TreeParams* p, int format, int d) {
-  const bool few = tree_few_rows(p->rows, format);
-  const int sms = sm_count() * (few ? few_ctas(p->rows, format, d) : 1);
-  if (sms <= 0) return;
-  const double us = few                    ? 0.9
-                    : format != kCacheBf16 ? (d == 64 ? 1.1 : 2.0)
-                                           : (d == 64 ? 0.7 : 1.2);
-  const double mt = static_cast<double>(most_tiles(*p));
-  const double bh = static_cast<double>(p->B) * p->Hkv;
-  const double units = bh * p->groups * mt;  // if cut
-  const double per_cta = units / sms > 1 ? units / sms : 1;
-  const double cut = per_cta * us * (p->pair ? 1.45 : 1.0) +
-                     (units <= sms ? 4 : p->pair ? 24 : 10);
-  if (few && mt > 1) {
-    int n = 2;
-    const bool two = few_ctas(p->rows, format, d) == 2;
-    while (n < 8 && n < mt && bh * 2 * n <= (n < 4 || two ? sms : sms / 2)) n *= 2;
-    const double shared = ceil(mt / n) * us + 2;
-    if (bh * n <= sms && shared < cut && shared < mt * us) {
-      p->cluster = n;
-      return;
-    }
-  }
-  const int groups = (p->rows + kTile - 1) / kTile;
-  if (ceil(bh * groups / sms) * mt * us > cut || (p->pair && bh * groups > sms)) return;
-  p->whole = 1;
-  p->pair = 0;
-  p->groups = groups;
 }
 
 cudaError_t launch_join(const TreeParams& p, int d, int grid, cudaStream_t stream) {
@@ -1010,7 +935,7 @@ cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap& tq, const C
   cudaError_t e = smem_attr_once(
       attr_done, reinterpret_cast<const void*>(fa_tree_kernel<D, FMT, PAIR, WIN>), L::ALLOC);
   if (e != cudaSuccess) return e;
-  const int grid = tree_grid(p, 1);
+  const int grid = tree_grid(p, sm_count());
   if (grid <= 0) return cudaErrorInvalidDevice;
   e = launch_pdl(fa_tree_kernel<D, FMT, PAIR, WIN>, dim3(grid), dim3(L::THREADS), L::ALLOC, stream,
                  tq, tk, tv, p);
@@ -1092,7 +1017,7 @@ fa_status tree_attention(const void* q, const void* k_cache, const void* v_cache
   p.window = window;
   p.sinks = sinks;
   p.scale = scale;
-  if (window) split_window(&p, format, d);
+  if (window) split_window(&p, format, d, sm_count());
   // units (TreeParams, find_run) are counted in 32 bits
   if (static_cast<long long>(B) * Hkv * p.groups > ((1LL << 31) - 1) / most_tiles(p))
     return FA_ERR_UNSUPPORTED;
@@ -1105,7 +1030,7 @@ fa_status tree_attention(const void* q, const void* k_cache, const void* v_cache
     if (!make_cache_map(&tk, k_cache, num_pages * Hkv, page_size, d, format != kCacheBf16) ||
         !make_cache_map(&tv, v_cache, num_pages * Hkv, page_size, d, format != kCacheBf16))
       return FA_ERR_CUDA;
-    const int grid = tree_grid(p, few_ctas(p.rows, format, d));
+    const int grid = tree_grid(p, sm_count() * few_ctas(p.rows, format, d));
     if (grid <= 0) return FA_ERR_CUDA;
     FA_CUDA(launch_tree_few(p, format, d, tk, tv, grid, stream));
     FA_CUDA(launch_join(p, d, grid, stream));

@@ -1,5 +1,4 @@
-// What the tree attention kernels share: the arguments, the lengths of the
-// sequences, the split of the work into runs, and which keys a draft sees.
+// What the tree attention kernels share: the lengths of the sequences, the split of the work into runs, and which keys a draft sees.
 #pragma once
 
 #include <math.h>
@@ -7,39 +6,9 @@
 
 #include "fa_internal.h"
 #include "fa_quant.cuh"
+#include "fa_tree_host.h"
 
 namespace fa {
-
-// CTAs, at most (the workspace holds two parts of each); up to 8 rows twice
-// as many
-constexpr int kMaxGrid = 192;
-
-struct TreeParams {
-  const void* q;           // bf16 [B, H, T, d]
-  const void *kc, *vc;     // caches [num_pages, Hkv, page, d]
-  const uint8_t *ks, *vs;  // scale bytes [num_pages, Hkv, page]
-  const int *page_table, *hist, *drafts;
-  const uint32_t* mask;    // [B, T, words] or null
-  void* o;                 // bf16 [B, H, T, d]
-  float* lse;              // [B, H, T]
-  // Parts of problems that several CTAs work on.  CTA c has two places: 2 c
-  // for the part that begins its run inside a problem, 2 c + 1 for the one
-  // that ends it inside a problem begun there.
-  float2* part_ml;         // [2 * grid][slot_rows] (max in log2 units, sum)
-  float* part_o;           // [2 * grid][slot_rows][d]
-  int2* joins;             // [grid] the problem begun and not ended by CTA c
-                           // ((b * Hkv + head) * groups + group) and its parts, or 0 parts
-  int B, Hkv, T, rows;     // rows = H / Hkv * T
-  int groups, slot_rows;   // row groups per key/value head; rows of a part
-  int pair;                // 256-row groups
-  int whole;               // (windows) CTAs take whole problems: nothing to join
-  int cluster;             // (windows, few rows) CTAs of a cluster share a problem and join it
-  int num_pages, log_page, max_pages, words;
-  int window, sinks;       // kernels with a window: at least 1, at least 0
-  float scale;
-  int* err;
-  uint64_t wait_ns;
-};
 
 // Lengths of a sequence, clamped to what the page table can hold.
 //
@@ -382,37 +351,7 @@ static __device__ __noinline__ void add_not_finite(const TreeParams& p, int b, i
   }
 }
 
-// Few query rows per key/value head: fa_tree_few.cu (warp MMAs) up to 16 rows
-// for bf16 and up to 24 for 8 bits, else fa_tree.cu.  The rule sees sizes,
-// not the lengths of the histories, which are on the device.  us by
-// fa_tree_few.cu | fa_tree.cu, 4 key/value heads, sequences x keys:
-//   d = 128           16 x 8192      256 x 500      1024 x 120     1 x 512
-//   bf16   9 rows   53.8 | 54.4    79.8 | 83.4    191 | 226    11.0 | 12.9
-//         12        54.7 | 54.5    86.5 | 80.1    218 | 227    11.3 | 12.7
-//         16        55.1 | 55.0    89.1 | 101     221 | 227    11.5 | 12.7
-//   e4m3  16        47.1 | 68.0    89.6 | 139     226 | 248    12.2 | 12.1
-//         24        59.2 | 68.6     115 | 140     301 | 254    13.8 | 12.4
-//   int8  16        51.0 | 69.5    94.4 | 142     231 | 251    12.3 | 12.1
-//         24        63.6 | 70.2     120 | 142     309 | 256    14.0 | 12.4
-//   d = 64
-//   bf16  16        33.5 | 37.5    59.7 | 92.5    141 | 176     9.2 | 10.7
-//   e4m3  24        43.5 | 54.1    80.0 | 114     205 | 220    11.3 | 10.7
-//   int8  24        45.6 | 55.9    82.6 | 116     207 | 219    11.4 | 10.7
-// At the rule's edge the two are equal for long histories of bf16, d = 128,
-// and 17 to 24 rows of 8 bits gain on long histories and lose on short ones
-// (a tile each, or one sequence alone).  Beyond it (16 x 8192 keys): bf16, d = 128, 24 rows 73.2 |
-// 56.8; e4m3 32 rows 149 | 69.6; int8 157 | 71.0; d = 64 bf16 24 rows 50.8 |
-// 40.0; e4m3 32 rows 55.6 | 55.6.
 // tk, tv: maps of whole pages (make_cache_map).
-inline bool tree_few_rows(int rows, int format) { return rows <= (format == kCacheBf16 ? 16 : 24); }
-// CTAs of it on an SM: two up to 8 rows, but for bf16 of d = 128, whose ring
-// takes the whole shared memory.  Two (8 warps each) | one (16 warps), e4m3,
-// 4 rows of 4 heads of 128, us: 4096 sequences of 60 keys 288 | 453, 256 of
-// 500 keys 47.7 | 55.4, 32 of up to 8192 keys 40.8 | 41.1, of 8191 keys each
-// 54.0 | 53.3.
-constexpr int few_ctas(int rows, int format, int d) {
-  return rows <= 8 && (format != kCacheBf16 || d == 64) ? 2 : 1;
-}
 // (with p.window: the kernels with a window)
 cudaError_t launch_tree_few(const TreeParams& p, int format, int d, const CUtensorMap& tk,
                             const CUtensorMap& tv, int grid, cudaStream_t stream);

@@ -1,5 +1,5 @@
 // Tree attention for few query rows per key/value head (a decode step, a
-// small tree): R = G T up to 16 rows, 24 for 8-bit caches (fa_tree.cuh has the
+// small tree): R = G T up to 16 rows, 24 for 8-bit caches (fa_tree_host.h has the
 // rule and both sides' times).
 //
 // With so few rows the work is reading the cache: per 128 keys a
@@ -47,7 +47,7 @@
 // ALU 46 %; the rest is the chain of a chunk and the ends of problems.
 // With a window of 4096: 64 sequences x 1 token of up to 32768 e4m3 keys 55.1 us, 4.9
 // TB/s (40.0); 1 sequence x 1 token, window 512, bf16: 10.4 us, one launch of
-// clusters whose CTAs share a problem (split_window in fa_tree.cu).
+// clusters whose CTAs share a problem (split_window in fa_tree_host.h).
 #include <math.h>
 #include <stdint.h>
 
