@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
         if (!ok) break;
         ++parts;
         if (lane == 0) {
-          const int r0 = (ti.it.hr - hkv * p.groups) * L::GROUP;
+          const int r0 = PAIR || WIN ? (ti.it.hr - hkv * p.groups) * L::GROUP : 0;
           const bool two = PAIR && r0 + kTile < p.rows;
           mbar_arrive_expect_tx(bar(L::B_QF + qb), (two ? 2 : 1) * L::TILE);
           for (int i = 0; i < (two ? 2 : 1); ++i)
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
           const int kb = ti.it.s.key_tile(ti.t) * kTile;
           int4* note = reinterpret_cast<int4*>(smem + L::NOTE + slot * 32);
           note[0] = make_int4(ti.it.s.len() - kb, ti.it.s.hist - kb, ti.part, 0);
-          if (WIN)
+          if constexpr (WIN)
             note[1] = make_int4(ti.it.s.sinks - kb, ti.it.s.lo - kb, ti.it.s.edge - kb, 0);
         }
         mbar_arrive_expect_tx(full, np * page * (L::Q8 ? D + 1 : 2 * D));
@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(TreeSmem<D, FMT, PAIR>::THREADS, 1)
     while (ok && it.next(p)) {
       ++part;
       const int hkv = it.hr / p.groups;
-      const int row0 = (it.hr - hkv * p.groups) * L::GROUP + (PAIR ? s * kTile : 0);
+      const int row0 = PAIR || WIN ? (it.hr - hkv * p.groups) * L::GROUP + (PAIR ? s * kTile : 0)
+                                   : 0;  // (only windows have several 128-row groups)
       const bool mine_all = row0 < p.rows;             // pair: this warpgroup has rows
       const bool busy = row0 + q4 * 32 < p.rows;       // this warp has rows
       const int row = row0 + r, t = row % p.T;

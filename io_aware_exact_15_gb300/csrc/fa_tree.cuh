@@ -23,19 +23,27 @@ namespace fa {
 template <bool WIN>
 struct SeqLen {
   int hist, nd, tiles;
+  FA_DEV int len() const { return hist + nd; }
+  FA_DEV int key_tile(int t) const { return t; }
+  FA_DEV bool nobody(int pos) const { return pos >= len(); }
+  FA_DEV bool everybody(int pos) const { return pos < hist; }
+  // whether n positions from pos on are not all everybody's, and are all nobody's
+  FA_DEV bool mixed(int pos, int n) const { return pos + n > hist; }
+  FA_DEV bool nothing(int pos, int) const { return pos >= len(); }
+};
+template <>
+struct SeqLen<true> {
+  int hist, nd, tiles;
   int sinks, lo, edge, sunk, skip;
   FA_DEV int len() const { return hist + nd; }
-  FA_DEV int key_tile(int t) const { return WIN && t >= sunk ? t + skip : t; }
-  FA_DEV bool nobody(int pos) const { return pos >= len() || (WIN && pos >= sinks && pos < lo); }
-  FA_DEV bool everybody(int pos) const {
-    return pos < hist && (!WIN || pos < sinks || pos >= edge);
-  }
-  // whether n positions from pos on are not all everybody's, and are all nobody's
+  FA_DEV int key_tile(int t) const { return t >= sunk ? t + skip : t; }
+  FA_DEV bool nobody(int pos) const { return pos >= len() || (pos >= sinks && pos < lo); }
+  FA_DEV bool everybody(int pos) const { return pos < hist && (pos < sinks || pos >= edge); }
   FA_DEV bool mixed(int pos, int n) const {
-    return pos + n > hist || (WIN && pos < edge && pos + n > sinks);
+    return pos + n > hist || (pos < edge && pos + n > sinks);
   }
   FA_DEV bool nothing(int pos, int n) const {
-    return pos >= len() || (WIN && pos >= sinks && pos + n <= lo);
+    return pos >= len() || (pos >= sinks && pos + n <= lo);
   }
 };
 template <bool WIN>
@@ -45,7 +53,7 @@ FA_DEV SeqLen<WIN> seq_len(const TreeParams& p, int b) {
   s.hist = min(max(p.hist[b], 0), cap);
   s.nd = min(p.drafts ? min(max(p.drafts[b], 0), p.T) : p.T, cap - s.hist);
   int tiles = (s.len() + kTile - 1) / kTile;
-  if (WIN) {
+  if constexpr (WIN) {
     s.sinks = p.sinks;
     s.lo = max(s.hist - p.window + 1, 0);
     s.edge = max(s.hist - p.window + max(s.nd, 1), 0);
@@ -281,7 +289,8 @@ FA_DEV uint32_t seen_bits(const TreeParams& p, const uint32_t* mask_row, const S
     w = d0 > -32 ? mask_row[0] << -d0 : 0u;
   }
   w = (w & low_bits(s.nd - d0)) | low_bits(-d0);
-  return WIN ? w & (~low_bits(begin - pos) | low_bits(s.sinks - pos)) : w;
+  if constexpr (WIN) w &= ~low_bits(begin - pos) | low_bits(s.sinks - pos);
+  return w;
 }
 
 FA_DEV uint32_t ld_shared_u8(uint32_t addr) {
