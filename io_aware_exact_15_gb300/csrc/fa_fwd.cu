@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
 
   FwdScheduleT<BC, WIN> sch;
   sch.init(pair, nT, p.causal != 0, p.lists, head, single, (N + BC - 1) / BC);
-  if (WIN) sch.reach(p.window, p.sinks, N);
+  if constexpr (WIN) sch.reach(p.window, p.sinks, N);
   // K_j or V_j into ring slot `pos`: CH column chunks of BC / KBOX boxes
   auto load_kv = [&](int pos, const CUtensorMap* m, int kt) {
 #pragma unroll

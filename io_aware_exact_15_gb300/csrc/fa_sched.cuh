@@ -25,12 +25,20 @@
 
 namespace fa {
 
+// A window's part of the forward's schedule (the other kinds do without it).
+template <bool WIN>
+struct FwdReach {};
+template <>
+struct FwdReach<true> {
+  int sink_end, win_lo[2];  // tiles with sinks, first tile of each query tile's windows
+};
+
 // BC: keys per key tile.  Query tiles are always kTile = 128 rows; the key
 // tile width differs from 128 only in the block-size sweep (dense and causal
 // batches): key tile j of width BC holds an allowed key of query tile i iff
 // j * BC <= 128 * i + 127.  Block masks (128 x 128 tiles) need BC = 128.
 template <int BC, bool WIN = false>
-struct FwdScheduleT {
+struct FwdScheduleT : FwdReach<WIN> {
   int qt[2];
   bool act[2];
   bool causal, sparse;
@@ -38,7 +46,6 @@ struct FwdScheduleT {
   const int* lb;
   int na, nb, ia, ib;
   int next_dense, end_dense;
-  int sink_end, win_lo[2];  // WIN: tiles with sinks, first tile of each query tile's windows
 
   // last key tile that query tile t reaches under the causal rule
   static FA_DEV int causal_last(int t) {
@@ -86,20 +93,21 @@ struct FwdScheduleT {
 
   // WIN, after init: N rows, key j for query i where i - j < window or j < sinks
   FA_DEV void reach(int window, int sinks, int N) {
-    sink_end = (min(sinks, N) + kTile - 1) / kTile;
+    this->sink_end = (min(sinks, N) + kTile - 1) / kTile;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) win_lo[s] = max(qt[s] * kTile - window + 1, 0) / kTile;
+    for (int s = 0; s < 2; ++s) this->win_lo[s] = max(qt[s] * kTile - window + 1, 0) / kTile;
   }
 
   FA_DEV bool next(int& kt, int& mem) {
     if constexpr (WIN) {
-      if (next_dense >= sink_end && next_dense < win_lo[0]) next_dense = win_lo[0];
+      const int sink_end = this->sink_end, lo0 = this->win_lo[0];
+      if (next_dense >= sink_end && next_dense < lo0) next_dense = lo0;
       if (next_dense >= end_dense) return false;
       kt = next_dense++;
       mem = 0;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
-        if (act[s] && kt <= qt[s] && (kt < sink_end || kt >= win_lo[s])) mem |= 1 << s;
+        if (act[s] && kt <= qt[s] && (kt < sink_end || kt >= this->win_lo[s])) mem |= 1 << s;
       return true;
     }
     if (!sparse) {
