@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(256) fa_window_finish_kernel(const WindowFinis
       const int nT = (s.n + kTile - 1) / kTile;
       // tiles that were written whole
       if (p.group_parts == 1 && kt >= 0 && kt < nT && !(kt < p.sink_tiles && kt + p.part_tiles < nT))
-        word = p.bad[t];
+        // (rows of the sequence alone: after a wait that gave up, anything may stand there)
+        word = p.bad[t] & low_bits(s.n - kt * kTile - 32 * static_cast<int>(t & 3));
     }
     for (uint32_t some = __ballot_sync(0xffffffffu, word != 0); some; some &= some - 1) {
       const int from = __ffs(some) - 1;
