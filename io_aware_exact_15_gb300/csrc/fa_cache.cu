@@ -172,7 +172,7 @@ cudaError_t launch_cache(const CacheParams& p, cudaStream_t stream) {
   // heads of 128, e4m3, one | eight rows: 64 tokens 6.8 | 8.9 us, 1024 8.9 |
   // 10.9, 4096 10.9 | 10.9, 8192 15.0 | 13.0, 32768 37.5 | 29.3).
   const bool wide = SLOTS ? 2LL * p.Hkv * p.N > 16384 * RPW : p.N > 8 * RPW;
-  const int need = (p.N + RPW - 1) / RPW;
+  const int need = (p.N - 1) / RPW + 1;  // (N may be close to 2^31)
   const int warps = wide ? 4 : need < 8 ? need : 8, per = warps * RPW * (wide ? 8 : 1);
   const long long blocks = static_cast<long long>(p.B) * 2 * p.Hkv * ((p.N - 1) / per + 1);
   if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
