@@ -41,10 +41,14 @@
 // Measured with the kernels around it: 6 sequences of up to 4096 rows, 12
 // heads of 64, window 512, 16 first keys: 193 us; 2 x 16 heads (4 of K and V)
 // of 8192 rows of 128, window 1024, 4 first keys: 533 us, 607 TFLOP/s of
-// visible pairs.  Tensor pipe 24 and 36 %, issue 32 and 22 %: a step is the
-// chain S, P, dP, dS, dQ of one 128 x 128 tile with its barriers.  At d = 64
-// P's exponentials and the dQ adds are longer than the products.  Tried and
-// no faster: 16 warps on half the columns each, keys on the lanes with P^T
+// visible pairs.  Tensor pipe 25 and 36 %, issue 35 and 25 %.  Windows of 1 to
+// 32 tiles (2 x 16 heads of 8192 rows) take 1.65 (d = 64) and 2.95 us (128) a
+// step, about what whole causal walks do: the chain S, P, dP, dS, dQ of one 128 x
+// 128 tile with its barriers, at d = 64 longer in P's exponentials and the dQ
+// adds than in the products.  Beside the steps they take 88 and 141 us: the
+// kernels around this one (76 of the 141), the start, a last round that not
+// every CTA has a unit of, and 0.6 to 2.7 us at a unit's end.  Tried and no
+// faster: 16 warps on half the columns each, keys on the lanes with P^T
 // and dS^T from tensor memory, P and dS by warps of their own, dP first.
 // TMEM: S [0,128) dP [128,256) dV [256,256+d) dK [256+d,256+2d);
 //       dQ at [384,448) for d = 64 and over the dP columns for d = 128.

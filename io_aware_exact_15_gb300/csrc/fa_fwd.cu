@@ -496,7 +496,9 @@ __global__ void __launch_bounds__(FwdSmem<D, NS_, BC, CMP>::THREADS,
           // dominant key's rounding cancels in O / l.  WIN: it sums the fp32
           // weights, which keeps lse exact to fp32 (few keys' roundings do not
           // average out) and takes one addition per pair instead of four
-          // operations.
+          // operations.  Its price: the rounding of one dominant weight, up to
+          // 2^-9 of it where the maximum that it is relative to is an older
+          // one (else it is 1, which rounds to itself), stays in O beside O's own.
           if (!WIN) {
             acc_bf16x2(ls0, ls1, sr[q][4 * c4]);
             acc_bf16x2(ls2, ls3, sr[q][4 * c4 + 1]);

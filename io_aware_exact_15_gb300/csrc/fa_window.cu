@@ -12,8 +12,9 @@
 // The backward is three kernels: D = <dO, O> and a cleared dQ accumulator;
 // the tiles; and what is here.  All but the second are bound by memory: of
 // 533 us for 2 x 16 heads (4 of K and V) of 8192 rows of 128, window 1024, 4
-// first keys, the first takes 40 and the last 35 (4.2 TB/s: fp32 accumulator
-// in, bf16 out), of 193 us for 6 packed sequences of up to 4096 rows, 12 heads
+// first keys, the first takes 40 and the last 36 (134 MB of fp32 accumulator in,
+// 67 of bf16 out, half of that not yet in DRAM when it ends: 4.9 TB/s of DRAM
+// traffic), of 193 us for 6 packed sequences of up to 4096 rows, 12 heads
 // of 64, window 512, 16 first keys, 17 and 21.
 #include <math.h>
 #include <stdint.h>
